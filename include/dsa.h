@@ -55,9 +55,12 @@ extern "C" {
 #define DSA_STATUS_BAD_BLOCK 2 /* block-table entry outside [0, num_blocks)    */
 #define DSA_STATUS_TIMEOUT 4   /* a pipeline wait gave up after ~1 s (results invalid) */
 #define DSA_STATUS_CACHE_FULL 8 /* dsa_indexer_store: a sequence's cache was full (not stored) */
+#define DSA_STATUS_BAD_SEQ 16   /* dsa_pages_*: a listed sequence was skipped (see the calls)  */
+#define DSA_STATUS_NO_PAGES 32  /* dsa_pages_reserve: too few free pages for a sequence        */
 
 #define DSA_KV_LORA_RANK 512 /* latent width the attention kernels are built for */
 #define DSA_MAX_KPOOL 16     /* most slots per pool dsa_compress handles         */
+#define DSA_MAX_PAGE_ARRAYS 128 /* most caches one dsa_page_arrays names          */
 
 typedef uint16_t dsa_bf16;
 
@@ -88,6 +91,21 @@ typedef struct dsa_paging {
     int32_t block_size;
     int64_t num_blocks;
 } dsa_paging;
+
+/*
+ * The paged caches whose pages dsa_pages_reserve and dsa_pages_compact copy: cache i is
+ * [num_blocks pages, page_bytes[i]] at device address base[i], pages back to back. A
+ * token cache of width D has block_size * D * (element size) bytes a page, a pooled-key
+ * cache block_size / kpool rows. Several layers that share one block table are listed
+ * together. Caches with a 16-byte aligned base and page size are copied 16 bytes at a
+ * time, others byte by byte (meant for small flags). The caches must not overlap.
+ */
+typedef struct dsa_page_arrays {
+    int32_t n;
+    int32_t reserved; /* 0 */
+    void* base[DSA_MAX_PAGE_ARRAYS];
+    int64_t page_bytes[DSA_MAX_PAGE_ARRAYS];
+} dsa_page_arrays;
 
 /* Message for the last error returned on this host thread ("" if none). */
 const char* dsa_last_error(void);
@@ -509,6 +527,167 @@ int dsa_sparse_mla_decode_fp8(const dsa_bf16* qlat, int rows, int heads, int kv_
                               const dsa_bf16* o_absorb, int hidden, dsa_bf16* y, float* olat,
                               int32_t* status, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * dsa_quantize_latent_fp4 -- encoder of the FP4 latent cache (288 bytes a token instead
+ * of 1,024 in bf16 or 528 in FP8). The pages have no 4-bit cache; the format is this
+ * library's stated choice: E2M1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives)
+ * under one E4M3 scale per token and 16-channel block, under one power of two for the
+ * whole cache:
+ *
+ *   value[r, c]  = 2^cache_exp * E4M3(scales[r, c / 16]) * E2M1(code[r, c])
+ *   scales[r, b] = E4M3 of amax_b * 2^-cache_exp / 6      (nearest even, at most 448)
+ *   code[r, c]   = E2M1 of x[r, c] * 2^-cache_exp / scale (nearest even, at most 6)
+ *
+ * code[r, 2i] is the low and code[r, 2i + 1] the high nibble of byte codes[r, i]. The
+ * sign of x is kept; a block whose scale rounds to 0 holds codes 0; a block with a NaN
+ * holds scale NaN (0x7F) and codes 0, so it decodes to NaN; infinities saturate. Decoding
+ * is exact in bf16. cache_exp puts the cache's magnitudes into E4M3's range: block maxima
+ * up to 2688 * 2^cache_exp do not saturate, those above 0.1 * 2^cache_exp keep a full
+ * scale; -8 suits rows of unit variance.
+ *
+ * x [rows, kv_lora_rank] bf16; codes [rows, kv_lora_rank / 2] u8; scales
+ * [rows, kv_lora_rank / 16] u8. Limits: kv_lora_rank a positive multiple of 16;
+ * -64 <= cache_exp <= 64; 16-byte aligned tensors.
+ */
+int dsa_quantize_latent_fp4(const dsa_bf16* x, long long rows, int kv_lora_rank, int cache_exp,
+                            uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * dsa_dequantize_latent_fp4 -- rows of an FP4 latent cache back as bf16 (exact): out row
+ * i is cache row row_ids[i], or row i with row_ids NULL. A row id outside
+ * [0, cache_rows) gives a row of zeros and sets DSA_STATUS_BAD_TOKEN.
+ *
+ * codes [cache_rows, kv_lora_rank / 2], scales [cache_rows, kv_lora_rank / 16] u8;
+ * row_ids [rows] i32 (device, nullable); out [rows, kv_lora_rank] bf16. Limits and
+ * cache_exp as dsa_quantize_latent_fp4; without row_ids, rows <= cache_rows.
+ */
+int dsa_dequantize_latent_fp4(const uint8_t* codes, const uint8_t* scales, long long cache_rows,
+                              const int32_t* row_ids, long long rows, int kv_lora_rank,
+                              int cache_exp, dsa_bf16* out, int32_t* status, void* stream);
+
+/*
+ * dsa_decode_append_fp4 -- dsa_decode_append for a layer with the FP4 latent cache: the
+ * staged latent row ckv_new is encoded into ckv_codes [.., kv_lora_rank / 2] and
+ * ckv_scales [.., kv_lora_rank / 16] at the token's cache row, the same bytes as
+ * dsa_quantize_latent_fp4 makes of it. ckv (the bf16 latent cache) is nullable; ckv_new
+ * is required. Limits: those of dsa_decode_append, kv_lora_rank % 128 == 0, FP4 caches
+ * 16-byte aligned, cache_exp as above.
+ */
+int dsa_decode_append_fp4(const dsa_bf16* k_new, const dsa_bf16* gate_new,
+                          const dsa_bf16* ckv_new, const float* ape, const dsa_bf16* ln_w,
+                          const dsa_bf16* ln_b, float eps, const dsa_paging* pg, int32_t* seq_lens,
+                          int first_key, int kpool, int ihd, int kv_lora_rank, dsa_bf16* k_raw,
+                          dsa_bf16* gate, uint8_t* token_valid, dsa_bf16* ckv, uint8_t* ckv_codes,
+                          uint8_t* ckv_scales, int cache_exp, dsa_bf16* kpool_out,
+                          uint8_t* pool_valid, int32_t* pool_idx, int32_t* row_ctx,
+                          int32_t* status, void* stream);
+
+/*
+ * dsa_sparse_mla_decode_fp4 -- dsa_sparse_mla_decode over an FP4 latent cache (see
+ * dsa_quantize_latent_fp4): the latent row of token t is its decoded row, everything
+ * else, the equations included, is dsa_sparse_mla_decode's. Each gathered row is 288
+ * bytes. The matrix products run in f16 (decoded rows are exact in it, q is scaled by a
+ * power of two per row, weights are rounded to 11 significant bits), sums in f32.
+ *
+ * ckv_codes: token cache of width kv_lora_rank / 2 (u8); ckv_scales: token cache of width
+ * kv_lora_rank / 16 (u8), laid out as pg says. olat [rows, heads, kv_lora_rank] f32 and
+ * olat16 (the same in bf16) are each nullable; y needs o_absorb (both or neither) and is
+ * the projection of olat16. A row without a token gives zeros. A row of the cache that
+ * is not selected is never read; a NaN in a selected row or in q stays in the results.
+ * Limits: kv_lora_rank == 512; rows <= 65535; heads <= 4096; with o_absorb hidden % 64
+ * == 0; 16-byte aligned tensors and workspace. The workspace's contents need not be
+ * kept between calls; calls that overlap in time need one each.
+ */
+int dsa_sparse_mla_decode_fp4_workspace(int rows, int heads, int kv_lora_rank, int out_width,
+                                        int hidden, int with_o_absorb, size_t* bytes);
+int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int heads, int kv_lora_rank,
+                              const int32_t* row_seq, const uint8_t* ckv_codes,
+                              const uint8_t* ckv_scales, int cache_exp, const dsa_paging* pg,
+                              const int32_t* token_ids, int out_width, float softmax_scale,
+                              const dsa_bf16* o_absorb, int hidden, dsa_bf16* y, float* olat,
+                              dsa_bf16* olat16, int32_t* status, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * Pages (no counterpart on the pages of the reference: it is given its block tables).
+ *
+ * The page operators keep, for a paged cache, the block table, the lengths and one count
+ * per page: refs [num_blocks] i32, the number of table entries that name the page. A
+ * table entry is a page or -1 (unmapped); a page whose count is 0 is free. All of it is
+ * read and written on the device, so a captured graph stays valid as sequences come, grow
+ * and go. Pages are handed out lowest id first, so results do not depend on timing.
+ *
+ * Pages may be shared after dsa_pages_fork. A shared page is never written: before
+ * tokens are appended, dsa_pages_reserve gives each sequence its own copy of the pages
+ * they will be written to.
+ *
+ * Common arguments: pg must be paged; block_table and seq_lens must be the descriptor's
+ * own (writable) tensors; refs [pg->num_blocks] i32. Lists of sequences are device i32
+ * arrays of at most pg->batch entries; an entry -1 is skipped (padding), one outside
+ * [0, batch) is skipped and sets DSA_STATUS_BAD_SEQ. Table entries outside
+ * [-1, num_blocks), and counts that a release would take below 0, set
+ * DSA_STATUS_BAD_BLOCK and are otherwise left out. Calls of one pool must be ordered (one
+ * stream); the workspace (dsa_pages_workspace bytes, 16-byte aligned, contents not kept)
+ * must not be shared by calls that overlap in time.
+ */
+int dsa_pages_workspace(long long num_pages, int batch, size_t* bytes);
+
+/*
+ * dsa_pages_free -- ends sequences: every page that a listed sequence's table row names
+ * loses a reference, the row becomes -1 and the length 0. Listing a sequence twice frees
+ * it once. The pages' data is left as it was.
+ */
+int dsa_pages_free(const int32_t* seqs, int n, const dsa_paging* pg, int32_t* block_table,
+                   int32_t* seq_lens, int32_t* refs, int32_t* status, void* stream);
+
+/*
+ * dsa_pages_fork -- child i becomes a copy of parent i: the child's former pages are
+ * released, then its row names the pages that hold the parent's seq_lens tokens (each
+ * gains a reference; -1 after them) and it takes the parent's length. Pages the parent
+ * has reserved beyond its length are not shared. No data is copied. Several children may
+ * name one parent. A pair is skipped, with DSA_STATUS_BAD_SEQ, when its parent or child
+ * is out of range, its child is listed earlier in the call, or its parent is listed as a
+ * child in the call.
+ */
+int dsa_pages_fork(const int32_t* parents, const int32_t* children, int n, const dsa_paging* pg,
+                   int32_t* block_table, int32_t* seq_lens, int32_t* refs, int32_t* status,
+                   void* stream);
+
+/*
+ * dsa_pages_reserve -- room for each listed sequence's next new_tokens tokens (seqs NULL:
+ * every sequence of the batch, n ignored). The pages those tokens will be written to are
+ * the token pages from seq_lens / block_size on and, with kpool > 0, the pages of the
+ * pooled keys that become whole (which lie before the tokens' when first_key > 0). An
+ * unmapped one gets a free page; a shared one (refs > 1) is replaced by a copy, in every
+ * cache of `arrays`, and loses a reference; others stay. Lengths do not change.
+ *
+ * Sequences are served in list order (the first entry that names a sequence counts), all
+ * of a sequence's pages or none: one for which the free pages do not suffice, after the
+ * needs of those before it, keeps its row and sets DSA_STATUS_NO_PAGES. Pages that lose
+ * their last reference in the call are free from the next call on. A sequence whose
+ * table row cannot hold the tokens is skipped with DSA_STATUS_CACHE_FULL.
+ *
+ * first_key, kpool: as in dsa_compress (block_size and first_key multiples of kpool);
+ * kpool 0 for caches without pooled keys. arrays: nullable (no data is copied). The
+ * copies read the pages as the work before this call on the stream left them.
+ */
+int dsa_pages_reserve(const int32_t* seqs, int n, const dsa_paging* pg, int32_t* block_table,
+                      int32_t* refs, int new_tokens, int first_key, int kpool,
+                      const dsa_page_arrays* arrays, int32_t* status, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * dsa_pages_compact -- moves the pool's live pages to its front: with n live pages
+ * (refs > 0), the k-th live page at or above n moves into the k-th free page below n, in
+ * every cache of `arrays` (nullable), with its count, and the block table is rewritten.
+ * Afterwards the pages below n are live and the rest free. remap [num_blocks] i32
+ * (nullable): the new id of each live page, -1 for pages that were free. live [1] i32
+ * (nullable): n.
+ */
+int dsa_pages_compact(const dsa_paging* pg, int32_t* block_table, int32_t* refs,
+                      const dsa_page_arrays* arrays, int32_t* remap, int32_t* live,
+                      int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * dsa_frontend -- the decode step's inputs from the hidden state x. build.rs lists

@@ -459,6 +459,195 @@ def dequantize_latent_fp8(codes, scales) -> np.ndarray:
 
 
 # ---------------------------------------------------------------------------
+# FP4 latent cache (no counterpart on the pages; the library's stated format): E2M1
+# codes under one E4M3 scale per token and 16-channel block, under one power of two
+# 2^cache_exp for the whole cache.
+
+E2M1_VALUES = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0)
+FP4_BLOCK = 16
+FP4_NAN_SCALE = 0x7F
+
+
+def e2m1_encode(v) -> np.ndarray:
+    """4-bit codes of float64 values: the nearest of E2M1_VALUES (ties to the even
+    code), saturating at 6; bit 3 is the sign."""
+    v = np.asarray(v, dtype=F64)
+    a = np.minimum(np.abs(v), 6.0)
+    table = np.array(E2M1_VALUES)
+    hi = np.searchsorted(table, a)  # table[hi - 1] < a <= table[hi]
+    lo = np.maximum(hi - 1, 0)
+    down, up = a - table[lo], table[hi] - a
+    code = np.where((down < up) | ((down == up) & (lo % 2 == 0)), lo, hi)
+    return (code + np.where(np.signbit(v), 8, 0)).astype(np.uint8)
+
+
+def e2m1_decode(codes) -> np.ndarray:
+    c = np.asarray(codes, dtype=np.int64)
+    return np.where(c & 8, -1.0, 1.0) * np.array(E2M1_VALUES)[c & 7]
+
+
+def quantize_latent_fp4(rows, cache_exp: int = 0):
+    """Latent rows ``[T, kvl]`` -> ``(codes uint8 [T, kvl/2], scales uint8 [T, kvl/16])``."""
+    x = np.asarray(rows, dtype=F64)
+    T, kvl = x.shape
+    g = np.ldexp(x.reshape(T, kvl // FP4_BLOCK, FP4_BLOCK), -cache_exp)
+    nan = np.isnan(g).any(axis=2)
+    g = np.where(nan[:, :, None], 0.0, g)
+    s = e4m3_round(np.minimum(np.abs(g).max(axis=2) / 6.0, E4M3_MAX))
+    with np.errstate(divide="ignore", invalid="ignore"):
+        q = np.where(s[:, :, None] > 0, g / s[:, :, None], 0.0)
+    c = np.where(s[:, :, None] > 0, e2m1_encode(q), 0).reshape(T, kvl)
+    scales = np.where(nan, FP4_NAN_SCALE, e4m3_encode(s))
+    return (c[:, 0::2] | (c[:, 1::2] << 4)).astype(np.uint8), scales.astype(np.uint8)
+
+
+def dequantize_latent_fp4(codes, scales, cache_exp: int = 0) -> np.ndarray:
+    """Values of an FP4 cache's rows (float64)."""
+    c = np.asarray(codes)
+    v = np.stack((e2m1_decode(c & 15), e2m1_decode(c >> 4)), -1)
+    T = c.shape[0]
+    v = v.reshape(T, -1, FP4_BLOCK) * e4m3_decode(scales)[:, :, None]
+    return np.ldexp(v.reshape(T, -1), cache_exp)
+
+
+# ---------------------------------------------------------------------------
+# Pages (no counterpart on the pages of the reference): a block table, the lengths and
+# one count per page, changed in place by plain loops.
+
+
+class PagePool:
+    """``table [B, max_blocks]``, ``lens [B]``, ``refs [num_pages]`` (numpy, int64) and
+    the paged caches, a list of arrays ``[num_pages, ...]``. ``bad`` collects what the
+    library flags: "seq", "block", "full", "pages"."""
+
+    def __init__(self, table, lens, num_pages: int, block_size: int, caches=(), refs=None):
+        self.table = np.array(table, dtype=np.int64)
+        self.lens = np.array(lens, dtype=np.int64)
+        self.bs = block_size
+        self.n = num_pages
+        self.caches = [np.array(c) for c in caches]
+        self.bad = set()
+        if refs is None:
+            refs = np.zeros(num_pages, dtype=np.int64)
+            for p in self.table[self.table >= 0]:
+                refs[p] += 1
+        self.refs = np.array(refs, dtype=np.int64)
+
+    def _release(self, p):
+        if p == -1:
+            return
+        if not 0 <= p < self.n or self.refs[p] <= 0:
+            self.bad.add("block")
+            return
+        self.refs[p] -= 1
+
+    def _listed(self, seqs):
+        seen = set()
+        for b in seqs:
+            if b == -1:
+                continue
+            if not 0 <= b < len(self.lens):
+                self.bad.add("seq")
+            elif b not in seen:
+                seen.add(b)
+                yield int(b)
+
+    def free(self, seqs):
+        for b in self._listed(seqs):
+            for p in self.table[b]:
+                self._release(p)
+            self.table[b] = -1
+            self.lens[b] = 0
+
+    def fork(self, parents, children):
+        B = len(self.lens)
+        kids = set(int(c) for c in children if c != -1)
+        done = set()
+        for p, c in zip(parents, children):
+            if c == -1:
+                continue
+            if not (0 <= p < B and 0 <= c < B) or c in done or p in kids:
+                self.bad.add("seq")
+                done.add(int(c))
+                continue
+            done.add(int(c))
+            row = np.full(self.table.shape[1], -1)
+            for j in range(min(-(-int(self.lens[p]) // self.bs), len(row))):
+                page = self.table[p, j]
+                if 0 <= page < self.n:
+                    row[j] = page
+                    self.refs[page] += 1
+                else:
+                    self.bad.add("block")
+            for page in self.table[c]:
+                self._release(page)
+            self.table[c] = row
+            self.lens[c] = self.lens[p]
+
+    def written_pages(self, b: int, new: int, first_key: int, kpool: int):
+        """Indices into b's row of the pages its next ``new`` tokens are written to: each
+        token's page, and the page of the pooled key of each pool that becomes whole."""
+        L = int(self.lens[b])
+        pages = {t // self.bs for t in range(L, L + new)}
+        if kpool:
+            pages |= {p // (self.bs // kpool)
+                      for p in pools_completed(L, L + new, first_key, kpool)}
+        return sorted(pages)
+
+    def reserve(self, new: int, first_key: int = 0, kpool: int = 0, seqs=None):
+        start = self.refs.copy()
+        free = [p for p in range(self.n) if start[p] == 0]
+        given = 0
+        for b in self._listed(range(len(self.lens)) if seqs is None else seqs):
+            L = int(self.lens[b])
+            if L < 0 or L + new > self.table.shape[1] * self.bs:
+                self.bad.add("full")
+                continue
+            needs = []
+            for j in self.written_pages(b, new, first_key, kpool):
+                p = int(self.table[b, j])
+                if 0 <= p < self.n:
+                    if start[p] > 1:
+                        needs.append((j, p))
+                elif p == -1 and j * self.bs >= L:
+                    needs.append((j, None))
+                else:
+                    self.bad.add("block")
+            at, given = given, given + len(needs)
+            if given > len(free):
+                if needs:
+                    self.bad.add("pages")
+                continue
+            for k, (j, old) in enumerate(needs):
+                page = free[at + k]
+                self.table[b, j] = page
+                self.refs[page] = 1
+                if old is not None:
+                    self.refs[old] -= 1
+                    for c in self.caches:
+                        c[page] = c[old]
+
+    def compact(self):
+        """Returns (live pages, remap)."""
+        live = [p for p in range(self.n) if self.refs[p] > 0]
+        n = len(live)
+        holes = [p for p in range(n) if self.refs[p] <= 0]
+        remap = np.full(self.n, -1)
+        remap[live] = live
+        for src, dst in zip([p for p in live if p >= n], holes):
+            remap[src] = dst
+            self.refs[dst], self.refs[src] = self.refs[src], 0
+            for c in self.caches:
+                c[dst] = c[src]
+        for i, p in np.ndenumerate(self.table):
+            if 0 <= p < self.n and remap[p] >= 0:
+                self.table[i] = remap[p]
+            elif p != -1 and not (0 <= p < n):
+                self.bad.add("block")
+        return n, remap
+
+
+# ---------------------------------------------------------------------------
 # Decode-time append and the geometry derived from the live length (mod.rs,
 # ``Glm5NextDsaKernels`` fields ``indexer_store`` and ``write_geom``;
 # ``Glm5NextDsaConfig::max_context``)

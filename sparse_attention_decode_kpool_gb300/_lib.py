@@ -21,6 +21,9 @@ DSA_STATUS_BAD_TOKEN = 1
 DSA_STATUS_BAD_BLOCK = 2
 DSA_STATUS_TIMEOUT = 4
 DSA_STATUS_CACHE_FULL = 8
+DSA_STATUS_BAD_SEQ = 16
+DSA_STATUS_NO_PAGES = 32
+DSA_MAX_PAGE_ARRAYS = 128
 DSA_ABI_VERSION = 8
 DSA_OPT_PDL = 0
 DSA_OPT_MLA_KERNEL = 1
@@ -50,11 +53,22 @@ class DsaPaging(ctypes.Structure):
     ]
 
 
+class DsaPageArrays(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("base", ctypes.c_void_p * DSA_MAX_PAGE_ARRAYS),
+        ("page_bytes", ctypes.c_int64 * DSA_MAX_PAGE_ARRAYS),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_LL = ctypes.c_longlong
 _PG = ctypes.POINTER(DsaPaging)
+_PA = ctypes.POINTER(DsaPageArrays)
 
 # name -> (restype, argtypes), in header order
 SIGNATURES = {
@@ -88,6 +102,18 @@ SIGNATURES = {
     "dsa_quantize_latent": (_I, [_P, ctypes.c_longlong, _I, _P, _P, _P]),
     "dsa_sparse_mla_decode_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P, _PG, _P, _I, _F, _P, _I, _P,
                                        _P, _P, _P, _SZ, _P]),
+    "dsa_quantize_latent_fp4": (_I, [_P, _LL, _I, _I, _P, _P, _P]),
+    "dsa_dequantize_latent_fp4": (_I, [_P, _P, _LL, _P, _LL, _I, _I, _P, _P, _P]),
+    "dsa_decode_append_fp4": (_I, [_P, _P, _P, _P, _P, _P, _F, _PG, _P, _I, _I, _I, _I, _P, _P,
+                                   _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
+    "dsa_sparse_mla_decode_fp4_workspace": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "dsa_sparse_mla_decode_fp4": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _PG, _P, _I, _F, _P, _I,
+                                       _P, _P, _P, _P, _P, _SZ, _P]),
+    "dsa_pages_workspace": (_I, [_LL, _I, ctypes.POINTER(_SZ)]),
+    "dsa_pages_free": (_I, [_P, _I, _PG, _P, _P, _P, _P, _P]),
+    "dsa_pages_fork": (_I, [_P, _P, _I, _PG, _P, _P, _P, _P, _P]),
+    "dsa_pages_reserve": (_I, [_P, _I, _PG, _P, _P, _I, _I, _I, _PA, _P, _P, _SZ, _P]),
+    "dsa_pages_compact": (_I, [_PG, _P, _P, _PA, _P, _P, _P, _P, _SZ, _P]),
     "dsa_frontend_workspace": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "dsa_frontend": (_I, [_P, _I, _I, _P, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P,
                           _P, _P, _P, _P, _P, _SZ, _P]),

@@ -11,13 +11,17 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import DsaPaging, check
+from ._lib import DsaPageArrays, DsaPaging, check
 
 __all__ = ["paging", "dsa_compress", "dsa_compress_append", "dsa_indexer_store",
            "dsa_write_geom", "dsa_decode_append", "dsa_decode_append_fp8", "dsa_score", "dsa_score_prefill", "dsa_select", "dsa_expand",
            "dsa_select_expand", "dsa_expand_tail", "dsa_select_expand_tail",
            "dsa_sparse_mla_decode_workspace", "dsa_sparse_mla_decode",
            "dsa_sparse_mla_decode_noalloc", "dsa_sparse_mla_decode_fp8", "dsa_quantize_latent",
+           "dsa_quantize_latent_fp4", "dsa_dequantize_latent_fp4", "dsa_decode_append_fp4",
+           "dsa_sparse_mla_decode_fp4_workspace", "dsa_sparse_mla_decode_fp4",
+           "page_arrays", "dsa_pages_workspace", "dsa_pages_free", "dsa_pages_fork",
+           "dsa_pages_reserve", "dsa_pages_compact", "DsaPageArrays",
            "dsa_frontend_workspace", "dsa_frontend", "dsa_latent_project_workspace",
            "dsa_latent_project", "dsa_select_k",
            "dsa_validate_config", "dsa_prefetch_l2", "dsa_set_option", "dsa_get_option", "mla_kernel",
@@ -431,6 +435,246 @@ def dsa_quantize_latent(x, codes, scales, stream=None) -> None:
     check(_lib.load().dsa_quantize_latent(
         _ptr(x, torch.bfloat16, "x"), rows, kvl, _ptr(codes, torch.uint8, "codes"),
         _ptr(scales, torch.float32, "scales"), _stream(stream)))
+
+
+# -- FP4 latent cache ------------------------------------------------------
+
+_FP4_BLOCK = 16  # channels under one scale
+
+
+def _fp4_cache(codes, scales) -> int:
+    """Channels of an FP4 latent cache (codes [.., kvl/2], scales [.., kvl/16])."""
+    kvl = 2 * int(codes.shape[-1])
+    if int(scales.shape[-1]) * _FP4_BLOCK != kvl or scales.numel() * 8 != codes.numel():
+        raise ValueError("codes must be [.., kvl/2] and scales [.., kvl/16] of the same rows")
+    return kvl
+
+
+def _call(t: torch.Tensor, stream, fn, *args, others=()) -> None:
+    """One library call for tensors on t's device: made with that device current, on its
+    current stream by default. ``others`` must live on the same device."""
+    dev = t.device
+    for o in others:
+        if o is not None and o.device != dev and o.is_cuda:
+            raise ValueError(f"tensors on {dev} and {o.device}: one device per call")
+    if torch.cuda.current_device() == dev.index:
+        check(fn(*args, _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        check(fn(*args, _stream(stream)))
+
+
+def dsa_quantize_latent_fp4(x, codes, scales, cache_exp: int = 0, stream=None) -> None:
+    """FP4 latent cache from bf16 rows: codes [..., kvl/2] u8 (two E2M1 codes a byte),
+    scales [..., kvl/16] u8 (E4M3), under 2^cache_exp (see include/dsa.h)."""
+    kvl = int(x.shape[-1])
+    if _fp4_cache(codes, scales) != kvl or codes.numel() * 2 != x.numel():
+        raise ValueError("codes [.., kvl/2] and scales [.., kvl/16] must match x [.., kvl]")
+    if x.numel() == 0:
+        return
+    _call(x, stream, _lib.load().dsa_quantize_latent_fp4,
+          _ptr(x, torch.bfloat16, "x"), x.numel() // kvl, kvl, int(cache_exp),
+          _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
+          others=(codes, scales))
+
+
+def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None, status=None,
+                              stream=None) -> None:
+    """Rows of an FP4 latent cache back as bf16, exactly: all of them in order, or the
+    cache rows named by ``rows`` (i32, one per row of out)."""
+    kvl = _fp4_cache(codes, scales)
+    if int(out.shape[-1]) != kvl:
+        raise ValueError(f"out must be [.., {kvl}]")
+    n, cache_rows = out.numel() // kvl, codes.numel() * 2 // kvl
+    if rows is not None and rows.numel() != n:
+        raise ValueError(f"rows must hold {n} row numbers")
+    if rows is None and n != cache_rows:
+        raise ValueError(f"out must hold the cache's {cache_rows} rows")
+    if n == 0:
+        return
+    _call(codes, stream, _lib.load().dsa_dequantize_latent_fp4,
+          _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"), cache_rows,
+          _ptr(rows, torch.int32, "rows"), n, kvl, int(cache_exp),
+          _ptr(out, torch.bfloat16, "out"), _ptr(status, torch.int32, "status"),
+          others=(scales, rows, out, status))
+
+
+def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float, pg: DsaPaging,
+                          seq_lens, first_key: int, kpool: int, k_raw, gate, token_valid,
+                          ckv_codes, ckv_scales, cache_exp: int, kpool_out, pool_valid, ckv=None,
+                          pool_idx=None, row_ctx=None, status=None, stream=None) -> None:
+    """dsa_decode_append that also encodes the staged latent row into the FP4 cache
+    (same codec and bytes as dsa_quantize_latent_fp4); the bf16 cache ``ckv`` is
+    optional."""
+    batch, ihd = (int(x) for x in k_new.shape)
+    if tuple(gate_new.shape) != (batch, ihd):
+        raise ValueError(f"gate_new must be [{batch}, {ihd}]")
+    kvl = int(ckv_new.shape[-1])
+    if tuple(ckv_new.shape) != (batch, kvl) or _fp4_cache(ckv_codes, ckv_scales) != kvl:
+        raise ValueError(f"ckv_new must be [{batch}, kvl], ckv_codes [.., kvl/2] and "
+                         "ckv_scales [.., kvl/16]")
+    if batch != pg.batch:
+        raise ValueError(f"one staged row per sequence: {batch} rows, {pg.batch} sequences")
+    _call(k_new, stream, _lib.load().dsa_decode_append_fp4,
+          _ptr(k_new, torch.bfloat16, "k_new"), _ptr(gate_new, torch.bfloat16, "gate_new"),
+          _ptr(ckv_new, torch.bfloat16, "ckv_new"), _ptr(ape, torch.float32, "ape"),
+          _ptr(ln_w, torch.bfloat16, "ln_w"), _ptr(ln_b, torch.bfloat16, "ln_b"), float(eps),
+          ctypes.byref(pg), _ptr(seq_lens, torch.int32, "seq_lens"), int(first_key), int(kpool),
+          ihd, kvl, _ptr(k_raw, torch.bfloat16, "k_raw"), _ptr(gate, torch.bfloat16, "gate"),
+          _ptr(token_valid, torch.uint8, "token_valid"), _ptr(ckv, torch.bfloat16, "ckv"),
+          _ptr(ckv_codes, torch.uint8, "ckv_codes"), _ptr(ckv_scales, torch.uint8, "ckv_scales"),
+          int(cache_exp), _ptr(kpool_out, torch.bfloat16, "kpool_out"),
+          _ptr(pool_valid, torch.uint8, "pool_valid"), _ptr(pool_idx, torch.int32, "pool_idx"),
+          _ptr(row_ctx, torch.int32, "row_ctx"), _ptr(status, torch.int32, "status"),
+          others=(gate_new, ckv_new, seq_lens, k_raw, ckv_codes, ckv_scales, kpool_out))
+
+
+def dsa_sparse_mla_decode_fp4_workspace(rows: int, heads: int, out_width: int, hidden: int,
+                                        with_o_absorb: bool, kv_lora_rank: int = 512) -> int:
+    n = ctypes.c_size_t(0)
+    check(_lib.load().dsa_sparse_mla_decode_fp4_workspace(
+        int(rows), int(heads), int(kv_lora_rank), int(out_width), int(hidden),
+        1 if with_o_absorb else 0, ctypes.byref(n)))
+    return int(n.value)
+
+
+def dsa_sparse_mla_decode_fp4(qlat, row_seq, ckv_codes, ckv_scales, cache_exp: int,
+                              pg: DsaPaging, token_ids, softmax_scale: float, o_absorb=None,
+                              y=None, olat=None, status=None, workspace=None,
+                              stream=None) -> None:
+    """dsa_sparse_mla_decode over an FP4 latent cache (see dsa_quantize_latent_fp4).
+    ``olat`` [rows, heads, 512] may be float32 or bfloat16."""
+    rows, heads, kvl = (int(x) for x in qlat.shape)
+    if token_ids.dim() != 2 or int(token_ids.shape[0]) != rows:
+        raise ValueError(f"token_ids must be [{rows}, out_width]")
+    ow = int(token_ids.shape[1])
+    if _fp4_cache(ckv_codes, ckv_scales) != kvl:
+        raise ValueError(f"ckv_codes must be [.., {kvl // 2}] and ckv_scales [.., {kvl // 16}]")
+    need = (pg.num_blocks * pg.block_size if pg.block_table else pg.batch * pg.max_seq_len)
+    if ckv_codes.numel() * 2 < need * kvl:
+        raise ValueError(f"the cache holds {ckv_codes.numel() * 2 // kvl} rows, the paging "
+                         f"descriptor names {need}")
+    if row_seq is not None and row_seq.numel() != rows:
+        raise ValueError(f"row_seq must be [{rows}]")
+    hidden = int(o_absorb.shape[0]) if o_absorb is not None else 0
+    if o_absorb is not None and tuple(o_absorb.shape) != (hidden, heads * kvl):
+        raise ValueError(f"o_absorb must be [hidden, {heads * kvl}]")
+    if y is not None and tuple(y.shape) != (rows, hidden):
+        raise ValueError(f"y must be [{rows}, {hidden}]")
+    if olat is not None and tuple(olat.shape) != (rows, heads, kvl):
+        raise ValueError(f"olat must be [{rows}, {heads}, {kvl}]")
+    if olat is not None and olat.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"olat must be float32 or bfloat16, got {olat.dtype}")
+    p_olat = _ptr(olat, None, "olat")
+    half = olat is not None and olat.dtype == torch.bfloat16
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(ckv_codes, stream, _lib.load().dsa_sparse_mla_decode_fp4,
+          _ptr(qlat, torch.bfloat16, "qlat"), rows, heads, kvl,
+          _ptr(row_seq, torch.int32, "row_seq"), _ptr(ckv_codes, torch.uint8, "ckv_codes"),
+          _ptr(ckv_scales, torch.uint8, "ckv_scales"), int(cache_exp), ctypes.byref(pg),
+          _ptr(token_ids, torch.int32, "token_ids"), ow, float(softmax_scale),
+          _ptr(o_absorb, torch.bfloat16, "o_absorb"), hidden,
+          _ptr(y, torch.bfloat16, "y", host_ok=True), None if half else p_olat,
+          p_olat if half else None, _ptr(status, torch.int32, "status"),
+          _ptr(workspace, None, "workspace"), ws_bytes,
+          others=(qlat, row_seq, ckv_scales, token_ids, o_absorb, y, olat, status, workspace))
+
+
+# -- pages -----------------------------------------------------------------
+
+
+def page_arrays(caches, num_blocks: int) -> DsaPageArrays:
+    """The paged caches that dsa_pages_reserve and dsa_pages_compact copy pages of: each a
+    contiguous CUDA tensor [num_blocks, ...] of any type (see ``dsa_page_arrays`` in
+    include/dsa.h). They must outlive every call that uses the returned descriptor."""
+    caches = list(caches)
+    if len(caches) > _lib.DSA_MAX_PAGE_ARRAYS:
+        raise ValueError(f"{len(caches)} caches: at most {_lib.DSA_MAX_PAGE_ARRAYS}")
+    pa = DsaPageArrays()
+    pa.n = len(caches)
+    for i, c in enumerate(caches):
+        if c.dim() < 1 or int(c.shape[0]) != int(num_blocks):
+            raise ValueError(f"cache {i} must be [{num_blocks}, ...], got {tuple(c.shape)}")
+        pa.base[i] = _ptr(c, None, f"cache {i}")
+        pa.page_bytes[i] = c.numel() // int(num_blocks) * c.element_size()
+    return pa
+
+
+def dsa_pages_workspace(num_blocks: int, batch: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(_lib.load().dsa_pages_workspace(int(num_blocks), int(batch), ctypes.byref(n)))
+    return int(n.value)
+
+
+def _pool(pg: DsaPaging, block_table, refs) -> None:
+    if tuple(block_table.shape) != (pg.batch, pg.max_blocks):
+        raise ValueError(f"block_table must be [{pg.batch}, {pg.max_blocks}]")
+    if refs.numel() != pg.num_blocks:
+        raise ValueError(f"refs must be [{pg.num_blocks}]")
+
+
+def dsa_pages_free(seqs, pg: DsaPaging, block_table, seq_lens, refs, status=None,
+                   stream=None) -> None:
+    """End the listed sequences: their pages lose a reference, their rows become -1 and
+    their lengths 0 (-1 entries of ``seqs`` are skipped)."""
+    _pool(pg, block_table, refs)
+    _call(refs, stream, _lib.load().dsa_pages_free,
+          _ptr(seqs, torch.int32, "seqs"), int(seqs.numel()), ctypes.byref(pg),
+          _ptr(block_table, torch.int32, "block_table"),
+          _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(refs, torch.int32, "refs"),
+          _ptr(status, torch.int32, "status"), others=(seqs, block_table, seq_lens, status))
+
+
+def dsa_pages_fork(parents, children, pg: DsaPaging, block_table, seq_lens, refs, status=None,
+                   stream=None) -> None:
+    """children[i] becomes a copy of parents[i] that shares its pages (-1 entries of
+    ``children`` are skipped)."""
+    _pool(pg, block_table, refs)
+    if parents.numel() != children.numel():
+        raise ValueError("parents and children must have the same length")
+    _call(refs, stream, _lib.load().dsa_pages_fork,
+          _ptr(parents, torch.int32, "parents"), _ptr(children, torch.int32, "children"),
+          int(children.numel()), ctypes.byref(pg),
+          _ptr(block_table, torch.int32, "block_table"),
+          _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(refs, torch.int32, "refs"),
+          _ptr(status, torch.int32, "status"),
+          others=(parents, children, block_table, seq_lens, status))
+
+
+def dsa_pages_reserve(pg: DsaPaging, block_table, refs, new_tokens: int,
+                      arrays: Optional[DsaPageArrays], first_key: int = 0, kpool: int = 0,
+                      seqs=None, status=None, workspace=None, stream=None) -> None:
+    """Room for the next ``new_tokens`` tokens of each listed sequence (all of them by
+    default): free pages where none is mapped, private copies of shared ones."""
+    _pool(pg, block_table, refs)
+    if seqs is not None and seqs.numel() == 0:
+        return  # an empty list has no address: to the C call it would mean every sequence
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(refs, stream, _lib.load().dsa_pages_reserve,
+          _ptr(seqs, torch.int32, "seqs"), 0 if seqs is None else int(seqs.numel()),
+          ctypes.byref(pg), _ptr(block_table, torch.int32, "block_table"),
+          _ptr(refs, torch.int32, "refs"), int(new_tokens), int(first_key), int(kpool),
+          None if arrays is None else ctypes.byref(arrays), _ptr(status, torch.int32, "status"),
+          _ptr(workspace, None, "workspace"), ws_bytes,
+          others=(seqs, block_table, status, workspace))
+
+
+def dsa_pages_compact(pg: DsaPaging, block_table, refs, arrays: Optional[DsaPageArrays],
+                      remap=None, live=None, status=None, workspace=None, stream=None) -> None:
+    """Move the pool's live pages to its front and rewrite the block table."""
+    _pool(pg, block_table, refs)
+    if remap is not None and remap.numel() != pg.num_blocks:
+        raise ValueError(f"remap must be [{pg.num_blocks}]")
+    if live is not None and live.numel() != 1:
+        raise ValueError("live must hold one number")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(refs, stream, _lib.load().dsa_pages_compact,
+          ctypes.byref(pg), _ptr(block_table, torch.int32, "block_table"),
+          _ptr(refs, torch.int32, "refs"),
+          None if arrays is None else ctypes.byref(arrays), _ptr(remap, torch.int32, "remap"),
+          _ptr(live, torch.int32, "live"), _ptr(status, torch.int32, "status"),
+          _ptr(workspace, None, "workspace"), ws_bytes,
+          others=(block_table, remap, live, status, workspace))
 
 
 def dsa_frontend_workspace(rows: int, hidden: int, n_x: int, q_lora_rank: int, kv_lora_rank: int,

@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "fp4.cuh"
 #include "fp8.cuh"
 #include "store.cuh"
 
@@ -260,6 +261,9 @@ struct AppendArgs {
     uint16_t* ckv;
     uint8_t* ckv8;      // nullable: the FP8 latent cache's codes ...
     float* ckv_scale;   // ... and scales, written from ckv_new
+    uint8_t* ckv4;       // nullable: the FP4 latent cache's codes ...
+    uint8_t* ckv4_scale; // ... and scales, under 2^cache_exp
+    int cache_exp;
     int32_t* seq_lens;
     int32_t* row_ctx;
     int32_t* status;
@@ -300,6 +304,19 @@ __global__ void __launch_bounds__(kAppendThreads) decode_append_kernel(AppendArg
                 fp8_encode_group(a.ckv_new + (long long)b * a.kvl + gi * 128,
                                  a.ckv8 + row * a.kvl + gi * 128, a.ckv_scale + row * G + gi,
                                  threadIdx.x & 31);
+        }
+        if (a.ckv4) {
+            // the FP4 cache: one 16-channel block a thread, the codec of
+            // dsa_quantize_latent_fp4
+            const int blocks = a.kvl / kF4Block;
+            for (int i = threadIdx.x; i < blocks; i += kAppendThreads) {
+                const uint16_t* src = a.ckv_new + (long long)b * a.kvl + i * kF4Block;
+                const uint4 v[2] = {ldg16(src), ldg16(src + 8)};
+                uint8_t sc;
+                *reinterpret_cast<uint2*>(a.ckv4 + row * (a.kvl / 2) + i * 8) =
+                    fp4_encode16(v, a.cache_exp, &sc);
+                a.ckv4_scale[row * blocks + i] = sc;
+            }
         }
     }
     __syncthreads();  // the stored rows are visible to the whole block from here on
@@ -450,14 +467,16 @@ extern "C" int dsa_compress_append(const dsa_bf16* k_raw, const dsa_bf16* gate,
 }
 
 namespace {
-// dsa_decode_append and dsa_decode_append_fp8 (ckv8 / ckv_scale set).
+// dsa_decode_append, dsa_decode_append_fp8 (ckv8 / ckv_scale set) and
+// dsa_decode_append_fp4 (ckv4 / ckv4_scale set).
 int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* gate_new,
                        const dsa_bf16* ckv_new, const float* ape, const dsa_bf16* ln_w,
                        const dsa_bf16* ln_b, float eps, const dsa_paging* pg, int32_t* seq_lens,
                        int first_key, int kpool, int ihd, int kv_lora_rank, dsa_bf16* k_raw,
                        dsa_bf16* gate, uint8_t* token_valid, dsa_bf16* ckv, uint8_t* ckv8,
-                       float* ckv_scale, dsa_bf16* kpool_out, uint8_t* pool_valid,
-                       int32_t* pool_idx, int32_t* row_ctx, int32_t* status, void* stream) {
+                       float* ckv_scale, uint8_t* ckv4, uint8_t* ckv4_scale, int cache_exp,
+                       dsa_bf16* kpool_out, uint8_t* pool_valid, int32_t* pool_idx,
+                       int32_t* row_ctx, int32_t* status, void* stream) {
     if (kpool < 1 || kpool > DSA_MAX_KPOOL)
         return fail(DSA_ERR_UNSUPPORTED, "%s: kpool %d outside [1, %d]", name, kpool,
                     DSA_MAX_KPOOL);
@@ -465,10 +484,10 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
         return fail(DSA_ERR_UNSUPPORTED, "%s: index_head_dim %d not in {64, 128}", name, ihd);
     if (first_key < 0) return fail(DSA_ERR_INVALID_ARG, "%s: first_key %d < 0", name, first_key);
     if (!(eps >= 0.f)) return fail(DSA_ERR_INVALID_ARG, "%s: eps must be >= 0", name);
-    const bool fp8 = ckv8 != nullptr;
+    const bool fp8 = ckv8 != nullptr, fp4 = ckv4 != nullptr;
     if (fp8 != (ckv_scale != nullptr))
         return fail(DSA_ERR_INVALID_ARG, "%s: ckv_codes and ckv_scales go together", name);
-    if (fp8 ? !ckv_new : (ckv == nullptr) != (ckv_new == nullptr))
+    if (fp8 || fp4 ? !ckv_new : (ckv == nullptr) != (ckv_new == nullptr))
         return fail(DSA_ERR_INVALID_ARG, "%s: ckv_new and the latent cache go together", name);
     if (ckv_new && (kv_lora_rank < 8 || kv_lora_rank % 8 != 0))
         return fail(DSA_ERR_INVALID_ARG, "%s: kv_lora_rank %d not a multiple of 8", name,
@@ -476,6 +495,12 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
     if (fp8 && kv_lora_rank % 128 != 0)
         return fail(DSA_ERR_INVALID_ARG, "%s: kv_lora_rank %d not a multiple of 128", name,
                     kv_lora_rank);
+    if (fp4 && kv_lora_rank % 128 != 0)
+        return fail(DSA_ERR_INVALID_ARG, "%s: kv_lora_rank %d not a multiple of 128", name,
+                    kv_lora_rank);
+    if (fp4 && (cache_exp < -kF4MaxExp || cache_exp > kF4MaxExp))
+        return fail(DSA_ERR_INVALID_ARG, "%s: cache_exp %d outside [-%d, %d]", name, cache_exp,
+                    kF4MaxExp, kF4MaxExp);
     Paging P;
     int rc = check_paging(pg, kpool, &P);
     if (rc) return rc;
@@ -491,7 +516,8 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
         return fail(DSA_ERR_INVALID_ARG, "%s: NULL tensor", name);
     if ((((uintptr_t)k_new) | ((uintptr_t)gate_new) | ((uintptr_t)ckv_new) | ((uintptr_t)k_raw) |
          ((uintptr_t)gate) | ((uintptr_t)ckv) | ((uintptr_t)kpool_out) | ((uintptr_t)ape) |
-         ((uintptr_t)ln_w) | ((uintptr_t)ln_b) | ((uintptr_t)ckv8) | ((uintptr_t)ckv_scale)) & 15)
+         ((uintptr_t)ln_w) | ((uintptr_t)ln_b) | ((uintptr_t)ckv8) | ((uintptr_t)ckv_scale) |
+         ((uintptr_t)ckv4) | ((uintptr_t)ckv4_scale)) & 15)
         return fail(DSA_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", name);
     AppendArgs a;
     a.k_new = k_new;
@@ -503,6 +529,9 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
     a.ckv = ckv;
     a.ckv8 = ckv8;
     a.ckv_scale = ckv_scale;
+    a.ckv4 = ckv4;
+    a.ckv4_scale = ckv4_scale;
+    a.cache_exp = cache_exp;
     a.seq_lens = seq_lens;
     a.row_ctx = row_ctx;
     a.status = status;
@@ -542,8 +571,8 @@ extern "C" int dsa_decode_append(const dsa_bf16* k_new, const dsa_bf16* gate_new
                                  int32_t* status, void* stream) {
     return decode_append_impl("dsa_decode_append", k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps,
                               pg, seq_lens, first_key, kpool, ihd, kv_lora_rank, k_raw, gate,
-                              token_valid, ckv, nullptr, nullptr, kpool_out, pool_valid, pool_idx,
-                              row_ctx, status, stream);
+                              token_valid, ckv, nullptr, nullptr, nullptr, nullptr, 0, kpool_out,
+                              pool_valid, pool_idx, row_ctx, status, stream);
 }
 
 extern "C" int dsa_decode_append_fp8(const dsa_bf16* k_new, const dsa_bf16* gate_new,
@@ -559,6 +588,23 @@ extern "C" int dsa_decode_append_fp8(const dsa_bf16* k_new, const dsa_bf16* gate
         return fail(DSA_ERR_INVALID_ARG, "dsa_decode_append_fp8: NULL FP8 cache");
     return decode_append_impl("dsa_decode_append_fp8", k_new, gate_new, ckv_new, ape, ln_w, ln_b,
                               eps, pg, seq_lens, first_key, kpool, ihd, kv_lora_rank, k_raw, gate,
-                              token_valid, ckv, ckv_codes, ckv_scales, kpool_out, pool_valid,
-                              pool_idx, row_ctx, status, stream);
+                              token_valid, ckv, ckv_codes, ckv_scales, nullptr, nullptr, 0, kpool_out,
+                              pool_valid, pool_idx, row_ctx, status, stream);
+}
+
+extern "C" int dsa_decode_append_fp4(const dsa_bf16* k_new, const dsa_bf16* gate_new,
+                                     const dsa_bf16* ckv_new, const float* ape,
+                                     const dsa_bf16* ln_w, const dsa_bf16* ln_b, float eps,
+                                     const dsa_paging* pg, int32_t* seq_lens, int first_key,
+                                     int kpool, int ihd, int kv_lora_rank, dsa_bf16* k_raw,
+                                     dsa_bf16* gate, uint8_t* token_valid, dsa_bf16* ckv,
+                                     uint8_t* ckv_codes, uint8_t* ckv_scales, int cache_exp,
+                                     dsa_bf16* kpool_out, uint8_t* pool_valid, int32_t* pool_idx,
+                                     int32_t* row_ctx, int32_t* status, void* stream) {
+    if (!ckv_codes || !ckv_scales)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_decode_append_fp4: NULL FP4 cache");
+    return decode_append_impl("dsa_decode_append_fp4", k_new, gate_new, ckv_new, ape, ln_w, ln_b,
+                              eps, pg, seq_lens, first_key, kpool, ihd, kv_lora_rank, k_raw, gate,
+                              token_valid, ckv, nullptr, nullptr, ckv_codes, ckv_scales, cache_exp,
+                              kpool_out, pool_valid, pool_idx, row_ctx, status, stream);
 }

@@ -1,0 +1,127 @@
+// dsa_quantize_latent_fp4 and dsa_dequantize_latent_fp4: rows into the FP4 latent cache
+// and out of it again (format and rounding in fp4.cuh).
+//
+// Both are streams: a token's rows are independent 16-channel blocks, so a thread takes
+// one block (32 bytes of bf16, 8 bytes of codes, one scale byte) and a warp 512
+// channels; a block's maximum needs no exchange between threads.
+#include "fp4.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kF4Threads = 256;
+
+__global__ void __launch_bounds__(kF4Threads) quantize_latent_fp4_kernel(
+    const uint4* __restrict__ x, long long blocks, int cache_exp, uint2* __restrict__ codes,
+    uint8_t* __restrict__ scales) {
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * kF4Threads + threadIdx.x;
+    if (i >= blocks) return;
+    const uint4 v[2] = {ldg16_stream(x + 2 * i), ldg16_stream(x + 2 * i + 1)};
+    uint8_t s;
+    codes[i] = fp4_encode16(v, cache_exp, &s);
+    scales[i] = s;
+}
+
+// out row i = cache row rows[i] (rows NULL: row i); a row outside [0, cache_rows) gives
+// zeros and flags DSA_STATUS_BAD_TOKEN.
+__global__ void __launch_bounds__(kF4Threads) dequantize_latent_fp4_kernel(
+    const uint2* __restrict__ codes, const uint8_t* __restrict__ scales,
+    const int32_t* __restrict__ rows, long long blocks, int per_row, long long cache_rows,
+    int cache_exp, uint4* __restrict__ out, int32_t* status) {
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * kF4Threads + threadIdx.x;
+    if (i >= blocks) return;
+    long long src = i;
+    if (rows) {
+        const long long r = i / per_row;
+        const int cr = rows[r];
+        if (cr < 0 || cr >= cache_rows) {
+            out[2 * i] = out[2 * i + 1] = make_uint4(0, 0, 0, 0);
+            if (i == r * per_row) flag_status(status, DSA_STATUS_BAD_TOKEN);
+            return;
+        }
+        src = (long long)cr * per_row + (i - r * per_row);
+    }
+    const uint2 c = codes[src];
+    const uint32_t sh = e4m3x2_to_f16x2(scales[src]);
+    const float s =
+        __half2float(__ushort_as_half((unsigned short)(sh & 0xffffu))) * pow2f(cache_exp);
+    const uint32_t cw[2] = {c.x, c.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t h[4], o[4];
+        e2m1x8_to_f16x8(h, cw[j]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+            o[k] = pack_bf16x2(f.x * s, f.y * s);  // exact
+        }
+        out[2 * i + j] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+int check_fp4(const char* name, long long rows, int kvl, int cache_exp) {
+    if (rows < 0 || kvl < kF4Block || kvl % kF4Block != 0)
+        return fail(DSA_ERR_INVALID_ARG, "%s: rows %lld, kv_lora_rank %d (a multiple of %d)", name,
+                    rows, kvl, kF4Block);
+    if (cache_exp < -kF4MaxExp || cache_exp > kF4MaxExp)
+        return fail(DSA_ERR_INVALID_ARG, "%s: cache_exp %d outside [-%d, %d]", name, cache_exp,
+                    kF4MaxExp, kF4MaxExp);
+    if (rows > 0x7fffffffLL || rows * (kvl / kF4Block) > 0x7fffffffLL * kF4Threads)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: too many rows", name);
+    return DSA_OK;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" int dsa_quantize_latent_fp4(const dsa_bf16* x, long long rows, int kv_lora_rank,
+                                       int cache_exp, uint8_t* codes, uint8_t* scales,
+                                       void* stream) {
+    int rc = check_fp4("dsa_quantize_latent_fp4", rows, kv_lora_rank, cache_exp);
+    if (rc) return rc;
+    if (rows == 0) return DSA_OK;
+    if (!x || !codes || !scales)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_quantize_latent_fp4: NULL tensor");
+    if ((((uintptr_t)x) | ((uintptr_t)codes) | ((uintptr_t)scales)) & 15)
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_quantize_latent_fp4: tensors must be 16-byte aligned");
+    const long long blocks = rows * (kv_lora_rank / kF4Block);
+    const long long grid = (blocks + kF4Threads - 1) / kF4Threads;
+    cudaError_t e = launch_pdl(quantize_latent_fp4_kernel, dim3((unsigned)grid), dim3(kF4Threads),
+                               0, (cudaStream_t)stream, (const uint4*)x, blocks, cache_exp,
+                               (uint2*)codes, scales);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_quantize_latent_fp4 launch");
+    return DSA_OK;
+}
+
+extern "C" int dsa_dequantize_latent_fp4(const uint8_t* codes, const uint8_t* scales,
+                                         long long cache_rows, const int32_t* row_ids,
+                                         long long rows, int kv_lora_rank, int cache_exp,
+                                         dsa_bf16* out, int32_t* status, void* stream) {
+    int rc = check_fp4("dsa_dequantize_latent_fp4", rows, kv_lora_rank, cache_exp);
+    if (rc) return rc;
+    if (cache_rows < 0 || (!row_ids && rows > cache_rows))
+        return fail(DSA_ERR_INVALID_ARG, "dsa_dequantize_latent_fp4: %lld rows of a cache of %lld",
+                    rows, cache_rows);
+    if (rows == 0) return DSA_OK;
+    if (!codes || !scales || !out)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_dequantize_latent_fp4: NULL tensor");
+    if ((((uintptr_t)out) | ((uintptr_t)codes) | ((uintptr_t)scales)) & 15)
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_dequantize_latent_fp4: tensors must be 16-byte aligned");
+    const int per_row = kv_lora_rank / kF4Block;
+    const long long blocks = rows * per_row;
+    const long long grid = (blocks + kF4Threads - 1) / kF4Threads;
+    cudaError_t e =
+        launch_pdl(dequantize_latent_fp4_kernel, dim3((unsigned)grid), dim3(kF4Threads), 0,
+                   (cudaStream_t)stream, (const uint2*)codes, scales, row_ids, blocks, per_row,
+                   cache_rows, cache_exp, (uint4*)out, status);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_dequantize_latent_fp4 launch");
+    return DSA_OK;
+}

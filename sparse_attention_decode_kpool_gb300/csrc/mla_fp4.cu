@@ -1,0 +1,488 @@
+// dsa_sparse_mla_decode_fp4: latent attention over the selected tokens of an FP4 cache.
+//
+// Page: metrale_model_arch/glm5next_dsa/mod.rs, "Shape of the pipeline" (last stage) and
+// build.rs module doc, transforms 1 and 3 (absorbed Q; each latent row is both key and
+// value). Per row r and head h over the selected tokens t, with v[t, :] the decoded row:
+//
+//   s[t] = softmax_scale * <q[h, :], v[t, :]>,  p = softmax(s),  olat[h, :] = sum_t p[t] v[t, :]
+//
+// The cache's power of two 2^cache_exp is taken out of v: it multiplies the logits'
+// scale and the output once, and the matrix products run on code * scale, which is exact
+// in f16. Q goes to f16 too, times a power of two per query row (f4_q_exp), and the
+// probabilities are kept in f16 shifted up by kUp (they reach 2^kUp): a weight is then
+// rounded by at most 2^-12 of itself down to 2^-14 - kUp of the row's largest, where bf16
+// weights would carry 2^-9. Sums, maxima and the output accumulate in f32.
+//
+// mla_f4_split_kernel -- one CTA of eight warps per (split of the token list, row, group
+// of up to 32 heads), mma.sync m16n8k16. A chunk is 64 tokens; warp w owns tokens
+// 8w .. 8w + 7: it resolves them, gathers their 288 bytes with cp.async into its part of
+// a three-stage ring, decodes them into the swizzled f16 tile and computes their scores,
+// all without the other warps. Then the heads' maxima are exchanged, P goes to shared
+// memory, and warp w adds P V for latent columns 64w .. 64w + 63.
+#include "mla_fp4.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int KVL = DSA_KV_LORA_RANK;
+constexpr int CH = 64;               // tokens per chunk
+constexpr int NW = 8;                // warps
+constexpr int NTH = NW * 32;
+constexpr int ROWB = KVL * 2;        // bytes of a decoded row
+constexpr int RAWB = KVL / 2 + KVL / kF4Block;  // 288
+constexpr int STAGES = 3;
+constexpr int kMaxSplits = 64;       // what the combine kernel takes
+constexpr float kUp = 14.f;          // probabilities reach 2^kUp in f16
+static_assert(CH == 8 * NW, "a warp owns eight tokens");
+
+// D += A * B, m16n8k16, f16 inputs, f32 accumulate.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return (uint32_t)(row * ROWB + ((chunk ^ (row & 7)) << 4));
+}
+
+template <int MT>
+struct Smem {
+    static constexpr int HP = 16 * MT;
+    static constexpr int Q = 0;
+    static constexpr int TILE = Q + HP * ROWB;
+    static constexpr int RAW = TILE + CH * ROWB;
+    static constexpr int P = RAW + STAGES * CH * RAWB;
+    static constexpr int RED = P + HP * CH * 2;   // [NW][HP] f32
+    static constexpr int MASK = RED + NW * HP * 4;  // [STAGES][CH]
+    static constexpr int QMAX = MASK + STAGES * CH;
+    static constexpr int BYTES = QMAX + NW * 4;
+};
+
+template <int MT>
+__global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
+    pdl_wait();
+    using S = Smem<MT>;
+    constexpr int HP = S::HP;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* Qs = smem + S::Q;
+    uint8_t* tile = smem + S::TILE;
+    uint8_t* raw = smem + S::RAW;
+    uint8_t* Ps = smem + S::P;
+    float* red = reinterpret_cast<float*>(smem + S::RED);
+    uint8_t* vmask = smem + S::MASK;
+    uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + S::QMAX);
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, q = lane & 3;
+    const int split = blockIdx.x, r = blockIdx.y, head0 = blockIdx.z * HP;
+    const int nh = min(HP, a.heads - head0);
+
+    int seq = a.row_seq ? __ldg(a.row_seq + r) : r;
+    int L = 0;
+    if (seq >= 0 && seq < a.pg.batch) {
+        L = min(__ldg(a.pg.seq_lens + seq), seq_capacity(a.pg));
+    } else {
+        if (tid == 0 && split == 0 && blockIdx.z == 0) flag_status(a.status, DSA_STATUS_BAD_TOKEN);
+        seq = 0;
+    }
+    const int t_begin = split * a.tps;
+    const int t_end = min(t_begin + a.tps, a.ow);
+    const int nch = t_end > t_begin ? (t_end - t_begin + CH - 1) / CH : 0;
+
+    // This warp's eight tokens of chunk c into ring stage c % STAGES (absent ones as zeros:
+    // a masked token's row is never read, so nothing in it can reach the sums).
+    auto gather = [&](int c) {
+        const int st = c % STAGES;
+        long long prow = -1;
+        if (lane < 8) {
+            prow = f4_token(a, r, seq, L, t_begin + c * CH + warp * 8 + lane, t_end);
+            vmask[st * CH + warp * 8 + lane] = prow >= 0 ? 1 : 0;
+        }
+        uint8_t* dst = raw + (st * CH + warp * 8) * RAWB;
+#pragma unroll
+        for (int k = 0; k < (8 * (RAWB / 16) + 31) / 32; ++k) {
+            const int i = lane + 32 * k;
+            const int j = min(i / (RAWB / 16), 7), c16 = i - j * (RAWB / 16);
+            const long long pr = __shfl_sync(0xffffffffu, prow, j);
+            if (i < 8 * (RAWB / 16)) {
+                const long long row = pr >= 0 ? pr : 0;
+                const uint8_t* src = c16 < 16
+                                         ? a.codes + row * (KVL / 2) + c16 * 16
+                                         : a.scales + row * (KVL / kF4Block) + (c16 - 16) * 16;
+                cp_async16(smem_u32(dst + j * RAWB + c16 * 16), src, pr >= 0 ? 16 : 0);
+            }
+        }
+    };
+#pragma unroll
+    for (int c = 0; c < STAGES - 1; ++c) {
+        if (c < nch) gather(c);
+        cp_async_commit();
+    }
+
+    // Q rows to f16 (zero rows past the last head), times 2^qe.
+    int qe;
+    {
+        const uint16_t* qb = a.qlat + ((long long)r * a.heads + head0) * KVL;
+        uint4 v[HP * 64 / NTH];
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < HP * 64 / NTH; ++k) {
+            const int i = tid + k * NTH, row = i >> 6, c = i & 63;
+            v[k] = row < nh ? ldg16(qb + row * KVL + c * 8) : make_uint4(0, 0, 0, 0);
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[k].x), f4_finite_abs2(v[k].y)),
+                                     __vmaxu2(f4_finite_abs2(v[k].z), f4_finite_abs2(v[k].w))));
+        }
+        m = max(m & 0xffffu, m >> 16);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) qmax[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) m = max(m, qmax[w]);
+        qe = f4_q_exp(m);
+        const float mul = pow2f(qe);
+#pragma unroll
+        for (int k = 0; k < HP * 64 / NTH; ++k) {
+            const int i = tid + k * NTH, row = i >> 6, c = i & 63;
+            *reinterpret_cast<uint4*>(Qs + swz(row, c)) =
+                make_uint4(f4_q_half2(v[k].x, mul), f4_q_half2(v[k].y, mul),
+                           f4_q_half2(v[k].z, mul), f4_q_half2(v[k].w, mul));
+        }
+    }
+    const float sl2 = a.scale * kLog2e4 * a.vscale * pow2f(-qe);
+
+    float m0[MT], m1[MT], l0[MT], l1[MT];  // heads 16 i + g and + 8: running max, this warp's sums
+    float oacc[MT][8][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        m0[i] = m1[i] = -INFINITY;
+        l0[i] = l1[i] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+            oacc[i][n][0] = oacc[i][n][1] = oacc[i][n][2] = oacc[i][n][3] = 0.f;
+    }
+    const int mi = lane >> 3;
+    const int arow = (lane & 7) + ((lane >> 3) & 1) * 8;
+
+    for (int c = 0; c < nch; ++c) {
+        const int st = c % STAGES;
+        if (c + STAGES - 1 < nch) gather(c + STAGES - 1);
+        cp_async_commit();
+        cp_async_wait<STAGES - 1>();
+        __syncthreads();  // Q in place (c == 0); the tile's readers of chunk c - 1 are done
+
+        // ---- decode this warp's tokens: 16-channel block b of token j, 8 bytes each
+        {
+            const uint8_t* rb = raw + (st * CH + warp * 8) * RAWB;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint8_t* row = rb + k * RAWB;
+                const uint2 cw = *reinterpret_cast<const uint2*>(row + lane * 8);
+                const uint32_t s = row[KVL / 2 + lane];
+                const uint32_t s2 = e4m3x2_to_f16x2(s | (s << 8));
+                *reinterpret_cast<uint4*>(tile + swz(warp * 8 + k, 2 * lane)) = fp4_decode8(cw.x, s2);
+                *reinterpret_cast<uint4*>(tile + swz(warp * 8 + k, 2 * lane + 1)) =
+                    fp4_decode8(cw.y, s2);
+            }
+        }
+        __syncwarp();
+
+        // ---- S = Q K^T: MT x 16 heads by this warp's 8 tokens
+        float sacc[MT][4];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) sacc[i][0] = sacc[i][1] = sacc[i][2] = sacc[i][3] = 0.f;
+#pragma unroll 4
+        for (int kk = 0; kk < KVL / 32; ++kk) {
+            uint32_t bf[4];  // k-steps 2 kk and 2 kk + 1
+            ldsm_x4(bf, smem_u32(tile + swz(warp * 8 + (lane & 7), 4 * kk + mi)));
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                uint32_t a0[4], a1[4];
+                ldsm_x4(a0, smem_u32(Qs + swz(16 * i + arow, 4 * kk + (lane >> 4))));
+                ldsm_x4(a1, smem_u32(Qs + swz(16 * i + arow, 4 * kk + 2 + (lane >> 4))));
+                mma_f16(sacc[i], a0, bf[0], bf[1]);
+                mma_f16(sacc[i], a1, bf[2], bf[3]);
+            }
+        }
+        const bool ok0 = vmask[st * CH + warp * 8 + 2 * q] != 0;
+        const bool ok1 = vmask[st * CH + warp * 8 + 2 * q + 1] != 0;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            sacc[i][0] = ok0 ? sacc[i][0] * sl2 : -INFINITY;
+            sacc[i][1] = ok1 ? sacc[i][1] * sl2 : -INFINITY;
+            sacc[i][2] = ok0 ? sacc[i][2] * sl2 : -INFINITY;
+            sacc[i][3] = ok1 ? sacc[i][3] * sl2 : -INFINITY;
+            float x0 = fmaxf(sacc[i][0], sacc[i][1]), x1 = fmaxf(sacc[i][2], sacc[i][3]);
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+            if (q == 0) {
+                red[warp * HP + 16 * i + g] = x0;
+                red[warp * HP + 16 * i + g + 8] = x1;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            float n0 = m0[i], n1 = m1[i];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                n0 = fmaxf(n0, red[w * HP + 16 * i + g]);
+                n1 = fmaxf(n1, red[w * HP + 16 * i + g + 8]);
+            }
+            // all logits so far absent (or -inf): any finite stand-in gives weights 0
+            const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+            const float al0 = exp2f(m0[i] - u0), al1 = exp2f(m1[i] - u1);
+            m0[i] = n0;
+            m1[i] = n1;
+            const __half2 p0 = __floats2half2_rn(exp2f(sacc[i][0] - u0 + kUp),
+                                                 exp2f(sacc[i][1] - u0 + kUp));
+            const __half2 p1 = __floats2half2_rn(exp2f(sacc[i][2] - u1 + kUp),
+                                                 exp2f(sacc[i][3] - u1 + kUp));
+            const float2 f0 = __half22float2(p0), f1 = __half22float2(p1);
+            l0[i] = l0[i] * al0 + (f0.x + f0.y);
+            l1[i] = l1[i] * al1 + (f1.x + f1.y);
+            const int h0 = 16 * i + g, h1 = h0 + 8;
+            *reinterpret_cast<__half2*>(Ps + h0 * (CH * 2) + ((warp ^ (h0 & 7)) << 4) + 4 * q) = p0;
+            *reinterpret_cast<__half2*>(Ps + h1 * (CH * 2) + ((warp ^ (h1 & 7)) << 4) + 4 * q) = p1;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                oacc[i][n][0] *= al0;
+                oacc[i][n][1] *= al0;
+                oacc[i][n][2] *= al1;
+                oacc[i][n][3] *= al1;
+            }
+        }
+        __syncthreads();
+
+        // ---- O += P V, latent columns 64 warp .. + 63
+#pragma unroll
+        for (int kk = 0; kk < CH / 16; ++kk) {
+            uint32_t af[MT][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int h = 16 * i + arow;
+                ldsm_x4(af[i], smem_u32(Ps + h * (CH * 2) + (((2 * kk + (lane >> 4)) ^ (h & 7)) << 4)));
+            }
+            const int tok = kk * 16 + (mi & 1) * 8 + (lane & 7);
+#pragma unroll
+            for (int dp = 0; dp < 4; ++dp) {
+                uint32_t bf[4];
+                ldsm_x4_t(bf, smem_u32(tile + swz(tok, warp * 8 + 2 * dp + (mi >> 1))));
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    mma_f16(oacc[i][2 * dp], af[i], bf[0], bf[1]);
+                    mma_f16(oacc[i][2 * dp + 1], af[i], bf[2], bf[3]);
+                }
+            }
+        }
+    }
+    cp_async_wait<0>();
+
+    // ---- the warps' sums, in warp order
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        l0[i] += __shfl_xor_sync(0xffffffffu, l0[i], 1);
+        l1[i] += __shfl_xor_sync(0xffffffffu, l1[i], 1);
+        l0[i] += __shfl_xor_sync(0xffffffffu, l0[i], 2);
+        l1[i] += __shfl_xor_sync(0xffffffffu, l1[i], 2);
+        if (q == 0) {
+            red[warp * HP + 16 * i + g] = l0[i];
+            red[warp * HP + 16 * i + g + 8] = l1[i];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int h = 16 * i + g + 8 * half;
+            if (h >= nh) continue;
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) l += red[w * HP + h];
+            const int d0 = warp * 64 + 2 * q;
+            if (a.ns == 1) {
+                // a NaN sum (a NaN in q or in a selected row) keeps its NaN
+                const float k = l == 0.f ? 0.f : a.vscale / l;
+                const long long o = ((long long)r * a.heads + head0 + h) * KVL + d0;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float x = oacc[i][n][2 * half] * k, y = oacc[i][n][2 * half + 1] * k;
+                    if (a.olat) *reinterpret_cast<float2*>(a.olat + o + 8 * n) = make_float2(x, y);
+                    if (a.olat16)
+                        *reinterpret_cast<uint32_t*>(a.olat16 + o + 8 * n) = pack_bf16x2(x, y);
+                }
+            } else {
+                const long long u = ((long long)r * a.ns + split) * a.heads + head0 + h;
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+                    *reinterpret_cast<float2*>(a.part_o + u * KVL + d0 + 8 * n) = make_float2(
+                        oacc[i][n][2 * half] * a.vscale, oacc[i][n][2 * half + 1] * a.vscale);
+                if (warp == 0 && q == 0)
+                    *reinterpret_cast<float2*>(a.part_ml + u * 2) =
+                        make_float2(half ? m1[i] : m0[i], l);
+            }
+        }
+}
+
+// ---------------------------------------------------------------------------
+struct F4Plan {
+    int mt, hgroups, ns, tps;
+    size_t off_part_o, off_part_ml, off_xbf, off_proj, bytes;
+};
+size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+F4Plan f4_plan(int rows, int heads, int ow, int hidden, bool with_oabs, int sms) {
+    F4Plan p;
+    p.mt = heads <= 16 ? 1 : 2;
+    p.hgroups = (heads + 16 * p.mt - 1) / (16 * p.mt);
+    const long long base = (long long)rows * p.hgroups;
+    const int max_ns = ow > 0 ? (ow + CH - 1) / CH : 1;
+    long long ns = base > 0 ? sms / base : 1;  // one wave of CTAs
+    if (ns < 1) ns = 1;
+    if (ns > max_ns) ns = max_ns;
+    if (ns > kMaxSplits) ns = kMaxSplits;
+    const int per = ow > 0 ? (int)((ow + ns - 1) / ns) : 0;
+    p.tps = per > 0 ? ((per + CH - 1) / CH) * CH : CH;
+    p.ns = ow > 0 ? (ow + p.tps - 1) / p.tps : 1;
+    size_t off = 0;
+    p.off_part_o = off;
+    if (p.ns > 1) off += al256((size_t)rows * p.ns * heads * KVL * 4);
+    p.off_part_ml = off;
+    if (p.ns > 1) off += al256((size_t)rows * p.ns * heads * 2 * 4);
+    p.off_xbf = off;
+    if (with_oabs) off += al256((size_t)rows * heads * KVL * 2);
+    p.off_proj = off;
+    if (with_oabs) off += al256(project_workspace_bytes(rows, heads * KVL, hidden, sms));
+    p.bytes = off;
+    return p;
+}
+
+int check_f4(int rows, int heads, int kvl, int ow, int hidden, bool with_oabs) {
+    if (rows < 0 || heads < 1 || ow < 0)
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_sparse_mla_decode_fp4: rows %d, heads %d, out_width %d", rows, heads, ow);
+    if (kvl != KVL)
+        return fail(kvl == 0 ? DSA_ERR_CONFIG : DSA_ERR_UNSUPPORTED,
+                    "dsa_sparse_mla_decode_fp4: kv_lora_rank %d, kernels are built for %d", kvl,
+                    KVL);
+    if (rows > 65535)
+        return fail(DSA_ERR_UNSUPPORTED, "dsa_sparse_mla_decode_fp4: rows %d > 65535", rows);
+    if (heads > 4096)
+        return fail(DSA_ERR_UNSUPPORTED, "dsa_sparse_mla_decode_fp4: heads %d > 4096", heads);
+    if (with_oabs && !project_supported(heads * KVL, hidden))
+        return fail(DSA_ERR_UNSUPPORTED,
+                    "dsa_sparse_mla_decode_fp4: hidden %d must be a positive multiple of 64",
+                    hidden);
+    return DSA_OK;
+}
+
+template <int MT>
+int launch_split(const MlaF4Args& a, const F4Plan& p, cudaStream_t st) {
+    static_assert(Smem<MT>::BYTES <= 227 * 1024, "split kernel shared memory");
+    int rc = set_max_smem((const void*)mla_f4_split_kernel<MT>, Smem<MT>::BYTES);
+    if (rc) return rc;
+    cudaError_t e = launch_pdl(mla_f4_split_kernel<MT>, dim3(p.ns, a.rows, p.hgroups), dim3(NTH),
+                               Smem<MT>::BYTES, st, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_sparse_mla_decode_fp4 split launch");
+    return DSA_OK;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" int dsa_sparse_mla_decode_fp4_workspace(int rows, int heads, int kv_lora_rank,
+                                                   int out_width, int hidden, int with_o_absorb,
+                                                   size_t* bytes) {
+    if (!bytes)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_sparse_mla_decode_fp4_workspace: bytes is NULL");
+    int rc = check_f4(rows, heads, kv_lora_rank, out_width, hidden, with_o_absorb != 0);
+    if (rc) return rc;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4_workspace: no CUDA device");
+    *bytes = f4_plan(rows, heads, out_width, hidden, with_o_absorb != 0, sms).bytes;
+    return DSA_OK;
+}
+
+extern "C" int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int heads,
+                                         int kv_lora_rank, const int32_t* row_seq,
+                                         const uint8_t* ckv_codes, const uint8_t* ckv_scales,
+                                         int cache_exp, const dsa_paging* pg,
+                                         const int32_t* token_ids, int out_width,
+                                         float softmax_scale, const dsa_bf16* o_absorb, int hidden,
+                                         dsa_bf16* y, float* olat, dsa_bf16* olat16,
+                                         int32_t* status, void* workspace, size_t workspace_bytes,
+                                         void* stream) {
+    const bool with_oabs = o_absorb != nullptr;
+    int rc = check_f4(rows, heads, kv_lora_rank, out_width, hidden, with_oabs);
+    if (rc) return rc;
+    if (cache_exp < -kF4MaxExp || cache_exp > kF4MaxExp)
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_sparse_mla_decode_fp4: cache_exp %d outside [-%d, %d]", cache_exp,
+                    kF4MaxExp, kF4MaxExp);
+    if (with_oabs != (y != nullptr))
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_sparse_mla_decode_fp4: o_absorb and y must be both given or both NULL");
+    Paging P;
+    rc = check_paging(pg, 0, &P);
+    if (rc) return rc;
+    if (rows == 0) return DSA_OK;
+    if (!qlat || !ckv_codes || !ckv_scales || (out_width > 0 && !token_ids))
+        return fail(DSA_ERR_INVALID_ARG, "dsa_sparse_mla_decode_fp4: NULL tensor");
+    if ((((uintptr_t)qlat) | ((uintptr_t)ckv_codes) | ((uintptr_t)ckv_scales) |
+         ((uintptr_t)o_absorb) | ((uintptr_t)olat) | ((uintptr_t)olat16) | ((uintptr_t)y) |
+         ((uintptr_t)workspace)) & 15)
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_sparse_mla_decode_fp4: tensors must be 16-byte aligned");
+    if (!olat && !olat16 && !with_oabs) return DSA_OK;  // nothing requested
+    const int sms = sm_count();
+    if (sms <= 0) return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4: no CUDA device");
+    const F4Plan p = f4_plan(rows, heads, out_width, hidden, with_oabs, sms);
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+        return fail(DSA_ERR_INVALID_ARG,
+                    "dsa_sparse_mla_decode_fp4: workspace %zu B < %zu B needed", workspace_bytes,
+                    p.bytes);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    cudaStream_t st = (cudaStream_t)stream;
+    // the projection reads a bf16 olat: the caller's where there is one
+    uint16_t* x16 = olat16 ? olat16
+                           : with_oabs ? reinterpret_cast<uint16_t*>(ws + p.off_xbf) : nullptr;
+    MlaF4Args a;
+    a.qlat = qlat;
+    a.row_seq = row_seq;
+    a.codes = ckv_codes;
+    a.scales = ckv_scales;
+    a.token_ids = token_ids;
+    a.part_o = p.ns > 1 ? reinterpret_cast<float*>(ws + p.off_part_o) : nullptr;
+    a.part_ml = p.ns > 1 ? reinterpret_cast<float*>(ws + p.off_part_ml) : nullptr;
+    a.olat = olat;
+    a.olat16 = x16;
+    a.status = status;
+    a.pg = P;
+    a.rows = rows;
+    a.heads = heads;
+    a.ow = out_width;
+    a.ns = p.ns;
+    a.tps = p.tps;
+    a.scale = softmax_scale;
+    a.vscale = ldexpf(1.f, cache_exp);
+    rc = p.mt == 1 ? launch_split<1>(a, p, st) : launch_split<2>(a, p, st);
+    if (rc) return rc;
+    if (p.ns > 1) {
+        rc = mla_combine_launch(a.part_o, a.part_ml, rows, heads, p.ns, olat, x16, st);
+        if (rc) return rc;
+    }
+    if (with_oabs)
+        return project_launch(x16, false, rows, heads * KVL, o_absorb, hidden, y, status,
+                              ws + p.off_proj, workspace_bytes - p.off_proj, st);
+    return DSA_OK;
+}

@@ -1,0 +1,64 @@
+// Arguments shared by the kernels of dsa_sparse_mla_decode_fp4 (mla_fp4.cu).
+#pragma once
+
+#include "fp4.cuh"
+
+namespace dsa {
+
+constexpr float kLog2e4 = 1.4426950408889634f;
+
+struct MlaF4Args {
+    const uint16_t* qlat;
+    const int32_t* row_seq;
+    const uint8_t* codes;   // [cache rows, 256]
+    const uint8_t* scales;  // [cache rows, 32]
+    const int32_t* token_ids;
+    float* part_o;    // ns > 1: [rows, ns, heads, 512] unnormalised
+    float* part_ml;   // ... and [rows, ns, heads, 2] (maximum in log2 units, sum)
+    float* olat;      // ns == 1, nullable
+    uint16_t* olat16; // ns == 1, nullable (bf16)
+    int32_t* status;
+    Paging pg;
+    int rows;
+    int heads;
+    int ow;
+    int ns;
+    int tps;
+    float scale;   // softmax_scale
+    float vscale;  // 2^cache_exp
+};
+
+// The cache row of selected position pos of row r (sequence seq, L tokens), or -1 where
+// there is none; bad ids and block entries are flagged.
+__device__ __forceinline__ long long f4_token(const MlaF4Args& a, int r, int seq, int L, int pos,
+                                              int end) {
+    if (pos >= end) return -1;
+    const int t = __ldg(a.token_ids + (long long)r * a.ow + pos);
+    if (t >= 0 && t < L) {
+        const long long row = token_row(a.pg, seq, t);
+        if (row < 0) flag_status(a.status, DSA_STATUS_BAD_BLOCK);
+        return row;
+    }
+    if (t != -1) flag_status(a.status, DSA_STATUS_BAD_TOKEN);
+    return -1;
+}
+
+// The power of two that brings a query row's largest finite magnitude (bf16 bits amax)
+// to [2^14, 2^15), where bf16 values convert to f16 without overflow and lose nothing
+// that the f32 sums would keep. 0 where the row is all zeros.
+__device__ __forceinline__ int f4_q_exp(uint32_t amax) {
+    if (amax == 0u) return 0;
+    const int e = max((int)(amax >> 7), 1) - 127;  // subnormals: their largest exponent
+    return min(14 - e, 126);
+}
+// Finite magnitudes of two packed bf16, Inf and NaN as 0.
+__device__ __forceinline__ uint32_t f4_finite_abs2(uint32_t u) {
+    const uint32_t lo = u & 0x7fffu, hi = (u >> 16) & 0x7fffu;
+    return (lo < 0x7f80u ? lo : 0u) | (hi < 0x7f80u ? hi << 16 : 0u);
+}
+__device__ __forceinline__ uint32_t f4_q_half2(uint32_t u, float mul) {
+    const __half2 h = __floats2half2_rn(bf16_lo(u) * mul, bf16_hi(u) * mul);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace dsa

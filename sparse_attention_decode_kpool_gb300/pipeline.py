@@ -8,6 +8,7 @@ CUDA graph.
 """
 from __future__ import annotations
 
+import math
 from typing import Optional
 
 import numpy as np
@@ -22,7 +23,8 @@ class DsaDecodeLayer:
                  with_o_absorb: bool = True, use_drawn_kpool: bool = False,
                  score_path: str = "auto", fuse_expand: bool = True, decode_from=None,
                  fuse_append: bool = True, latent_fp8: bool = False, frontend=None,
-                 l2_prefetch_bytes: Optional[int] = None):
+                 l2_prefetch_bytes: Optional[int] = None, latent_fp4: bool = False,
+                 fp4_exp: Optional[int] = None, manage_pages: bool = False):
         g = wl.geom
         self.wl = wl
         self.geom = g
@@ -50,7 +52,9 @@ class DsaDecodeLayer:
         # FP8 latent cache (E4M3 codes + power-of-two scales per 128 channels), encoded
         # once from the bf16 cache; attention then gathers 528 instead of 1,024 bytes
         # per token.
-        self.latent_fp8 = bool(latent_fp8)
+        self.latent_fp8, self.latent_fp4 = bool(latent_fp8), bool(latent_fp4)
+        if self.latent_fp8 and self.latent_fp4:
+            raise ValueError("one latent cache format: latent_fp8 or latent_fp4")
         self.ckv_codes = self.ckv_scales = None
         if self.latent_fp8:
             if decode_from is not None and not fuse_append:
@@ -61,6 +65,22 @@ class DsaDecodeLayer:
             self.ckv_scales = torch.empty(self.ckv.shape[:-1] + (kvl // 128,),
                                           dtype=torch.float32, device=dev)
             api.dsa_quantize_latent(self.ckv, self.ckv_codes, self.ckv_scales)
+        # FP4 latent cache (E2M1 codes, an E4M3 scale per 16 channels, 2^fp4_exp over all):
+        # 288 bytes per token. fp4_exp defaults to the smallest power of two under which
+        # no block of the uploaded cache saturates.
+        if self.latent_fp4:
+            if decode_from is not None and not fuse_append:
+                raise ValueError("the FP4 latent cache is appended by dsa_decode_append_fp4 "
+                                 "only (fuse_append=True)")
+            kvl = g.kv_lora_rank
+            if fp4_exp is None:
+                amax = float(self.ckv.abs().max()) if self.ckv.numel() else 0.0
+                fp4_exp = math.ceil(math.log2(amax / 2688.0)) if 0.0 < amax < math.inf else 0
+            self.fp4_exp = max(-64, min(64, int(fp4_exp)))
+            lead = self.ckv.shape[:-1]
+            self.ckv_codes = torch.empty(lead + (kvl // 2,), dtype=torch.uint8, device=dev)
+            self.ckv_scales = torch.empty(lead + (kvl // 16,), dtype=torch.uint8, device=dev)
+            api.dsa_quantize_latent_fp4(self.ckv, self.ckv_codes, self.ckv_scales, self.fp4_exp)
         self.o_absorb = up(wl.o_absorb) if with_o_absorb else None
         # The step prefetches the first l2_prefetch_bytes of o_absorb into L2 on a
         # second stream while top-k and the gather run (they leave HBM mostly idle);
@@ -102,7 +122,7 @@ class DsaDecodeLayer:
         self.keep_olat = bool(keep_olat)
         self.olat = (torch.empty((R, g.heads, g.kv_lora_rank), dtype=torch.float32, device=dev)
                      if (keep_olat or self.o_absorb is not None) else None)
-        ws = api.dsa_sparse_mla_decode_workspace(R, g.heads, g.out_width, 0, False)
+        ws = self._mla_workspace(0, False)
         self.workspace = torch.zeros(max(ws, 1), dtype=torch.uint8, device=dev)
         # The stages attend() and project() are the two-call form (attention to olat,
         # then dsa_latent_project) where the projection kernels support the shape
@@ -138,11 +158,81 @@ class DsaDecodeLayer:
         self.append_graph: Optional[torch.cuda.CUDAGraph] = None
         if decode_from is not None:
             self._init_append(decode_from)
+        # Pages: with manage_pages the layer keeps a count per page, maps pages as the
+        # sequences grow, and can fork, free and compact them.
+        self.refs: Optional[torch.Tensor] = None
+        if manage_pages:
+            self._init_pages()
         # Projection front-end (dsa_frontend): the step's query inputs and the token's
         # staged rows computed from a hidden state x on the device.
         self.fe = None
         if frontend is not None:
             self._init_frontend(frontend)
+
+    # -- pages -------------------------------------------------------------
+    def _init_pages(self) -> None:
+        wl, g = self.wl, self.geom
+        if not wl.paged:
+            raise ValueError("manage_pages needs a paged workload")
+        if wl.rows != wl.batch or not (wl.row_seq == np.arange(wl.batch)).all():
+            raise ValueError("manage_pages takes one decode row per sequence")
+        # only the pages that hold tokens are mapped; the others are free
+        held = (self.seq_lens.long() + wl.block_size - 1) // wl.block_size
+        j = torch.arange(self.block_table.shape[1], device=self.device)
+        self.block_table.masked_fill_(j[None] >= held[:, None], -1)
+        ids = self.block_table[self.block_table >= 0].long()
+        self.refs = torch.bincount(ids, minlength=wl.num_blocks).int()
+        latent = ([self.ckv_codes, self.ckv_scales] if self.latent_fp8 or self.latent_fp4
+                  else [self.ckv])
+        caches = [self.k_raw, self.gate, self.valid, *latent, self.kpool, self.pool_valid]
+        self._paged = [c for c in caches if c is not None]
+        self.page_arrays = api.page_arrays(self._paged, wl.num_blocks)
+        n = api.dsa_pages_workspace(wl.num_blocks, wl.batch)
+        self.page_workspace = torch.zeros(n, dtype=torch.uint8, device=self.device)
+        self.page_remap = torch.zeros(wl.num_blocks, dtype=torch.int32, device=self.device)
+        self.pages_live = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _seq_list(self, seqs, stream) -> torch.Tensor:
+        """A device list of sequences; one made here belongs to the stream that reads it."""
+        if self.refs is None:
+            raise ValueError("the layer was not built with manage_pages")
+        if isinstance(seqs, torch.Tensor) and seqs.is_cuda:
+            return seqs
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.as_tensor(seqs, dtype=torch.int32, device=self.device)
+
+    def free_sequences(self, seqs, stream=None) -> None:
+        """End sequences: their pages lose a reference, their length becomes 0."""
+        api.dsa_pages_free(self._seq_list(seqs, stream), self.pg, self.block_table,
+                           self.seq_lens, self.refs, self.status, stream=stream)
+
+    def fork_sequences(self, parents, children, stream=None) -> None:
+        """children[i] continues from a copy of parents[i] (the pages are shared until one
+        of the two writes to them)."""
+        api.dsa_pages_fork(self._seq_list(parents, stream), self._seq_list(children, stream),
+                           self.pg, self.block_table, self.seq_lens, self.refs, self.status,
+                           stream=stream)
+
+    def reserve_pages(self, new_tokens: int = 1, seqs=None, stream=None) -> None:
+        """Pages for the next tokens of each sequence (append() does it for its one)."""
+        g = self.geom
+        if self.refs is None:
+            raise ValueError("the layer was not built with manage_pages")
+        api.dsa_pages_reserve(self.pg, self.block_table, self.refs, new_tokens, self.page_arrays,
+                              g.first_key, g.index_kpool,
+                              seqs=None if seqs is None else self._seq_list(seqs, stream),
+                              status=self.status, workspace=self.page_workspace, stream=stream)
+
+    def compact_pages(self, stream=None) -> None:
+        """Move the live pages to the pool's front (pages_live: how many, page_remap: where
+        each went)."""
+        if self.refs is None:
+            raise ValueError("the layer was not built with manage_pages")
+        api.dsa_pages_compact(self.pg, self.block_table, self.refs, self.page_arrays,
+                              self.page_remap, self.pages_live, self.status,
+                              self.page_workspace, stream=stream)
 
     def _init_frontend(self, fe) -> None:
         g, dev, R = self.geom, self.device, self.wl.rows
@@ -249,6 +339,8 @@ class DsaDecodeLayer:
         self.row_ctx.copy_(self.seq_lens)
         if self.latent_fp8:  # the FP8 cache of the cut-back bf16 cache
             api.dsa_quantize_latent(self.ckv, self.ckv_codes, self.ckv_scales)
+        if self.latent_fp4:
+            api.dsa_quantize_latent_fp4(self.ckv, self.ckv_codes, self.ckv_scales, self.fp4_exp)
 
     def staged_rows(self, i: int):
         """Host rows (k, gate, ckv) [batch, ...] of the token each sequence appends at
@@ -282,6 +374,16 @@ class DsaDecodeLayer:
     def append(self, stream=None) -> None:
         """indexer_store -> write_geom -> compress of the newly whole pool."""
         g = self.geom
+        if self.refs is not None:
+            self.reserve_pages(1, stream=stream)
+        if self.latent_fp4:  # the token's latent row goes to the FP4 cache only
+            api.dsa_decode_append_fp4(self.k_new, self.gate_new, self.ckv_new, self.ape, self.ln_w,
+                                      self.ln_b, g.eps, self.pg, self.seq_lens, g.first_key,
+                                      g.index_kpool, self.k_raw, self.gate, self.valid,
+                                      self.ckv_codes, self.ckv_scales, self.fp4_exp, self.kpool,
+                                      self.pool_valid, row_ctx=self.row_ctx, status=self.status,
+                                      stream=stream)
+            return
         if self.latent_fp8:  # the token's latent row goes to the FP8 cache only
             api.dsa_decode_append_fp8(self.k_new, self.gate_new, self.ckv_new, self.ape, self.ln_w,
                                       self.ln_b, g.eps, self.pg, self.seq_lens, g.first_key,
@@ -323,13 +425,17 @@ class DsaDecodeLayer:
         self.append_graph = gr
         return gr
 
+    def _mla_workspace(self, hidden: int, with_o_absorb: bool) -> int:
+        g = self.geom
+        query = (api.dsa_sparse_mla_decode_fp4_workspace if self.latent_fp4
+                 else api.dsa_sparse_mla_decode_workspace)
+        return query(self.wl.rows, g.heads, g.out_width, hidden, with_o_absorb)
+
     def fused_workspace(self) -> torch.Tensor:
         """Workspace for the one-call form dsa_sparse_mla_decode(..., o_absorb, y)."""
         if self._fused_ws is None:
-            g, R = self.geom, self.wl.rows
-            hidden = g.hidden if self.o_absorb is not None else 0
-            n = api.dsa_sparse_mla_decode_workspace(R, g.heads, g.out_width, hidden,
-                                                    self.o_absorb is not None)
+            hidden = self.geom.hidden if self.o_absorb is not None else 0
+            n = self._mla_workspace(hidden, self.o_absorb is not None)
             self._fused_ws = torch.zeros(max(n, 1), dtype=torch.uint8, device=self.device)
         return self._fused_ws
 
@@ -374,7 +480,12 @@ class DsaDecodeLayer:
         api.dsa_expand(self.pool_ids, g.first_key, g.index_kpool, self.token_ids, stream=stream)
 
     def _mla(self, o_absorb, y, workspace, stream, olat=None) -> None:
-        if self.latent_fp8:
+        if self.latent_fp4:
+            api.dsa_sparse_mla_decode_fp4(self.qlat, self.row_seq, self.ckv_codes,
+                                          self.ckv_scales, self.fp4_exp, self.pg, self.token_ids,
+                                          self.geom.softmax_scale, o_absorb, y, olat,
+                                          self.status, workspace, stream=stream)
+        elif self.latent_fp8:
             api.dsa_sparse_mla_decode_fp8(self.qlat, self.row_seq, self.ckv_codes, self.ckv_scales,
                                           self.pg, self.token_ids, self.geom.softmax_scale,
                                           o_absorb, y, olat, self.status, workspace,
@@ -427,7 +538,7 @@ class DsaDecodeLayer:
         """Library kernel launches one step() makes."""
         R, g = self.wl.rows, self.geom
         n = 3 if self.fuse_expand else 4  # score, select(+expand), [expand], split attention
-        if api.dsa_sparse_mla_decode_workspace(R, g.heads, g.out_width, 0, False) > 0:
+        if self._mla_workspace(0, False) > 0:
             n += 1  # split combine
         if self.o_absorb is not None:
             # tensor-core projection: one launch per 64 query rows; else the stream-K
@@ -460,12 +571,16 @@ class DsaDecodeLayer:
         """Library kernel launches one layer_step() makes: the front-end's two GEMMs
         with their reductions and the norm kernel, the append, the step."""
         n = 5 + self.launches_per_step()
-        return n + (0 if self.decode_from is None else (1 if self.fuse_append else 3))
+        return n + (0 if self.decode_from is None else self._append_launches())
 
     def launches_per_append_step(self) -> int:
         """Library kernel launches one append_step() makes."""
-        # store, write_geom, compress of the new pool (one launch when fused)
-        return self.launches_per_step() + (1 if self.fuse_append else 3)
+        return self.launches_per_step() + self._append_launches()
+
+    def _append_launches(self) -> int:
+        # store, write_geom, compress of the new pool (one launch when fused); with managed
+        # pages the reservation's two before them
+        return (1 if self.fuse_append else 3) + (0 if self.refs is None else 2)
 
     # -- graphs ------------------------------------------------------------
     def capture(self) -> torch.cuda.CUDAGraph:

@@ -452,16 +452,20 @@ def _fp4_cache(codes, scales) -> int:
 
 def _call(t: torch.Tensor, stream, fn, *args, others=()) -> None:
     """One library call for tensors on t's device: made with that device current, on its
-    current stream by default. ``others`` must live on the same device."""
-    dev = t.device
+    current stream by default. ``others`` must live on the same device (pinned host
+    memory is no device's)."""
+    dev = t.get_device()
     for o in others:
-        if o is not None and o.device != dev and o.is_cuda:
-            raise ValueError(f"tensors on {dev} and {o.device}: one device per call")
-    if torch.cuda.current_device() == dev.index:
-        check(fn(*args, _stream(stream)))
+        if o is not None and o.get_device() != dev and o.is_cuda:
+            raise ValueError(f"tensors on {t.device} and {o.device}: one device per call")
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            check(fn(*args, _stream(stream)))
         return
-    with torch.cuda.device(dev):
-        check(fn(*args, _stream(stream)))
+    # the raw handle, without a Stream object around it: these calls' GPU work is often
+    # shorter than that object's making
+    check(fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+             else _stream(stream)))
 
 
 def dsa_quantize_latent_fp4(x, codes, scales, cache_exp: int = 0, stream=None) -> None:

@@ -332,24 +332,36 @@ __global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
 
 // ---------------------------------------------------------------------------
 struct F4Plan {
+    bool tc;  // the tcgen05 kernel (mla_fp4_tc.cu), else the mma.sync kernel above
     int mt, hgroups, ns, tps;
     size_t off_part_o, off_part_ml, off_xbf, off_proj, bytes;
 };
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-F4Plan f4_plan(int rows, int heads, int ow, int hidden, bool with_oabs, int sms) {
+F4Plan f4_plan(bool tc, int rows, int heads, int ow, int hidden, bool with_oabs, int sms) {
     F4Plan p;
+    p.tc = tc;
     p.mt = heads <= 16 ? 1 : 2;
-    p.hgroups = (heads + 16 * p.mt - 1) / (16 * p.mt);
+    p.hgroups = tc ? (heads + 63) / 64 : (heads + 16 * p.mt - 1) / (16 * p.mt);
+    const int chunk = tc ? mla_f4_tc_chunk() : CH;
     const long long base = (long long)rows * p.hgroups;
-    const int max_ns = ow > 0 ? (ow + CH - 1) / CH : 1;
-    long long ns = base > 0 ? sms / base : 1;  // one wave of CTAs
-    if (ns < 1) ns = 1;
-    if (ns > max_ns) ns = max_ns;
-    if (ns > kMaxSplits) ns = kMaxSplits;
-    const int per = ow > 0 ? (int)((ow + ns - 1) / ns) : 0;
-    p.tps = per > 0 ? ((per + CH - 1) / CH) * CH : CH;
-    p.ns = ow > 0 ? (ow + p.tps - 1) / p.tps : 1;
+    const long long cpr = ow > 0 ? (ow + chunk - 1) / chunk : 1;  // chunks per row
+    p.tps = (int)cpr * chunk;
+    p.ns = 1;
+    // The busiest CTA walks ceil(units / sms) units of ceil(chunks / ns) chunks, plus about
+    // a chunk's time per unit for Q, the epilogue and the combine: the split count that
+    // makes this smallest, the fewest splits on ties.
+    long long best = -1;
+    for (long long t = 1; t <= cpr && t <= kMaxSplits; ++t) {
+        const long long tps = (cpr + t - 1) / t;
+        const long long ns = (cpr + tps - 1) / tps;
+        const long long cost = (base * ns + sms - 1) / sms * (tps + 1);
+        if (best < 0 || cost < best) {
+            best = cost;
+            p.tps = (int)tps * chunk;
+            p.ns = (int)ns;
+        }
+    }
     size_t off = 0;
     p.off_part_o = off;
     if (p.ns > 1) off += al256((size_t)rows * p.ns * heads * KVL * 4);
@@ -361,6 +373,23 @@ F4Plan f4_plan(int rows, int heads, int ow, int hidden, bool with_oabs, int sms)
     if (with_oabs) off += al256(project_workspace_bytes(rows, heads * KVL, hidden, sms));
     p.bytes = off;
     return p;
+}
+
+// Enough for either kernel: the call's choice depends on the cache's size too.
+size_t f4_bytes(int rows, int heads, int ow, int hidden, bool with_oabs, int sms) {
+    const size_t b0 = f4_plan(false, rows, heads, ow, hidden, with_oabs, sms).bytes;
+    const size_t b1 = f4_plan(true, rows, heads, ow, hidden, with_oabs, sms).bytes;
+    return b0 > b1 ? b0 : b1;
+}
+
+// Which kernel: DSA_OPT_MLA_KERNEL's, else the tcgen05 kernel above 32 heads.
+bool f4_use_tc(int heads, int ow, long long cache_rows) {
+    if (ow < 1 || cache_rows > 0x7fffffffLL) return false;
+    switch (mla_kernel_choice()) {
+        case DSA_MLA_KERNEL_TCGEN05: return true;
+        case DSA_MLA_KERNEL_MMA: return false;
+        default: return heads > 32;
+    }
 }
 
 int check_f4(int rows, int heads, int kvl, int ow, int hidden, bool with_oabs) {
@@ -409,7 +438,7 @@ extern "C" int dsa_sparse_mla_decode_fp4_workspace(int rows, int heads, int kv_l
     const int sms = sm_count();
     if (sms <= 0)
         return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4_workspace: no CUDA device");
-    *bytes = f4_plan(rows, heads, out_width, hidden, with_o_absorb != 0, sms).bytes;
+    *bytes = f4_bytes(rows, heads, out_width, hidden, with_o_absorb != 0, sms);
     return DSA_OK;
 }
 
@@ -446,11 +475,15 @@ extern "C" int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int hea
     if (!olat && !olat16 && !with_oabs) return DSA_OK;  // nothing requested
     const int sms = sm_count();
     if (sms <= 0) return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4: no CUDA device");
-    const F4Plan p = f4_plan(rows, heads, out_width, hidden, with_oabs, sms);
-    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+    const long long cache_rows = P.block_table ? P.num_blocks * P.block_size
+                                               : (long long)P.batch * P.max_seq_len;
+    const F4Plan p = f4_plan(f4_use_tc(heads, out_width, cache_rows), rows, heads, out_width,
+                             hidden, with_oabs, sms);
+    const size_t need = f4_bytes(rows, heads, out_width, hidden, with_oabs, sms);
+    if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(DSA_ERR_INVALID_ARG,
                     "dsa_sparse_mla_decode_fp4: workspace %zu B < %zu B needed", workspace_bytes,
-                    p.bytes);
+                    need);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     cudaStream_t st = (cudaStream_t)stream;
     // the projection reads a bf16 olat: the caller's where there is one
@@ -475,7 +508,8 @@ extern "C" int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int hea
     a.tps = p.tps;
     a.scale = softmax_scale;
     a.vscale = ldexpf(1.f, cache_exp);
-    rc = p.mt == 1 ? launch_split<1>(a, p, st) : launch_split<2>(a, p, st);
+    rc = p.tc ? mla_f4_tc_launch(a, st)
+              : p.mt == 1 ? launch_split<1>(a, p, st) : launch_split<2>(a, p, st);
     if (rc) return rc;
     if (p.ns > 1) {
         rc = mla_combine_launch(a.part_o, a.part_ml, rows, heads, p.ns, olat, x16, st);

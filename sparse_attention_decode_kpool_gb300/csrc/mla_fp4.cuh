@@ -28,6 +28,11 @@ struct MlaF4Args {
     float vscale;  // 2^cache_exp
 };
 
+// The tensor-core kernel (mla_fp4_tc.cu): out_width > 0, cache rows below 2^31, splits of
+// a multiple of mla_f4_tc_chunk() tokens.
+int mla_f4_tc_chunk();
+int mla_f4_tc_launch(const MlaF4Args& a, cudaStream_t st);
+
 // The cache row of selected position pos of row r (sequence seq, L tokens), or -1 where
 // there is none; bad ids and block entries are flagged.
 __device__ __forceinline__ long long f4_token(const MlaF4Args& a, int r, int seq, int L, int pos,

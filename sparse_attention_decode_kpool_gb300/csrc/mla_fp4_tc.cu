@@ -1,0 +1,552 @@
+// dsa_sparse_mla_decode_fp4 on the tensor cores (tcgen05): 64 heads at a time, a
+// persistent grid over (row, head group, split) units, 128 tokens per chunk.
+//
+//   S^T = V Q^T     M = 128 tokens, N = 64 heads, K = 512 latent columns
+//   O^T += V^T P^T  M = 512 latent columns (four tiles), N = 64 heads, K = 128 tokens
+//
+// V is the chunk's decoded rows in f16 (128 x 512, 128 KB of shared memory in 128-byte
+// swizzle atoms): one tile serves both products, K-major for the scores and MN-major for
+// the values. With Q (64 KB) and P (16 KB) there is no room for a second tile, nor for a
+// stage of undecoded rows; instead the next chunk's 288 bytes per token wait in registers
+// (20 of them in each of 512 threads), loaded a chunk ahead, so the tile's refill is
+// arithmetic and shared-memory stores only. It is refilled a quarter (128 columns) at a
+// time, as the value product of the chunk before leaves it, and the score product starts
+// on a quarter as soon as it is filled.
+//
+// Sixteen worker warps do everything but addresses and MMA issue; what they do in a chunk
+// follows from what is ready: decode the four quarters, request the next chunk's rows,
+// softmax. In the softmax warp w has tensor-memory lane quarter w & 3 (32 tokens) and
+// heads 16 (w >> 2) .. + 15. A head's running maximum is moved only when a score exceeds
+// it by more than kLazy (or there is none yet): one vote per chunk among the four warps
+// of a head group, and only after such a vote are maxima exchanged and O^T rescaled.
+// Weights are held at 2^kUp over the maximum, so with the lag they reach 2^15 in f16.
+//
+// Warps 16 and 18 resolve token ids to cache rows, chunks ahead; warp 17 issues the MMAs.
+//
+// Waits are bounded: one that runs out sets DSA_STATUS_TIMEOUT and a flag that makes all
+// later waits return at once; every role then runs its loops to the end (rows stay
+// checked ones), so named barriers stay matched, and the tensor memory is released.
+#include "mla_fp4.cuh"
+#include "tc.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr int kT = 128;  // tokens per chunk
+constexpr int kH = 64;   // heads per unit
+constexpr int kKVL = 512;
+constexpr int kAtoms = kKVL / 64;
+constexpr uint32_t kLatAtom = kT * 128;
+constexpr uint32_t kQAtom = kH * 128;
+constexpr int kRing = 4;  // chunks of resolved rows
+constexpr uint32_t kOffQ = 0;
+constexpr uint32_t kOffLat = kOffQ + kAtoms * kQAtom;
+constexpr uint32_t kOffP = kOffLat + kAtoms * kLatAtom;
+constexpr uint32_t kOffRows = kOffP + kT * 128;         // [kRing][kT] cache row, or -1
+constexpr uint32_t kOffRed = kOffRows + kRing * kT * 4;  // [4][kH] chunk maxima
+constexpr uint32_t kOffSums = kOffRed + 4 * kH * 4;      // [4][kH] head sums
+constexpr uint32_t kOffQmax = kOffSums + 4 * kH * 4;     // [16] per-warp maxima of |q|
+constexpr uint32_t kOffBar = kOffQmax + 16 * 4;
+constexpr int ROWS_FULL = 0;                    // [kRing]
+constexpr int ROWS_EMPTY = ROWS_FULL + kRing;   // [kRing]
+constexpr int LAT_FULL = ROWS_EMPTY + kRing;    // [4] quarter decoded
+constexpr int LAT_EMPTY = LAT_FULL + 4;         // [4] quarter's value product done
+constexpr int Q_FULL = LAT_EMPTY + 4;
+constexpr int S_FULL = Q_FULL + 1;
+constexpr int P_FULL = S_FULL + 1;
+constexpr int O_DONE = P_FULL + 1;
+constexpr int O_FREE = O_DONE + 1;
+constexpr int DRAIN = O_FREE + 1;
+constexpr int kBars = DRAIN + 1;
+constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+constexpr uint32_t kBytes = kOffMisc + 16;
+constexpr uint32_t kDyn = kBytes + 1024;
+static_assert(kDyn <= 227 * 1024, "shared memory");
+static_assert(kOffBar % 8 == 0 && kOffRows % 16 == 0, "alignment");
+constexpr uint32_t kTmemCols = 512;  // S^T: columns [0, 64); O^T tile i: [64 + 64 i, + 64)
+constexpr int kWorkers = 16;
+constexpr int kThreads = (kWorkers + 4) * 32;
+// Launched at 96 registers a thread (640 x 96 of the SM's 65,536); the four worker
+// warpgroups take 112 and the fifth 32: 4 x 112 + 32 = 5 x 96.
+constexpr int kRegLow = 32, kRegHigh = 112;
+static_assert(4 * kRegHigh + kRegLow <= 5 * 96, "register split");
+constexpr float kLazy = 8.f;
+constexpr float kUpTc = 7.f;  // weights reach 2^(kUpTc + kLazy) = 2^15
+
+// D f32, A and B f16.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// 16 consecutive f32 columns of this thread's lane, loaded and complete.
+__device__ __forceinline__ void tc_ld16(uint32_t (&v)[16], uint32_t taddr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
+          "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]),
+          "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+        "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ bool bar_any(int id, int threads, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\n"
+        "barrier.cta.red.or.pred q, %2, %3, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)p), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(addr), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Waits for a phase, for about a second at most; after a timeout (here or in another
+// role) it returns at once.
+__device__ __forceinline__ void wait_or_go(uint64_t* bar, uint32_t parity,
+                                           volatile int* abort_flag, int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_ns();
+    for (;;) {
+        if (*abort_flag) return;
+        if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
+        if (global_ns() - t0 > 1000000000ull) {
+            *abort_flag = 1;
+            flag_status(status, DSA_STATUS_TIMEOUT);
+            return;
+        }
+    }
+}
+
+struct Unit {
+    int r, hg, split, t_begin, t_end, nch;
+};
+__device__ __forceinline__ Unit unit_of(const MlaF4Args& a, int hgroups, int u) {
+    Unit w;
+    const int rh = u / a.ns;
+    w.split = u - rh * a.ns;
+    w.r = rh / hgroups;
+    w.hg = rh - w.r * hgroups;
+    w.t_begin = w.split * a.tps;
+    w.t_end = min(w.t_begin + a.tps, a.ow);
+    w.nch = (w.t_end - w.t_begin + kT - 1) / kT;
+    return w;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int hgroups, int units) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    volatile int* rows = reinterpret_cast<volatile int*>(smem + kOffRows);
+    float* red = reinterpret_cast<float*>(smem + kOffRed);
+    float* sums = reinterpret_cast<float*>(smem + kOffSums);
+    uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + kOffQmax);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < kRing; ++b) {
+            mbar_init(bars + ROWS_FULL + b, 1);
+            mbar_init(bars + ROWS_EMPTY + b, kWorkers);
+        }
+        for (int q = 0; q < 4; ++q) {
+            mbar_init(bars + LAT_FULL + q, kWorkers);
+            mbar_init(bars + LAT_EMPTY + q, 1);
+        }
+        mbar_init(bars + Q_FULL, kWorkers);
+        mbar_init(bars + S_FULL, 1);
+        mbar_init(bars + P_FULL, kWorkers);
+        mbar_init(bars + O_DONE, 1);
+        mbar_init(bars + O_FREE, kWorkers);
+        mbar_init(bars + DRAIN, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < kRing * kT; i += kThreads) rows[i] = -1;
+    if (warp == kWorkers + 1) tc_alloc(tmem_slot, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+
+    // one lane waits for its warp
+    auto wait = [&](int bar, uint32_t parity) {
+        if (lane == 0) wait_or_go(bars + bar, parity, abort_flag, a.status);
+        __syncwarp();
+    };
+    auto arrive = [&](int bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + bar);
+    };
+
+    if (warp < kWorkers) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegHigh));
+        const int qd = warp & 3, hb = (warp >> 2) * 16;  // lane quarter, first head
+        const int j = 32 * qd + lane;                    // softmax: this thread's token
+        const uint32_t lrow = (uint32_t)(32 * qd) << 16;
+        const int dj = 8 * warp + (lane & 7), dp = lane >> 3;  // decode: token, 32-column piece
+        const uint32_t drow = smem_u32(smem + kOffLat) + (dp >> 1) * kLatAtom + dj * 128;
+        const float NEG_INF = __int_as_float(0xff800000);
+
+        // This thread's part of a chunk's undecoded rows: per quarter k 16 bytes of codes
+        // (channels 128 k + 32 dp .. + 31) and their two scales.
+        uint4 code[4];
+        uint32_t scl[4];
+        auto request = [&](int n) {
+            const int row = rows[(n & (kRing - 1)) * kT + dj];
+            if (row >= 0) {
+                const uint8_t* c = a.codes + (long long)row * (kKVL / 2) + dp * 16;
+                const uint8_t* s = a.scales + (long long)row * (kKVL / kF4Block) + dp * 2;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    code[k] = ldg16(c + 64 * k);
+                    scl[k] = __ldg(reinterpret_cast<const uint16_t*>(s + 8 * k));
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    code[k] = make_uint4(0, 0, 0, 0);
+                    scl[k] = 0;
+                }
+            }
+        };
+
+        int n = 0, ku = 0;
+        if ((int)blockIdx.x < units) {
+            wait(ROWS_FULL, 0);
+            request(0);
+        }
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
+            const Unit w = unit_of(a, hgroups, u);
+            const int nh = min(kH, a.heads - w.hg * kH);
+            // ---- Q of the unit: f16, times 2^qe. The last unit's score products are
+            // complete (its last S^T was read), so the buffer is free.
+            int qe;
+            {
+                const uint16_t* qb = a.qlat + ((long long)w.r * a.heads + w.hg * kH) * kKVL;
+                uint4 v[8];
+                uint32_t m = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = threadIdx.x + 512 * k, h = i >> 6;
+                    v[k] = h < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[k].x), f4_finite_abs2(v[k].y)),
+                                             __vmaxu2(f4_finite_abs2(v[k].z), f4_finite_abs2(v[k].w))));
+                m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+                if (lane == 0) qmax[warp] = m;
+                bar_sync(1, kWorkers * 32);
+                m = qmax[lane & 15];
+                qe = f4_q_exp(__reduce_max_sync(0xffffffffu, m));
+                const float mul = pow2f(qe);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = threadIdx.x + 512 * k, h = i >> 6, c = i & 63;
+                    sts16(smem_u32(smem + kOffQ) + (c >> 3) * kQAtom + h * 128 +
+                              (((c & 7) ^ (h & 7)) << 4),
+                          make_uint4(f4_q_half2(v[k].x, mul), f4_q_half2(v[k].y, mul),
+                                     f4_q_half2(v[k].z, mul), f4_q_half2(v[k].w, mul)));
+                }
+                fence_async_smem();
+                arrive(Q_FULL);
+            }
+            const float sl2 = a.scale * kLog2e4 * a.vscale * pow2f(-qe);
+
+            float e[16], l[16];  // maximum less kUpTc, this lane's sum of weights, per head
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+                e[h] = NEG_INF;
+                l[h] = 0.f;
+            }
+            for (int c = 0; c < w.nch; ++c, ++n) {
+                // ---- decode, quarter by quarter
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    wait(LAT_EMPTY + k, (uint32_t)(n & 1) ^ 1u);
+                    const uint32_t s = e4m3x2_to_f16x2(scl[k]);
+                    const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+                    const uint32_t base = drow + 2 * k * kLatAtom;
+                    const int c0 = 4 * (dp & 1), x = dj & 7;
+                    sts16(base + (((c0 + 0) ^ x) << 4), fp4_decode8(code[k].x, s0));
+                    sts16(base + (((c0 + 1) ^ x) << 4), fp4_decode8(code[k].y, s0));
+                    sts16(base + (((c0 + 2) ^ x) << 4), fp4_decode8(code[k].z, s1));
+                    sts16(base + (((c0 + 3) ^ x) << 4), fp4_decode8(code[k].w, s1));
+                    fence_async_smem();
+                    arrive(LAT_FULL + k);
+                }
+                // ---- request the next chunk's rows (the next unit's first, at the end)
+                if (c + 1 < w.nch || u + (int)gridDim.x < units) {
+                    wait(ROWS_FULL + ((n + 1) & (kRing - 1)), (uint32_t)(((n + 1) / kRing) & 1));
+                    request(n + 1);
+                }
+                // ---- softmax
+                wait(S_FULL, (uint32_t)(n & 1));
+                tc_fence_after();
+                uint32_t sv[16];
+                tc_ld16(sv, tmem + lrow + hb);
+                const bool valid = rows[(n & (kRing - 1)) * kT + j] >= 0;
+                arrive(ROWS_EMPTY + (n & (kRing - 1)));
+                bool up = false;
+#pragma unroll
+                for (int h = 0; h < 16; ++h) {
+                    const float x = __uint_as_float(sv[h]) * sl2;
+                    sv[h] = __float_as_uint(x);
+                    up = up || x > e[h] + (kUpTc + kLazy);
+                }
+                if (bar_any(2 + (warp >> 2), 128, c == 0 || (up && valid))) {
+                    // move the maxima that a score of this chunk exceeds
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) {
+                        const float mx = warp_max(valid ? __uint_as_float(sv[h]) : NEG_INF);
+                        if (lane == 0) red[qd * kH + hb + h] = mx;
+                    }
+                    bar_sync(2 + (warp >> 2), 128);
+                    float f[16];
+                    bool resc = false;
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) {
+                        const float mx = fmaxf(fmaxf(red[hb + h], red[kH + hb + h]),
+                                               fmaxf(red[2 * kH + hb + h], red[3 * kH + hb + h])) -
+                                         kUpTc;
+                        const bool moved = mx > e[h] + kLazy;
+                        f[h] = moved ? ex2_sfu(e[h] - mx) : 1.f;
+                        e[h] = moved ? mx : e[h];
+                        l[h] *= f[h];
+                        resc = resc || moved;
+                    }
+                    if (resc && c > 0) {  // the chunk before's O^T is complete (S_FULL)
+#pragma unroll 1
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t v[16];
+                            const uint32_t addr = tmem + lrow + 64 + 64 * i + hb;
+                            tc_ld16(v, addr);
+#pragma unroll
+                            for (int h = 0; h < 16; ++h)
+                                v[h] = __float_as_uint(__uint_as_float(v[h]) * f[h]);
+                            tc_st16(addr, v);
+                        }
+                        tc_wait_st();
+                    }
+                }
+                {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p0 =
+                            valid ? ex2_sfu(__uint_as_float(sv[2 * i]) - e[2 * i]) : 0.f;
+                        const float p1 =
+                            valid ? ex2_sfu(__uint_as_float(sv[2 * i + 1]) - e[2 * i + 1]) : 0.f;
+                        l[2 * i] += p0;
+                        l[2 * i + 1] += p1;
+                        pk[i] = half2_bits(p0, p1);
+                    }
+                    const uint32_t prow = smem_u32(smem + kOffP) + j * 128;
+                    const int c0 = hb >> 3, x = j & 7;
+                    sts16(prow + ((c0 ^ x) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+                    sts16(prow + (((c0 + 1) ^ x) << 4), make_uint4(pk[4], pk[5], pk[6], pk[7]));
+                }
+                fence_async_smem();
+                tc_fence_before();
+                arrive(P_FULL);
+            }
+
+            // ---- epilogue: head sums over the lanes, then over the four lane quarters
+#pragma unroll
+            for (int ww = 8, m = 16; ww >= 1; ww >>= 1, m >>= 1) {
+#pragma unroll
+                for (int i = 0; i < ww; ++i) {
+                    const bool hi = (lane & m) != 0;
+                    const float send = hi ? l[i] : l[ww + i];
+                    const float recv = __shfl_xor_sync(0xffffffffu, send, m);
+                    l[i] = (hi ? l[ww + i] : l[i]) + recv;
+                }
+            }
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);  // head hb + lane / 2
+            if ((lane & 1) == 0) sums[qd * kH + hb + (lane >> 1)] = l[0];
+            bar_sync(2 + (warp >> 2), 128);
+            float k[16];  // what each head's accumulators are multiplied by
+#pragma unroll
+            for (int h = 0; h < 16; ++h) {
+                const float s = (sums[hb + h] + sums[kH + hb + h]) +
+                                (sums[2 * kH + hb + h] + sums[3 * kH + hb + h]);
+                // a NaN sum keeps its NaN
+                k[h] = a.ns > 1 ? a.vscale : (s == 0.f ? 0.f : __fdividef(a.vscale, s));
+                if (a.ns > 1 && qd == 0 && lane == h && hb + h < nh) {
+                    const long long p =
+                        ((long long)w.r * a.ns + w.split) * a.heads + w.hg * kH + hb + h;
+                    *reinterpret_cast<float2*>(a.part_ml + p * 2) =
+                        make_float2(e[h] + kUpTc, s * exp2f(-kUpTc));
+                }
+            }
+            wait(O_DONE, (uint32_t)(ku & 1));
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[16];
+                tc_ld16(v, tmem + lrow + 64 + 64 * i + hb);
+                const int col = 128 * i + j;
+                if (a.ns > 1) {
+                    float* o = a.part_o + (((long long)w.r * a.ns + w.split) * a.heads +
+                                           w.hg * kH + hb) * kKVL + col;
+#pragma unroll
+                    for (int h = 0; h < 16; ++h)
+                        if (hb + h < nh)
+                            o[h * kKVL] = __uint_as_float(v[h]) * (k[h] * exp2f(-kUpTc));
+                } else {
+                    const long long o = ((long long)w.r * a.heads + w.hg * kH + hb) * kKVL + col;
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) {
+                        const float x = __uint_as_float(v[h]) * k[h];
+                        if (hb + h < nh) {
+                            if (a.olat) a.olat[o + h * kKVL] = x;
+                            if (a.olat16)
+                                a.olat16[o + h * kKVL] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            arrive(O_FREE);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegLow));
+        if (warp == kWorkers + 1) {
+            // ---- MMA issue
+            if (lane == 0) {
+                constexpr uint32_t IDESC_QK = idesc_f16(kT, kH);
+                constexpr uint32_t IDESC_PV = idesc_f16(128, kH) | (1u << 15) | (1u << 16);
+                const uint32_t q0 = smem_u32(smem + kOffQ), l0 = smem_u32(smem + kOffLat),
+                               p0 = smem_u32(smem + kOffP);
+                auto wait1 = [&](int bar, uint32_t parity) {
+                    wait_or_go(bars + bar, parity, abort_flag, a.status);
+                };
+                int n = 0, ku = 0;
+                for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
+                    const Unit w = unit_of(a, hgroups, u);
+                    wait1(Q_FULL, (uint32_t)(ku & 1));
+                    for (int c = 0; c < w.nch; ++c, ++n) {
+                        for (int q = 0; q < 4; ++q) {
+                            wait1(LAT_FULL + q, (uint32_t)(n & 1));
+                            tc_fence_after();
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int at = 2 * q + h;
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma(tmem, sw128_desc(l0 + at * kLatAtom + 32 * kk),
+                                           sw128_desc(q0 + at * kQAtom + 32 * kk), IDESC_QK,
+                                           (at | kk) != 0 ? 1u : 0u);
+                            }
+                        }
+                        tc_commit(bars + S_FULL);
+                        wait1(P_FULL, (uint32_t)(n & 1));
+                        if (c == 0 && ku > 0) wait1(O_FREE, (uint32_t)((ku - 1) & 1));
+                        tc_fence_after();
+                        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                            for (int kk = 0; kk < kT / 16; ++kk)
+                                tc_mma(tmem + 64 + 64 * i,
+                                       sw128_desc_mn(l0 + 2 * i * kLatAtom + kk * 2048, kLatAtom,
+                                                     1024),
+                                       sw128_desc_mn(p0 + kk * 2048, kQAtom, 1024), IDESC_PV,
+                                       (c > 0 || kk > 0) ? 1u : 0u);
+                            tc_commit(bars + LAT_EMPTY + i);
+                        }
+                        if (c == w.nch - 1) tc_commit(bars + O_DONE);
+                    }
+                }
+                // every MMA issued has completed before tensor memory is released
+                tc_commit(bars + DRAIN);
+                mbar_wait(bars + DRAIN, 0);
+            }
+        } else if (warp != kWorkers + 3) {
+            // ---- cache rows: warps 16 and 18 take every other chunk
+            const int mine = warp == kWorkers ? 0 : 1;
+            int n = 0;
+            for (int u = blockIdx.x; u < units; u += gridDim.x) {
+                const Unit w = unit_of(a, hgroups, u);
+                int seq = a.row_seq ? __ldg(a.row_seq + w.r) : w.r;
+                int L = 0;
+                if (seq >= 0 && seq < a.pg.batch) {
+                    L = min(__ldg(a.pg.seq_lens + seq), seq_capacity(a.pg));
+                } else {
+                    if (lane == 0) flag_status(a.status, DSA_STATUS_BAD_TOKEN);
+                    seq = 0;
+                }
+                for (int c = 0; c < w.nch; ++c, ++n) {
+                    if ((n & 1) != mine) continue;
+                    const int b = n & (kRing - 1);
+                    int prow[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        prow[k] = (int)f4_token(a, w.r, seq, L, w.t_begin + c * kT + 32 * k + lane,
+                                                w.t_end);
+                    wait(ROWS_EMPTY + b, (uint32_t)((n / kRing) & 1) ^ 1u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) rows[b * kT + 32 * k + lane] = prow[k];
+                    arrive(ROWS_FULL + b);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWorkers + 1) {
+        tc_fence_after();
+        tc_dealloc(tmem, kTmemCols);
+    }
+}
+
+}  // namespace
+
+int mla_f4_tc_chunk() { return kT; }
+
+int mla_f4_tc_launch(const MlaF4Args& a, cudaStream_t st) {
+    const int sms = sm_count();
+    if (sms <= 0) return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4: no CUDA device");
+    const int hgroups = (a.heads + kH - 1) / kH;
+    const long long units = (long long)a.rows * hgroups * a.ns;
+    if (units > 0x7fffffffLL - sms)
+        return fail(DSA_ERR_UNSUPPORTED, "dsa_sparse_mla_decode_fp4: too many rows");
+    int rc = set_max_smem((const void*)mla_f4_tc_kernel, (int)kDyn);
+    if (rc) return rc;
+    // setmaxnreg's split adds up to 96 registers a thread: with fewer at launch its raise
+    // would wait for ever
+    static const int regs = [] {
+        cudaFuncAttributes at;
+        return cudaFuncGetAttributes(&at, mla_f4_tc_kernel) == cudaSuccess ? at.numRegs : 0;
+    }();
+    if (regs < 96)
+        return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4: built at %d registers", regs);
+    cudaError_t e = launch_pdl(mla_f4_tc_kernel, dim3((unsigned)(units < sms ? units : sms)),
+                               dim3(kThreads), kDyn, st, a, hgroups, (int)units);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_sparse_mla_decode_fp4 tensor-core launch");
+    return DSA_OK;
+}
+
+}  // namespace dsa

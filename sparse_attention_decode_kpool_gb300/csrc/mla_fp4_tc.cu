@@ -67,12 +67,14 @@ constexpr uint32_t kTmemCols = 512;  // S^T: columns [0, 64); O^T tile i: [64 + 
 constexpr int kWorkers = 16;
 constexpr int kThreads = (kWorkers + 4) * 32;
 // Launched at 96 registers a thread (640 x 96 of the SM's 65,536); the four worker
-// warpgroups take 112 and the fifth 32: 4 x 112 + 32 = 5 x 96.
-constexpr int kRegLow = 32, kRegHigh = 112;
+// warpgroups take 104 and the fifth 64: 4 x 104 + 64 = 5 x 96.
+constexpr int kRegLow = 64, kRegHigh = 104;
 static_assert(4 * kRegHigh + kRegLow <= 5 * 96, "register split");
 constexpr float kLazy = 8.f;
 constexpr float kUpTc = 7.f;  // weights reach 2^(kUpTc + kLazy) = 2^15
 
+// The descriptor `bytes` further on (an operand's next 16 columns or rows).
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) { return d + (bytes >> 4); }
 // D f32, A and B f16.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -120,16 +122,36 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// Waits for a phase, for about a second at most; after a timeout (here or in another
-// role) it returns at once.
-__device__ __forceinline__ void wait_or_go(uint64_t* bar, uint32_t parity,
-                                           volatile int* abort_flag, int32_t* status) {
-    if (mbar_try_wait(bar, parity)) return;
+// MMA and commit by one elected lane of a converged warp (always the same one). The whole
+// warp runs the issue loop, so descriptors and loop counters stay in uniform registers,
+// where tcgen05.mma takes them; with one lane in the loop each was moved there again and
+// an issue took about 100 cycles instead of 60.
+__device__ __forceinline__ void warp_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p, e;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %4, 0;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+// A warp waits for a phase, for about a second at most; after a timeout (here or in another
+// role) it returns at once. The whole warp waits and stays converged: with one lane
+// waiting for the others the warp came out in two parts, and each decoded by itself.
+__device__ __forceinline__ void warp_wait_or_go(uint64_t* bar, uint32_t parity,
+                                                volatile int* abort_flag, int32_t* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return;
     const uint64_t t0 = global_ns();
     for (;;) {
-        if (*abort_flag) return;
-        if (mbar_try_wait_sleep(bar, parity, 20000u)) return;
-        if (global_ns() - t0 > 1000000000ull) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) return;
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, 20000u))) return;
+        if (__any_sync(0xffffffffu, global_ns() - t0 > 1000000000ull)) {
             *abort_flag = 1;
             flag_status(status, DSA_STATUS_TIMEOUT);
             return;
@@ -162,7 +184,9 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the same in every lane of a warp, which the shuffle shows to the compiler
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);
+    const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < kRing; ++b) {
@@ -190,10 +214,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
     const uint32_t tmem = *tmem_slot;
     pdl_wait();
 
-    // one lane waits for its warp
     auto wait = [&](int bar, uint32_t parity) {
-        if (lane == 0) wait_or_go(bars + bar, parity, abort_flag, a.status);
-        __syncwarp();
+        warp_wait_or_go(bars + bar, parity, abort_flag, a.status);
     };
     auto arrive = [&](int bar) {
         __syncwarp();
@@ -205,30 +227,30 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
         const int qd = warp & 3, hb = (warp >> 2) * 16;  // lane quarter, first head
         const int j = 32 * qd + lane;                    // softmax: this thread's token
         const uint32_t lrow = (uint32_t)(32 * qd) << 16;
-        const int dj = 8 * warp + (lane & 7), dp = lane >> 3;  // decode: token, 32-column piece
+        // decode: token dj, 32-column piece dp of each quarter (four lanes share a token, so a
+        // quarter of a warp's 16-byte loads covers two lines of 64 bytes; eight lanes on
+        // eight tokens cost four times the L1 cycles, which the MMAs' operand reads lose)
+        const int dj = 8 * warp + (lane >> 2), dp = lane & 3;
         const uint32_t drow = smem_u32(smem + kOffLat) + (dp >> 1) * kLatAtom + dj * 128;
         const float NEG_INF = __int_as_float(0xff800000);
 
         // This thread's part of a chunk's undecoded rows: per quarter k 16 bytes of codes
-        // (channels 128 k + 32 dp .. + 31) and their two scales.
+        // (channels 128 k + 32 dp .. + 31), and the eight scales of channels 128 dp .. + 127
+        // (quarter dp; the token's four lanes exchange them at the decode).
         uint4 code[4];
-        uint32_t scl[4];
+        uint2 scl;
         auto request = [&](int n) {
             const int row = rows[(n & (kRing - 1)) * kT + dj];
             if (row >= 0) {
                 const uint8_t* c = a.codes + (long long)row * (kKVL / 2) + dp * 16;
-                const uint8_t* s = a.scales + (long long)row * (kKVL / kF4Block) + dp * 2;
+                const uint8_t* s = a.scales + (long long)row * (kKVL / kF4Block) + dp * 8;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    code[k] = ldg16(c + 64 * k);
-                    scl[k] = __ldg(reinterpret_cast<const uint16_t*>(s + 8 * k));
-                }
+                for (int k = 0; k < 4; ++k) code[k] = ldg16(c + 64 * k);
+                scl = __ldg(reinterpret_cast<const uint2*>(s));
             } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    code[k] = make_uint4(0, 0, 0, 0);
-                    scl[k] = 0;
-                }
+                for (int k = 0; k < 4; ++k) code[k] = make_uint4(0, 0, 0, 0);
+                scl = make_uint2(0, 0);
             }
         };
 
@@ -282,18 +304,35 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                 l[h] = 0.f;
             }
             for (int c = 0; c < w.nch; ++c, ++n) {
-                // ---- decode, quarter by quarter
+                // ---- decode, quarter by quarter. First the token's scales: lane dp holds the
+                // four 16-bit pairs of quarter dp and needs pair dp of every quarter (a 4 x 4
+                // transpose in two exchanges): ev = quarters 0 and 2, od = 1 and 3.
+                uint32_t ev, od;
+                {
+                    const bool hi = (dp & 2) != 0, odd = (dp & 1) != 0;
+                    const uint32_t r = __shfl_xor_sync(0xffffffffu, hi ? scl.x : scl.y, 2);
+                    const uint32_t x = hi ? r : scl.x, y = hi ? scl.y : r;
+                    const uint32_t lo2 = __byte_perm(x, y, 0x5410), hi2 = __byte_perm(x, y, 0x7632);
+                    const uint32_t t = __shfl_xor_sync(0xffffffffu, odd ? lo2 : hi2, 1);
+                    ev = odd ? t : lo2;
+                    od = odd ? hi2 : t;
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     wait(LAT_EMPTY + k, (uint32_t)(n & 1) ^ 1u);
-                    const uint32_t s = e4m3x2_to_f16x2(scl[k]);
+                    const uint32_t s = e4m3x2_to_f16x2(((k & 1) ? od : ev) >> (8 * (k & 2)));
                     const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
+                    // lanes 2 and 3 of a token store their blocks in the other order: the
+                    // eight lanes of a store then hit eight different 16-byte columns
+                    const uint4 cw = (dp & 2) ? make_uint4(code[k].z, code[k].w, code[k].x, code[k].y)
+                                              : code[k];
+                    const uint32_t sa = (dp & 2) ? s1 : s0, sb = (dp & 2) ? s0 : s1;
                     const uint32_t base = drow + 2 * k * kLatAtom;
-                    const int c0 = 4 * (dp & 1), x = dj & 7;
-                    sts16(base + (((c0 + 0) ^ x) << 4), fp4_decode8(code[k].x, s0));
-                    sts16(base + (((c0 + 1) ^ x) << 4), fp4_decode8(code[k].y, s0));
-                    sts16(base + (((c0 + 2) ^ x) << 4), fp4_decode8(code[k].z, s1));
-                    sts16(base + (((c0 + 3) ^ x) << 4), fp4_decode8(code[k].w, s1));
+                    const int c0 = 4 * (dp & 1) + (dp & 2), x = dj & 7;
+                    sts16(base + ((c0 ^ x) << 4), fp4_decode8(cw.x, sa));
+                    sts16(base + (((c0 + 1) ^ x) << 4), fp4_decode8(cw.y, sa));
+                    sts16(base + (((c0 ^ 2) ^ x) << 4), fp4_decode8(cw.z, sb));
+                    sts16(base + ((((c0 ^ 2) + 1) ^ x) << 4), fp4_decode8(cw.w, sb));
                     fence_async_smem();
                     arrive(LAT_FULL + k);
                 }
@@ -435,53 +474,52 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegLow));
         if (warp == kWorkers + 1) {
             // ---- MMA issue
-            if (lane == 0) {
-                constexpr uint32_t IDESC_QK = idesc_f16(kT, kH);
-                constexpr uint32_t IDESC_PV = idesc_f16(128, kH) | (1u << 15) | (1u << 16);
-                const uint32_t q0 = smem_u32(smem + kOffQ), l0 = smem_u32(smem + kOffLat),
-                               p0 = smem_u32(smem + kOffP);
-                auto wait1 = [&](int bar, uint32_t parity) {
-                    wait_or_go(bars + bar, parity, abort_flag, a.status);
-                };
-                int n = 0, ku = 0;
-                for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
-                    const Unit w = unit_of(a, hgroups, u);
-                    wait1(Q_FULL, (uint32_t)(ku & 1));
-                    for (int c = 0; c < w.nch; ++c, ++n) {
-                        for (int q = 0; q < 4; ++q) {
-                            wait1(LAT_FULL + q, (uint32_t)(n & 1));
+            constexpr uint32_t IDESC_QK = idesc_f16(kT, kH);
+            constexpr uint32_t IDESC_PV = idesc_f16(128, kH) | (1u << 15) | (1u << 16);
+            // Loops, not straight-line code: this warp's few instructions then stay in the
+            // instruction cache beside the workers' many. Shared memory ends below 2^18
+            // bytes, so stepping a descriptor's address never carries out of its field.
+            const uint64_t q0 = sw128_desc(smem_u32(smem + kOffQ));
+            const uint64_t k0 = sw128_desc(smem_u32(smem + kOffLat));
+            const uint64_t v0 = sw128_desc_mn(smem_u32(smem + kOffLat), kLatAtom, 1024);
+            const uint64_t p0 = sw128_desc_mn(smem_u32(smem + kOffP), kQAtom, 1024);
+            int n = 0, ku = 0;
+            for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
+                const Unit w = unit_of(a, hgroups, u);
+                wait(Q_FULL, (uint32_t)(ku & 1));
+                for (int c = 0; c < w.nch; ++c, ++n) {
+#pragma unroll 1
+                    for (int at = 0; at < kAtoms; ++at) {
+                        if ((at & 1) == 0) {
+                            wait(LAT_FULL + (at >> 1), (uint32_t)(n & 1));
                             tc_fence_after();
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const int at = 2 * q + h;
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    tc_mma(tmem, sw128_desc(l0 + at * kLatAtom + 32 * kk),
-                                           sw128_desc(q0 + at * kQAtom + 32 * kk), IDESC_QK,
-                                           (at | kk) != 0 ? 1u : 0u);
-                            }
                         }
-                        tc_commit(bars + S_FULL);
-                        wait1(P_FULL, (uint32_t)(n & 1));
-                        if (c == 0 && ku > 0) wait1(O_FREE, (uint32_t)((ku - 1) & 1));
-                        tc_fence_after();
-                        for (int i = 0; i < 4; ++i) {
+                        const uint64_t ka = desc_at(k0, at * kLatAtom);
+                        const uint64_t qa = desc_at(q0, at * kQAtom);
 #pragma unroll
-                            for (int kk = 0; kk < kT / 16; ++kk)
-                                tc_mma(tmem + 64 + 64 * i,
-                                       sw128_desc_mn(l0 + 2 * i * kLatAtom + kk * 2048, kLatAtom,
-                                                     1024),
-                                       sw128_desc_mn(p0 + kk * 2048, kQAtom, 1024), IDESC_PV,
-                                       (c > 0 || kk > 0) ? 1u : 0u);
-                            tc_commit(bars + LAT_EMPTY + i);
-                        }
-                        if (c == w.nch - 1) tc_commit(bars + O_DONE);
+                        for (int kk = 0; kk < 4; ++kk)
+                            warp_mma(tmem, desc_at(ka, 32 * kk), desc_at(qa, 32 * kk), IDESC_QK,
+                                     (at | kk) != 0 ? 1u : 0u);
                     }
+                    warp_commit(bars + S_FULL);
+                    wait(P_FULL, (uint32_t)(n & 1));
+                    if (c == 0 && ku > 0) wait(O_FREE, (uint32_t)((ku - 1) & 1));
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        const uint64_t vi = desc_at(v0, 2 * i * kLatAtom);
+#pragma unroll
+                        for (int kk = 0; kk < kT / 16; ++kk)
+                            warp_mma(tmem + 64 + 64 * i, desc_at(vi, kk * 2048),
+                                     desc_at(p0, kk * 2048), IDESC_PV, (c > 0 || kk > 0) ? 1u : 0u);
+                        warp_commit(bars + LAT_EMPTY + i);
+                    }
+                    if (c == w.nch - 1) warp_commit(bars + O_DONE);
                 }
-                // every MMA issued has completed before tensor memory is released
-                tc_commit(bars + DRAIN);
-                mbar_wait(bars + DRAIN, 0);
             }
+            // every MMA issued has completed before tensor memory is released
+            warp_commit(bars + DRAIN);
+            if (lane == 0) mbar_wait(bars + DRAIN, 0);
         } else if (warp != kWorkers + 3) {
             // ---- cache rows: warps 16 and 18 take every other chunk
             const int mine = warp == kWorkers ? 0 : 1;

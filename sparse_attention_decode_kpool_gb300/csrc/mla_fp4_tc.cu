@@ -267,30 +267,31 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
             int qe;
             {
                 const uint16_t* qb = a.qlat + ((long long)w.r * a.heads + w.hg * kH) * kKVL;
-                uint4 v[8];
                 uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int i = threadIdx.x + 512 * k, h = i >> 6;
-                    v[k] = h < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
+                    const int i = threadIdx.x + 512 * k;
+                    if ((i >> 6) < nh) {
+                        const uint4 v = ldg16(qb + (long long)i * 8);
+                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v.x), f4_finite_abs2(v.y)),
+                                                 __vmaxu2(f4_finite_abs2(v.z), f4_finite_abs2(v.w))));
+                    }
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[k].x), f4_finite_abs2(v[k].y)),
-                                             __vmaxu2(f4_finite_abs2(v[k].z), f4_finite_abs2(v[k].w))));
                 m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
                 if (lane == 0) qmax[warp] = m;
                 bar_sync(1, kWorkers * 32);
                 m = qmax[lane & 15];
                 qe = f4_q_exp(__reduce_max_sync(0xffffffffu, m));
                 const float mul = pow2f(qe);
-#pragma unroll
+                // read again (from L2) rather than held across the exchange in registers
+#pragma unroll 4
                 for (int k = 0; k < 8; ++k) {
                     const int i = threadIdx.x + 512 * k, h = i >> 6, c = i & 63;
+                    const uint4 v = h < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
                     sts16(smem_u32(smem + kOffQ) + (c >> 3) * kQAtom + h * 128 +
                               (((c & 7) ^ (h & 7)) << 4),
-                          make_uint4(f4_q_half2(v[k].x, mul), f4_q_half2(v[k].y, mul),
-                                     f4_q_half2(v[k].z, mul), f4_q_half2(v[k].w, mul)));
+                          make_uint4(f4_q_half2(v.x, mul), f4_q_half2(v.y, mul),
+                                     f4_q_half2(v.z, mul), f4_q_half2(v.w, mul)));
                 }
                 fence_async_smem();
                 arrive(Q_FULL);
@@ -319,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    wait(LAT_EMPTY + k, (uint32_t)(n & 1) ^ 1u);
                     const uint32_t s = e4m3x2_to_f16x2(((k & 1) ? od : ev) >> (8 * (k & 2)));
                     const uint32_t s0 = __byte_perm(s, s, 0x1010), s1 = __byte_perm(s, s, 0x3232);
                     // lanes 2 and 3 of a token store their blocks in the other order: the
@@ -327,12 +327,16 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     const uint4 cw = (dp & 2) ? make_uint4(code[k].z, code[k].w, code[k].x, code[k].y)
                                               : code[k];
                     const uint32_t sa = (dp & 2) ? s1 : s0, sb = (dp & 2) ? s0 : s1;
+                    const uint4 d0 = fp4_decode8(cw.x, sa), d1 = fp4_decode8(cw.y, sa),
+                                d2 = fp4_decode8(cw.z, sb), d3 = fp4_decode8(cw.w, sb);
+                    // decoded before the wait: the product that frees the quarter still runs
+                    wait(LAT_EMPTY + k, (uint32_t)(n & 1) ^ 1u);
                     const uint32_t base = drow + 2 * k * kLatAtom;
                     const int c0 = 4 * (dp & 1) + (dp & 2), x = dj & 7;
-                    sts16(base + ((c0 ^ x) << 4), fp4_decode8(cw.x, sa));
-                    sts16(base + (((c0 + 1) ^ x) << 4), fp4_decode8(cw.y, sa));
-                    sts16(base + (((c0 ^ 2) ^ x) << 4), fp4_decode8(cw.z, sb));
-                    sts16(base + ((((c0 ^ 2) + 1) ^ x) << 4), fp4_decode8(cw.w, sb));
+                    sts16(base + ((c0 ^ x) << 4), d0);
+                    sts16(base + (((c0 + 1) ^ x) << 4), d1);
+                    sts16(base + (((c0 ^ 2) ^ x) << 4), d2);
+                    sts16(base + ((((c0 ^ 2) + 1) ^ x) << 4), d3);
                     fence_async_smem();
                     arrive(LAT_FULL + k);
                 }
@@ -342,24 +346,51 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     request(n + 1);
                 }
                 // ---- softmax
+                const int rb = n & (kRing - 1);
+                const bool valid = rows[rb * kT + j] >= 0;
+                const uint32_t prow = smem_u32(smem + kOffP) + j * 128;
+                const uint32_t pc0 = prow + (((hb >> 3) ^ (j & 7)) << 4);
+                const uint32_t pc1 = prow + ((((hb >> 3) + 1) ^ (j & 7)) << 4);
+                uint32_t sv[16];  // scores, then weights, of heads hb .. hb + 15
+                // weights 2^(score - maximum + kUpTc) of this thread's token into its row of P
+                auto weights = [&]() {
+                    uint32_t pk[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float p0 = ex2_sfu(__uint_as_float(sv[2 * i]));
+                        const float p1 = ex2_sfu(__uint_as_float(sv[2 * i + 1]));
+                        sv[2 * i] = __float_as_uint(p0);
+                        sv[2 * i + 1] = __float_as_uint(p1);
+                        pk[i] = valid ? half2_bits(p0, p1) : 0u;
+                    }
+                    sts16(pc0, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+                    sts16(pc1, make_uint4(pk[4], pk[5], pk[6], pk[7]));
+                    fence_async_smem();
+                };
                 wait(S_FULL, (uint32_t)(n & 1));
                 tc_fence_after();
-                uint32_t sv[16];
                 tc_ld16(sv, tmem + lrow + hb);
-                const bool valid = rows[(n & (kRing - 1)) * kT + j] >= 0;
-                arrive(ROWS_EMPTY + (n & (kRing - 1)));
-                bool up = false;
-#pragma unroll
-                for (int h = 0; h < 16; ++h) {
-                    const float x = __uint_as_float(sv[h]) * sl2;
-                    sv[h] = __float_as_uint(x);
-                    up = up || x > e[h] + (kUpTc + kLazy);
-                }
-                if (bar_any(2 + (warp >> 2), 128, c == 0 || (up && valid))) {
-                    // move the maxima that a score of this chunk exceeds
+                bool moving = c == 0;
+                if (!moving) {
+                    // With the maxima as they are; the vote on whether they may stay comes
+                    // when the weights are stored, so that it does not delay them.
+                    float top = NEG_INF;
 #pragma unroll
                     for (int h = 0; h < 16; ++h) {
-                        const float mx = warp_max(valid ? __uint_as_float(sv[h]) : NEG_INF);
+                        const float y = fmaf(__uint_as_float(sv[h]), sl2, -e[h]);
+                        sv[h] = __float_as_uint(y);
+                        top = fmaxf(top, y);
+                    }
+                    weights();
+                    moving = bar_any(2 + (warp >> 2), 128, valid && top > kUpTc + kLazy);
+                    if (moving) tc_ld16(sv, tmem + lrow + hb);
+                }
+                if (moving) {
+                    // move the maxima that a score of this chunk exceeds by more than kLazy
+#pragma unroll
+                    for (int h = 0; h < 16; ++h) {
+                        const float mx =
+                            warp_max(valid ? __uint_as_float(sv[h]) * sl2 : NEG_INF);
                         if (lane == 0) red[qd * kH + hb + h] = mx;
                     }
                     bar_sync(2 + (warp >> 2), 128);
@@ -389,27 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                         }
                         tc_wait_st();
                     }
-                }
-                {
-                    uint32_t pk[8];
+                    tc_ld16(sv, tmem + lrow + hb);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float p0 =
-                            valid ? ex2_sfu(__uint_as_float(sv[2 * i]) - e[2 * i]) : 0.f;
-                        const float p1 =
-                            valid ? ex2_sfu(__uint_as_float(sv[2 * i + 1]) - e[2 * i + 1]) : 0.f;
-                        l[2 * i] += p0;
-                        l[2 * i + 1] += p1;
-                        pk[i] = half2_bits(p0, p1);
-                    }
-                    const uint32_t prow = smem_u32(smem + kOffP) + j * 128;
-                    const int c0 = hb >> 3, x = j & 7;
-                    sts16(prow + ((c0 ^ x) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
-                    sts16(prow + (((c0 + 1) ^ x) << 4), make_uint4(pk[4], pk[5], pk[6], pk[7]));
+                    for (int h = 0; h < 16; ++h)
+                        sv[h] = __float_as_uint(fmaf(__uint_as_float(sv[h]), sl2, -e[h]));
+                    weights();
                 }
-                fence_async_smem();
                 tc_fence_before();
                 arrive(P_FULL);
+                if (lane == 0) mbar_arrive(bars + ROWS_EMPTY + rb);
+#pragma unroll
+                for (int h = 0; h < 16; ++h) l[h] += valid ? __uint_as_float(sv[h]) : 0.f;
             }
 
             // ---- epilogue: head sums over the lanes, then over the four lane quarters

@@ -45,7 +45,8 @@ constexpr uint32_t kOffP = kOffLat + kAtoms * kLatAtom;
 constexpr uint32_t kOffRows = kOffP + kT * 128;         // [kRing][kT] cache row, or -1
 constexpr uint32_t kOffRed = kOffRows + kRing * kT * 4;  // [4][kH] chunk maxima
 constexpr uint32_t kOffSums = kOffRed + 4 * kH * 4;      // [4][kH] head sums
-constexpr uint32_t kOffQmax = kOffSums + 4 * kH * 4;     // [16] per-warp maxima of |q|
+constexpr uint32_t kOffK = kOffSums + 4 * kH * 4;        // [kH] factors of the output
+constexpr uint32_t kOffQmax = kOffK + kH * 4;            // [16] per-warp maxima of |q|
 constexpr uint32_t kOffBar = kOffQmax + 16 * 4;
 constexpr int ROWS_FULL = 0;                    // [kRing]
 constexpr int ROWS_EMPTY = ROWS_FULL + kRing;   // [kRing]
@@ -99,6 +100,24 @@ __device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&v)[16])
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
         "r"(v[15])
         : "memory");
+}
+// Reduce-scatter of 16 values over a warp: lane l ends with op over all lanes of value
+// l / 2.
+template <typename Op>
+__device__ __forceinline__ float scatter16(float (&v)[16], int lane, Op op) {
+#pragma unroll
+    for (int w = 8, m = 16; w >= 1; w >>= 1, m >>= 1) {
+        const bool hi = (lane & m) != 0;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float got = __shfl_xor_sync(0xffffffffu, hi ? v[i] : v[w + i], m);
+            v[i] = op(hi ? v[w + i] : v[i], got);
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p));
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
     asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
@@ -164,9 +183,9 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_of(const MlaF4Args& a, int hgroups, int u) {
     Unit w;
-    const int rh = u / a.ns;
+    const int rh = a.ns == 1 ? u : u / a.ns;
     w.split = u - rh * a.ns;
-    w.r = rh / hgroups;
+    w.r = hgroups == 1 ? rh : rh / hgroups;
     w.hg = rh - w.r * hgroups;
     w.t_begin = w.split * a.tps;
     w.t_end = min(w.t_begin + a.tps, a.ow);
@@ -180,6 +199,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
     volatile int* rows = reinterpret_cast<volatile int*>(smem + kOffRows);
     float* red = reinterpret_cast<float*>(smem + kOffRed);
     float* sums = reinterpret_cast<float*>(smem + kOffSums);
+    float* kout = reinterpret_cast<float*>(smem + kOffK);
     uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + kOffQmax);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -254,49 +274,93 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
             }
         };
 
+        // O^T of a unit, times its heads' factors, to the output or the split's partials
+        auto write_out = [&](const Unit& w, int k) {
+            const int nh = min(kH, a.heads - w.hg * kH);
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 x = *reinterpret_cast<const float4*>(kout + hb + 4 * i);
+                f[4 * i] = x.x, f[4 * i + 1] = x.y, f[4 * i + 2] = x.z, f[4 * i + 3] = x.w;
+            }
+            wait(O_DONE, (uint32_t)(k & 1));
+            tc_fence_after();
+            const long long head = a.ns > 1 ? ((long long)w.r * a.ns + w.split) * a.heads
+                                            : (long long)w.r * a.heads;
+            const long long o0 = (head + w.hg * kH + hb) * kKVL + j;
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[16];
+                tc_ld16(v, tmem + lrow + 64 + 64 * i + hb);
+                float* o32 = (a.ns > 1 ? a.part_o : a.olat) + o0 + 128 * i;
+                uint16_t* o16 = a.olat16 + o0 + 128 * i;
+                if (a.ns > 1 || a.olat) {
+#pragma unroll
+                    for (int h = 0; h < 16; ++h)
+                        if (hb + h < nh) o32[h * kKVL] = __uint_as_float(v[h]) * f[h];
+                }
+                if (a.ns == 1 && a.olat16) {
+#pragma unroll
+                    for (int h = 0; h < 16; ++h)
+                        if (hb + h < nh)
+                            o16[h * kKVL] = __bfloat16_as_ushort(
+                                __float2bfloat16_rn(__uint_as_float(v[h]) * f[h]));
+                }
+            }
+            tc_fence_before();
+            arrive(O_FREE);
+        };
+
         int n = 0, ku = 0;
         if ((int)blockIdx.x < units) {
             wait(ROWS_FULL, 0);
             request(0);
         }
+        Unit prev = {};
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
             const Unit w = unit_of(a, hgroups, u);
             const int nh = min(kH, a.heads - w.hg * kH);
             // ---- Q of the unit: f16, times 2^qe. The last unit's score products are
-            // complete (its last S^T was read), so the buffer is free.
+            // complete (its last S^T was read), so the buffer is free; its value product
+            // may still run, and its output is written after this unit's first decode.
             int qe;
             {
                 const uint16_t* qb = a.qlat + ((long long)w.r * a.heads + w.hg * kH) * kKVL;
+                uint4 v[8];
                 uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int i = threadIdx.x + 512 * k;
-                    if ((i >> 6) < nh) {
-                        const uint4 v = ldg16(qb + (long long)i * 8);
-                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v.x), f4_finite_abs2(v.y)),
-                                                 __vmaxu2(f4_finite_abs2(v.z), f4_finite_abs2(v.w))));
-                    }
+                    v[k] = (i >> 6) < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
                 }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[k].x), f4_finite_abs2(v[k].y)),
+                                             __vmaxu2(f4_finite_abs2(v[k].z), f4_finite_abs2(v[k].w))));
                 m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
                 if (lane == 0) qmax[warp] = m;
                 bar_sync(1, kWorkers * 32);
                 m = qmax[lane & 15];
                 qe = f4_q_exp(__reduce_max_sync(0xffffffffu, m));
                 const float mul = pow2f(qe);
-                // read again (from L2) rather than held across the exchange in registers
-#pragma unroll 4
+#pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const int i = threadIdx.x + 512 * k, h = i >> 6, c = i & 63;
-                    const uint4 v = h < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
                     sts16(smem_u32(smem + kOffQ) + (c >> 3) * kQAtom + h * 128 +
                               (((c & 7) ^ (h & 7)) << 4),
-                          make_uint4(f4_q_half2(v.x, mul), f4_q_half2(v.y, mul),
-                                     f4_q_half2(v.z, mul), f4_q_half2(v.w, mul)));
+                          make_uint4(f4_q_half2(v[k].x, mul), f4_q_half2(v[k].y, mul),
+                                     f4_q_half2(v[k].z, mul), f4_q_half2(v[k].w, mul)));
                 }
                 fence_async_smem();
                 arrive(Q_FULL);
             }
             const float sl2 = a.scale * kLog2e4 * a.vscale * pow2f(-qe);
+            if (u + (int)gridDim.x < units) {  // the next unit's Q into L2, a line a thread
+                const Unit x = unit_of(a, hgroups, u + gridDim.x);
+                const int i = threadIdx.x;  // 64 channels of head i / 8
+                if (x.hg * kH + (i >> 3) < a.heads)
+                    prefetch_l2(a.qlat + ((long long)x.r * a.heads + x.hg * kH) * kKVL + 64 * i);
+            }
 
             float e[16], l[16];  // maximum less kUpTc, this lane's sum of weights, per head
 #pragma unroll
@@ -345,6 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     wait(ROWS_FULL + ((n + 1) & (kRing - 1)), (uint32_t)(((n + 1) / kRing) & 1));
                     request(n + 1);
                 }
+                // ---- the last unit's output, while this one's first score product runs
+                if (c == 0 && ku > 0) {
+                    bar_sync(2 + (warp >> 2), 128);  // kout is in place
+                    write_out(prev, ku - 1);
+                }
                 // ---- softmax
                 const int rb = n & (kRing - 1);
                 const bool valid = rows[rb * kT + j] >= 0;
@@ -387,25 +456,35 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                 }
                 if (moving) {
                     // move the maxima that a score of this chunk exceeds by more than kLazy
-#pragma unroll
-                    for (int h = 0; h < 16; ++h) {
-                        const float mx =
-                            warp_max(valid ? __uint_as_float(sv[h]) * sl2 : NEG_INF);
-                        if (lane == 0) red[qd * kH + hb + h] = mx;
-                    }
-                    bar_sync(2 + (warp >> 2), 128);
                     float f[16];
+#pragma unroll
+                    for (int h = 0; h < 16; ++h)
+                        f[h] = valid ? __uint_as_float(sv[h]) * sl2 : NEG_INF;
+                    const float mine =
+                        scatter16(f, lane, [](float x, float y) { return fmaxf(x, y); });
+                    if ((lane & 1) == 0) red[qd * kH + hb + (lane >> 1)] = mine;
+                    bar_sync(2 + (warp >> 2), 128);
                     bool resc = false;
 #pragma unroll
-                    for (int h = 0; h < 16; ++h) {
-                        const float mx = fmaxf(fmaxf(red[hb + h], red[kH + hb + h]),
-                                               fmaxf(red[2 * kH + hb + h], red[3 * kH + hb + h])) -
-                                         kUpTc;
-                        const bool moved = mx > e[h] + kLazy;
-                        f[h] = moved ? ex2_sfu(e[h] - mx) : 1.f;
-                        e[h] = moved ? mx : e[h];
-                        l[h] *= f[h];
-                        resc = resc || moved;
+                    for (int i = 0; i < 4; ++i) {
+                        float4 r[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            r[q] = *reinterpret_cast<const float4*>(red + q * kH + hb + 4 * i);
+                        const float t[4] = {
+                            fmaxf(fmaxf(r[0].x, r[1].x), fmaxf(r[2].x, r[3].x)) - kUpTc,
+                            fmaxf(fmaxf(r[0].y, r[1].y), fmaxf(r[2].y, r[3].y)) - kUpTc,
+                            fmaxf(fmaxf(r[0].z, r[1].z), fmaxf(r[2].z, r[3].z)) - kUpTc,
+                            fmaxf(fmaxf(r[0].w, r[1].w), fmaxf(r[2].w, r[3].w)) - kUpTc};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int h = 4 * i + k;
+                            const bool moved = t[k] > e[h] + kLazy;
+                            f[h] = moved ? ex2_sfu(e[h] - t[k]) : 1.f;
+                            e[h] = moved ? t[k] : e[h];
+                            l[h] *= f[h];
+                            resc = resc || moved;
+                        }
                     }
                     if (resc && c > 0) {  // the chunk before's O^T is complete (S_FULL)
 #pragma unroll 1
@@ -433,63 +512,31 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                 for (int h = 0; h < 16; ++h) l[h] += valid ? __uint_as_float(sv[h]) : 0.f;
             }
 
-            // ---- epilogue: head sums over the lanes, then over the four lane quarters
+            // ---- head sums over the lanes, then over the four lane quarters; the factors
+            // of the output follow from them
+            float first = e[0];  // lane h: head hb + h's maximum
 #pragma unroll
-            for (int ww = 8, m = 16; ww >= 1; ww >>= 1, m >>= 1) {
-#pragma unroll
-                for (int i = 0; i < ww; ++i) {
-                    const bool hi = (lane & m) != 0;
-                    const float send = hi ? l[i] : l[ww + i];
-                    const float recv = __shfl_xor_sync(0xffffffffu, send, m);
-                    l[i] = (hi ? l[ww + i] : l[i]) + recv;
-                }
-            }
-            l[0] += __shfl_xor_sync(0xffffffffu, l[0], 1);  // head hb + lane / 2
-            if ((lane & 1) == 0) sums[qd * kH + hb + (lane >> 1)] = l[0];
+            for (int h = 1; h < 16; ++h) first = lane == h ? e[h] : first;
+            const float sum = scatter16(l, lane, [](float x, float y) { return x + y; });
+            if ((lane & 1) == 0) sums[qd * kH + hb + (lane >> 1)] = sum;
             bar_sync(2 + (warp >> 2), 128);
-            float k[16];  // what each head's accumulators are multiplied by
-#pragma unroll
-            for (int h = 0; h < 16; ++h) {
-                const float s = (sums[hb + h] + sums[kH + hb + h]) +
-                                (sums[2 * kH + hb + h] + sums[3 * kH + hb + h]);
+            if (qd == 0 && lane < 16) {
+                const int h = hb + lane;
+                const float t = (sums[h] + sums[kH + h]) + (sums[2 * kH + h] + sums[3 * kH + h]);
                 // a NaN sum keeps its NaN
-                k[h] = a.ns > 1 ? a.vscale : (s == 0.f ? 0.f : __fdividef(a.vscale, s));
-                if (a.ns > 1 && qd == 0 && lane == h && hb + h < nh) {
+                kout[h] = a.ns > 1 ? a.vscale * exp2f(-kUpTc) : (t == 0.f ? 0.f : a.vscale / t);
+                if (a.ns > 1 && h < nh) {
                     const long long p =
-                        ((long long)w.r * a.ns + w.split) * a.heads + w.hg * kH + hb + h;
+                        ((long long)w.r * a.ns + w.split) * a.heads + w.hg * kH + h;
                     *reinterpret_cast<float2*>(a.part_ml + p * 2) =
-                        make_float2(e[h] + kUpTc, s * exp2f(-kUpTc));
+                        make_float2(first + kUpTc, t * exp2f(-kUpTc));
                 }
             }
-            wait(O_DONE, (uint32_t)(ku & 1));
-            tc_fence_after();
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-                uint32_t v[16];
-                tc_ld16(v, tmem + lrow + 64 + 64 * i + hb);
-                const int col = 128 * i + j;
-                if (a.ns > 1) {
-                    float* o = a.part_o + (((long long)w.r * a.ns + w.split) * a.heads +
-                                           w.hg * kH + hb) * kKVL + col;
-#pragma unroll
-                    for (int h = 0; h < 16; ++h)
-                        if (hb + h < nh)
-                            o[h * kKVL] = __uint_as_float(v[h]) * (k[h] * exp2f(-kUpTc));
-                } else {
-                    const long long o = ((long long)w.r * a.heads + w.hg * kH + hb) * kKVL + col;
-#pragma unroll
-                    for (int h = 0; h < 16; ++h) {
-                        const float x = __uint_as_float(v[h]) * k[h];
-                        if (hb + h < nh) {
-                            if (a.olat) a.olat[o + h * kKVL] = x;
-                            if (a.olat16)
-                                a.olat16[o + h * kKVL] = __bfloat16_as_ushort(__float2bfloat16_rn(x));
-                        }
-                    }
-                }
-            }
-            tc_fence_before();
-            arrive(O_FREE);
+            prev = w;
+        }
+        if (ku > 0) {
+            bar_sync(2 + (warp >> 2), 128);
+            write_out(prev, ku - 1);
         }
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegLow));

@@ -98,7 +98,9 @@ __global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
         const int st = c % STAGES;
         long long prow = -1;
         if (lane < 8) {
-            prow = f4_token(a, r, seq, L, t_begin + c * CH + warp * 8 + lane, t_end);
+            const int pos = t_begin + c * CH + warp * 8 + lane;
+            if (pos < t_end)
+                prow = f4_token_row(a, seq, L, __ldg(a.token_ids + (long long)r * a.ow + pos));
             vmask[st * CH + warp * 8 + lane] = prow >= 0 ? 1 : 0;
         }
         uint8_t* dst = raw + (st * CH + warp * 8) * RAWB;

@@ -33,12 +33,9 @@ struct MlaF4Args {
 int mla_f4_tc_chunk();
 int mla_f4_tc_launch(const MlaF4Args& a, cudaStream_t st);
 
-// The cache row of selected position pos of row r (sequence seq, L tokens), or -1 where
-// there is none; bad ids and block entries are flagged.
-__device__ __forceinline__ long long f4_token(const MlaF4Args& a, int r, int seq, int L, int pos,
-                                              int end) {
-    if (pos >= end) return -1;
-    const int t = __ldg(a.token_ids + (long long)r * a.ow + pos);
+// The cache row of token t of sequence seq (L tokens), or -1 where there is none; bad ids
+// and block entries are flagged.
+__device__ __forceinline__ long long f4_token_row(const MlaF4Args& a, int seq, int L, int t) {
     if (t >= 0 && t < L) {
         const long long row = token_row(a.pg, seq, t);
         if (row < 0) flag_status(a.status, DSA_STATUS_BAD_BLOCK);

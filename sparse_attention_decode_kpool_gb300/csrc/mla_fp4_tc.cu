@@ -137,10 +137,6 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
                  "r"(v.z), "r"(v.w)
                  : "memory");
 }
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 // MMA and commit by one elected lane of a converged warp (always the same one). The whole
 // warp runs the issue loop, so descriptors and loop counters stay in uniform registers,
 // where tcgen05.mma takes them; with one lane in the loop each was moved there again and
@@ -312,10 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
         };
 
         int n = 0, ku = 0;
-        if ((int)blockIdx.x < units) {
-            wait(ROWS_FULL, 0);
-            request(0);
-        }
         Unit prev = {};
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
             const Unit w = unit_of(a, hgroups, u);
@@ -332,6 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                 for (int k = 0; k < 8; ++k) {
                     const int i = threadIdx.x + 512 * k;
                     v[k] = (i >> 6) < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
+                }
+                if (ku == 0) {  // the first chunk's rows, beside the first Q
+                    wait(ROWS_FULL, 0);
+                    request(0);
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
@@ -430,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                         const float p1 = ex2_sfu(__uint_as_float(sv[2 * i + 1]));
                         sv[2 * i] = __float_as_uint(p0);
                         sv[2 * i + 1] = __float_as_uint(p1);
-                        pk[i] = valid ? half2_bits(p0, p1) : 0u;
+                        const __half2 p = __floats2half2_rn(p0, p1);
+                        pk[i] = valid ? *reinterpret_cast<const uint32_t*>(&p) : 0u;
                     }
                     sts16(pc0, make_uint4(pk[0], pk[1], pk[2], pk[3]));
                     sts16(pc1, make_uint4(pk[4], pk[5], pk[6], pk[7]));
@@ -594,22 +591,29 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
             int n = 0;
             for (int u = blockIdx.x; u < units; u += gridDim.x) {
                 const Unit w = unit_of(a, hgroups, u);
-                int seq = a.row_seq ? __ldg(a.row_seq + w.r) : w.r;
-                int L = 0;
-                if (seq >= 0 && seq < a.pg.batch) {
-                    L = min(__ldg(a.pg.seq_lens + seq), seq_capacity(a.pg));
-                } else {
-                    if (lane == 0) flag_status(a.status, DSA_STATUS_BAD_TOKEN);
-                    seq = 0;
-                }
+                int seq = -1, L = 0;
                 for (int c = 0; c < w.nch; ++c, ++n) {
                     if ((n & 1) != mine) continue;
                     const int b = n & (kRing - 1);
+                    int id[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int pos = w.t_begin + c * kT + 32 * k + lane;
+                        id[k] = pos < w.t_end ? __ldg(a.token_ids + (long long)w.r * a.ow + pos) : -1;
+                    }
+                    if (c < 2) {  // this warp's first chunk of the unit; the ids are on their way
+                        seq = a.row_seq ? __ldg(a.row_seq + w.r) : w.r;
+                        if (seq >= 0 && seq < a.pg.batch) {
+                            L = min(__ldg(a.pg.seq_lens + seq), seq_capacity(a.pg));
+                        } else {
+                            if (lane == 0) flag_status(a.status, DSA_STATUS_BAD_TOKEN);
+                            seq = 0;
+                            L = 0;
+                        }
+                    }
                     int prow[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        prow[k] = (int)f4_token(a, w.r, seq, L, w.t_begin + c * kT + 32 * k + lane,
-                                                w.t_end);
+                    for (int k = 0; k < 4; ++k) prow[k] = (int)f4_token_row(a, seq, L, id[k]);
                     wait(ROWS_EMPTY + b, (uint32_t)((n / kRing) & 1) ^ 1u);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) rows[b * kT + 32 * k + lane] = prow[k];

@@ -331,8 +331,19 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                 }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[k].x), f4_finite_abs2(v[k].y)),
-                                             __vmaxu2(f4_finite_abs2(v[k].z), f4_finite_abs2(v[k].w))));
+                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+                if (max(m & 0xffffu, m >> 16) >= 0x7f80u) {  // an Inf or NaN: the finite ones
+                    m = 0;
+#pragma unroll 1
+                    for (int k = 0; k < 8; ++k) {
+                        const int i = threadIdx.x + 512 * k;
+                        if ((i >> 6) >= nh) break;
+                        const uint4 x = ldg16(qb + (long long)i * 8);
+                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(x.x), f4_finite_abs2(x.y)),
+                                                 __vmaxu2(f4_finite_abs2(x.z), f4_finite_abs2(x.w))));
+                    }
+                }
                 m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
                 if (lane == 0) qmax[warp] = m;
                 bar_sync(1, kWorkers * 32);

@@ -450,22 +450,33 @@ def _fp4_cache(codes, scales) -> int:
     return kvl
 
 
-def _call(t: torch.Tensor, stream, fn, *args, others=()) -> None:
-    """One library call for tensors on t's device: made with that device current, on its
-    current stream by default. ``others`` must live on the same device (pinned host
-    memory is no device's)."""
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev and o.is_cuda:
-            raise ValueError(f"tensors on {t.device} and {o.device}: one device per call")
+def _dev_ptr(t: Optional[torch.Tensor], dtype, dev: int, name: str) -> Optional[int]:
+    """_ptr for the calls whose tensors must all live on one device, ``dev``."""
+    if t is None:
+        return None
+    if t.get_device() == dev and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return t.data_ptr()
+    p = _ptr(t, dtype, name)
+    raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}: one device per call ({p:#x})")
+
+
+def _run(dev: int, stream, fn, *args) -> None:
+    """One library call with device ``dev`` current, on its current stream by default (by
+    its raw handle: the GPU work of these calls is often shorter than making a Stream
+    object takes)."""
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             check(fn(*args, _stream(stream)))
         return
-    # the raw handle, without a Stream object around it: these calls' GPU work is often
-    # shorter than that object's making
-    check(fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
-             else _stream(stream)))
+    rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if rc:
+        check(rc)
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def dsa_quantize_latent_fp4(x, codes, scales, cache_exp: int = 0, stream=None) -> None:
@@ -476,10 +487,10 @@ def dsa_quantize_latent_fp4(x, codes, scales, cache_exp: int = 0, stream=None) -
         raise ValueError("codes [.., kvl/2] and scales [.., kvl/16] must match x [.., kvl]")
     if x.numel() == 0:
         return
-    _call(x, stream, _lib.load().dsa_quantize_latent_fp4,
-          _ptr(x, torch.bfloat16, "x"), x.numel() // kvl, kvl, int(cache_exp),
-          _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"),
-          others=(codes, scales))
+    dev = _device_of(x, "x")
+    _run(dev, stream, _lib.load().dsa_quantize_latent_fp4,
+         _dev_ptr(x, torch.bfloat16, dev, "x"), x.numel() // kvl, kvl, int(cache_exp),
+         _dev_ptr(codes, torch.uint8, dev, "codes"), _dev_ptr(scales, torch.uint8, dev, "scales"))
 
 
 def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None, status=None,
@@ -496,11 +507,11 @@ def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None,
         raise ValueError(f"out must hold the cache's {cache_rows} rows")
     if n == 0:
         return
-    _call(codes, stream, _lib.load().dsa_dequantize_latent_fp4,
-          _ptr(codes, torch.uint8, "codes"), _ptr(scales, torch.uint8, "scales"), cache_rows,
-          _ptr(rows, torch.int32, "rows"), n, kvl, int(cache_exp),
-          _ptr(out, torch.bfloat16, "out"), _ptr(status, torch.int32, "status"),
-          others=(scales, rows, out, status))
+    dev = _device_of(codes, "codes")
+    _run(dev, stream, _lib.load().dsa_dequantize_latent_fp4,
+         _dev_ptr(codes, torch.uint8, dev, "codes"), _dev_ptr(scales, torch.uint8, dev, "scales"),
+         cache_rows, _dev_ptr(rows, torch.int32, dev, "rows"), n, kvl, int(cache_exp),
+         _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(status, torch.int32, dev, "status"))
 
 
 def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float, pg: DsaPaging,
@@ -519,18 +530,19 @@ def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float,
                          "ckv_scales [.., kvl/16]")
     if batch != pg.batch:
         raise ValueError(f"one staged row per sequence: {batch} rows, {pg.batch} sequences")
-    _call(k_new, stream, _lib.load().dsa_decode_append_fp4,
-          _ptr(k_new, torch.bfloat16, "k_new"), _ptr(gate_new, torch.bfloat16, "gate_new"),
-          _ptr(ckv_new, torch.bfloat16, "ckv_new"), _ptr(ape, torch.float32, "ape"),
-          _ptr(ln_w, torch.bfloat16, "ln_w"), _ptr(ln_b, torch.bfloat16, "ln_b"), float(eps),
-          ctypes.byref(pg), _ptr(seq_lens, torch.int32, "seq_lens"), int(first_key), int(kpool),
-          ihd, kvl, _ptr(k_raw, torch.bfloat16, "k_raw"), _ptr(gate, torch.bfloat16, "gate"),
-          _ptr(token_valid, torch.uint8, "token_valid"), _ptr(ckv, torch.bfloat16, "ckv"),
-          _ptr(ckv_codes, torch.uint8, "ckv_codes"), _ptr(ckv_scales, torch.uint8, "ckv_scales"),
-          int(cache_exp), _ptr(kpool_out, torch.bfloat16, "kpool_out"),
-          _ptr(pool_valid, torch.uint8, "pool_valid"), _ptr(pool_idx, torch.int32, "pool_idx"),
-          _ptr(row_ctx, torch.int32, "row_ctx"), _ptr(status, torch.int32, "status"),
-          others=(gate_new, ckv_new, seq_lens, k_raw, ckv_codes, ckv_scales, kpool_out))
+    dev = _device_of(k_new, "k_new")
+    bf16, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+    _run(dev, stream, _lib.load().dsa_decode_append_fp4,
+         _dev_ptr(k_new, bf16, dev, "k_new"), _dev_ptr(gate_new, bf16, dev, "gate_new"),
+         _dev_ptr(ckv_new, bf16, dev, "ckv_new"), _dev_ptr(ape, f32, dev, "ape"),
+         _dev_ptr(ln_w, bf16, dev, "ln_w"), _dev_ptr(ln_b, bf16, dev, "ln_b"), float(eps),
+         ctypes.byref(pg), _dev_ptr(seq_lens, i32, dev, "seq_lens"), int(first_key), int(kpool),
+         ihd, kvl, _dev_ptr(k_raw, bf16, dev, "k_raw"), _dev_ptr(gate, bf16, dev, "gate"),
+         _dev_ptr(token_valid, u8, dev, "token_valid"), _dev_ptr(ckv, bf16, dev, "ckv"),
+         _dev_ptr(ckv_codes, u8, dev, "ckv_codes"), _dev_ptr(ckv_scales, u8, dev, "ckv_scales"),
+         int(cache_exp), _dev_ptr(kpool_out, bf16, dev, "kpool_out"),
+         _dev_ptr(pool_valid, u8, dev, "pool_valid"), _dev_ptr(pool_idx, i32, dev, "pool_idx"),
+         _dev_ptr(row_ctx, i32, dev, "row_ctx"), _dev_ptr(status, i32, dev, "status"))
 
 
 def dsa_sparse_mla_decode_fp4_workspace(rows: int, heads: int, out_width: int, hidden: int,
@@ -569,19 +581,18 @@ def dsa_sparse_mla_decode_fp4(qlat, row_seq, ckv_codes, ckv_scales, cache_exp: i
         raise ValueError(f"olat must be [{rows}, {heads}, {kvl}]")
     if olat is not None and olat.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"olat must be float32 or bfloat16, got {olat.dtype}")
-    p_olat = _ptr(olat, None, "olat")
-    half = olat is not None and olat.dtype == torch.bfloat16
+    dev = _device_of(ckv_codes, "ckv_codes")
+    bf16, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    p_olat = _dev_ptr(olat, None, dev, "olat")
+    half = olat is not None and olat.dtype is bf16
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(ckv_codes, stream, _lib.load().dsa_sparse_mla_decode_fp4,
-          _ptr(qlat, torch.bfloat16, "qlat"), rows, heads, kvl,
-          _ptr(row_seq, torch.int32, "row_seq"), _ptr(ckv_codes, torch.uint8, "ckv_codes"),
-          _ptr(ckv_scales, torch.uint8, "ckv_scales"), int(cache_exp), ctypes.byref(pg),
-          _ptr(token_ids, torch.int32, "token_ids"), ow, float(softmax_scale),
-          _ptr(o_absorb, torch.bfloat16, "o_absorb"), hidden,
-          _ptr(y, torch.bfloat16, "y", host_ok=True), None if half else p_olat,
-          p_olat if half else None, _ptr(status, torch.int32, "status"),
-          _ptr(workspace, None, "workspace"), ws_bytes,
-          others=(qlat, row_seq, ckv_scales, token_ids, o_absorb, y, olat, status, workspace))
+    _run(dev, stream, _lib.load().dsa_sparse_mla_decode_fp4,
+         _dev_ptr(qlat, bf16, dev, "qlat"), rows, heads, kvl, _dev_ptr(row_seq, i32, dev, "row_seq"),
+         _dev_ptr(ckv_codes, u8, dev, "ckv_codes"), _dev_ptr(ckv_scales, u8, dev, "ckv_scales"),
+         int(cache_exp), ctypes.byref(pg), _dev_ptr(token_ids, i32, dev, "token_ids"), ow,
+         float(softmax_scale), _dev_ptr(o_absorb, bf16, dev, "o_absorb"), hidden,
+         _ptr(y, bf16, "y", host_ok=True), None if half else p_olat, p_olat if half else None,
+         _dev_ptr(status, i32, dev, "status"), _dev_ptr(workspace, None, dev, "workspace"), ws_bytes)
 
 
 # -- pages -----------------------------------------------------------------
@@ -610,39 +621,40 @@ def dsa_pages_workspace(num_blocks: int, batch: int) -> int:
     return int(n.value)
 
 
-def _pool(pg: DsaPaging, block_table, refs) -> None:
+def _pool(pg: DsaPaging, block_table, refs) -> int:
+    """The pool's device."""
     if tuple(block_table.shape) != (pg.batch, pg.max_blocks):
         raise ValueError(f"block_table must be [{pg.batch}, {pg.max_blocks}]")
     if refs.numel() != pg.num_blocks:
         raise ValueError(f"refs must be [{pg.num_blocks}]")
+    return _device_of(refs, "refs")
 
 
 def dsa_pages_free(seqs, pg: DsaPaging, block_table, seq_lens, refs, status=None,
                    stream=None) -> None:
     """End the listed sequences: their pages lose a reference, their rows become -1 and
     their lengths 0 (-1 entries of ``seqs`` are skipped)."""
-    _pool(pg, block_table, refs)
-    _call(refs, stream, _lib.load().dsa_pages_free,
-          _ptr(seqs, torch.int32, "seqs"), int(seqs.numel()), ctypes.byref(pg),
-          _ptr(block_table, torch.int32, "block_table"),
-          _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(refs, torch.int32, "refs"),
-          _ptr(status, torch.int32, "status"), others=(seqs, block_table, seq_lens, status))
+    dev = _pool(pg, block_table, refs)
+    i32 = torch.int32
+    _run(dev, stream, _lib.load().dsa_pages_free,
+         _dev_ptr(seqs, i32, dev, "seqs"), seqs.numel(), ctypes.byref(pg),
+         _dev_ptr(block_table, i32, dev, "block_table"), _dev_ptr(seq_lens, i32, dev, "seq_lens"),
+         _dev_ptr(refs, i32, dev, "refs"), _dev_ptr(status, i32, dev, "status"))
 
 
 def dsa_pages_fork(parents, children, pg: DsaPaging, block_table, seq_lens, refs, status=None,
                    stream=None) -> None:
     """children[i] becomes a copy of parents[i] that shares its pages (-1 entries of
     ``children`` are skipped)."""
-    _pool(pg, block_table, refs)
+    dev = _pool(pg, block_table, refs)
     if parents.numel() != children.numel():
         raise ValueError("parents and children must have the same length")
-    _call(refs, stream, _lib.load().dsa_pages_fork,
-          _ptr(parents, torch.int32, "parents"), _ptr(children, torch.int32, "children"),
-          int(children.numel()), ctypes.byref(pg),
-          _ptr(block_table, torch.int32, "block_table"),
-          _ptr(seq_lens, torch.int32, "seq_lens"), _ptr(refs, torch.int32, "refs"),
-          _ptr(status, torch.int32, "status"),
-          others=(parents, children, block_table, seq_lens, status))
+    i32 = torch.int32
+    _run(dev, stream, _lib.load().dsa_pages_fork,
+         _dev_ptr(parents, i32, dev, "parents"), _dev_ptr(children, i32, dev, "children"),
+         children.numel(), ctypes.byref(pg), _dev_ptr(block_table, i32, dev, "block_table"),
+         _dev_ptr(seq_lens, i32, dev, "seq_lens"), _dev_ptr(refs, i32, dev, "refs"),
+         _dev_ptr(status, i32, dev, "status"))
 
 
 def dsa_pages_reserve(pg: DsaPaging, block_table, refs, new_tokens: int,
@@ -650,35 +662,34 @@ def dsa_pages_reserve(pg: DsaPaging, block_table, refs, new_tokens: int,
                       seqs=None, status=None, workspace=None, stream=None) -> None:
     """Room for the next ``new_tokens`` tokens of each listed sequence (all of them by
     default): free pages where none is mapped, private copies of shared ones."""
-    _pool(pg, block_table, refs)
+    dev = _pool(pg, block_table, refs)
     if seqs is not None and seqs.numel() == 0:
         return  # an empty list has no address: to the C call it would mean every sequence
+    i32 = torch.int32
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(refs, stream, _lib.load().dsa_pages_reserve,
-          _ptr(seqs, torch.int32, "seqs"), 0 if seqs is None else int(seqs.numel()),
-          ctypes.byref(pg), _ptr(block_table, torch.int32, "block_table"),
-          _ptr(refs, torch.int32, "refs"), int(new_tokens), int(first_key), int(kpool),
-          None if arrays is None else ctypes.byref(arrays), _ptr(status, torch.int32, "status"),
-          _ptr(workspace, None, "workspace"), ws_bytes,
-          others=(seqs, block_table, status, workspace))
+    _run(dev, stream, _lib.load().dsa_pages_reserve,
+         _dev_ptr(seqs, i32, dev, "seqs"), 0 if seqs is None else seqs.numel(), ctypes.byref(pg),
+         _dev_ptr(block_table, i32, dev, "block_table"), _dev_ptr(refs, i32, dev, "refs"),
+         int(new_tokens), int(first_key), int(kpool),
+         None if arrays is None else ctypes.byref(arrays), _dev_ptr(status, i32, dev, "status"),
+         _dev_ptr(workspace, None, dev, "workspace"), ws_bytes)
 
 
 def dsa_pages_compact(pg: DsaPaging, block_table, refs, arrays: Optional[DsaPageArrays],
                       remap=None, live=None, status=None, workspace=None, stream=None) -> None:
     """Move the pool's live pages to its front and rewrite the block table."""
-    _pool(pg, block_table, refs)
+    dev = _pool(pg, block_table, refs)
     if remap is not None and remap.numel() != pg.num_blocks:
         raise ValueError(f"remap must be [{pg.num_blocks}]")
     if live is not None and live.numel() != 1:
         raise ValueError("live must hold one number")
+    i32 = torch.int32
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(refs, stream, _lib.load().dsa_pages_compact,
-          ctypes.byref(pg), _ptr(block_table, torch.int32, "block_table"),
-          _ptr(refs, torch.int32, "refs"),
-          None if arrays is None else ctypes.byref(arrays), _ptr(remap, torch.int32, "remap"),
-          _ptr(live, torch.int32, "live"), _ptr(status, torch.int32, "status"),
-          _ptr(workspace, None, "workspace"), ws_bytes,
-          others=(block_table, remap, live, status, workspace))
+    _run(dev, stream, _lib.load().dsa_pages_compact,
+         ctypes.byref(pg), _dev_ptr(block_table, i32, dev, "block_table"),
+         _dev_ptr(refs, i32, dev, "refs"), None if arrays is None else ctypes.byref(arrays),
+         _dev_ptr(remap, i32, dev, "remap"), _dev_ptr(live, i32, dev, "live"),
+         _dev_ptr(status, i32, dev, "status"), _dev_ptr(workspace, None, dev, "workspace"), ws_bytes)
 
 
 def dsa_frontend_workspace(rows: int, hidden: int, n_x: int, q_lora_rank: int, kv_lora_rank: int,

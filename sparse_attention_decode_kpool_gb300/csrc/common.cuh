@@ -90,12 +90,6 @@ int project_launch(const void* x, bool x_f32, int rows, int K, const uint16_t* A
                    uint16_t* y, int32_t* status, void* ws, size_t ws_bytes, cudaStream_t st,
                    float* yf = nullptr, uint16_t* y2 = nullptr, int split = 0);
 
-// Merges ns <= 64 splits' partials (mla.cu): part_o [rows, ns, heads, 512] unnormalised,
-// part_ml [rows, ns, heads, 2] = (maximum in log2 units, sum) -> olat (f32) and xbf (bf16),
-// each nullable.
-int mla_combine_launch(const float* part_o, const float* part_ml, int rows, int heads, int ns,
-                       float* olat, uint16_t* xbf, cudaStream_t st);
-
 // Sparse latent attention on the tensor cores (mla_tc.cu): the split kernel of
 // dsa_sparse_mla_decode for 64 heads (large batches, or forced by DSA_OPT_MLA_KERNEL). Writes the splits' partials
 // (ns > 1) or olat / its bf16 copy (ns == 1) in the same layout as the mma.sync split

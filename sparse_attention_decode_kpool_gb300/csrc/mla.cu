@@ -732,16 +732,6 @@ void launch_gemv(GemvArgs g, cudaStream_t st) {
 }
 
 }  // namespace
-
-int mla_combine_launch(const float* part_o, const float* part_ml, int rows, int heads, int ns,
-                       float* olat, uint16_t* xbf, cudaStream_t st) {
-    cudaError_t e = launch_pdl(mla_combine_kernel, dim3(heads, rows), dim3(128), 0, st, part_o,
-                               part_ml, heads, ns, olat, xbf);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "dsa_sparse_mla_decode combine launch");
-    return DSA_OK;
-}
-
 }  // namespace dsa
 
 using namespace dsa;
@@ -852,8 +842,10 @@ int mla_decode_impl(const dsa_bf16* qlat, int rows, int heads, int kv_lora_rank,
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_sparse_mla_decode split launch");
     if ((p.ns > 1 && !p.dec) || (p.dec && !p.dec_merge)) {
-        rc = mla_combine_launch(a.part_o, a.part_ml, rows, heads, p.ns, olat, a.xbf, st);
-        if (rc) return rc;
+        e = launch_pdl(mla_combine_kernel, dim3(heads, rows), dim3(128), 0, st,
+                       (const float*)a.part_o, (const float*)a.part_ml, heads, p.ns, olat, a.xbf);
+        if (e == cudaSuccess) e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e, "dsa_sparse_mla_decode combine launch");
     }
     if (p.tma_proj) {
         return project_launch(a.xbf, false, rows, heads * KVL, o_absorb, hidden, y, status,

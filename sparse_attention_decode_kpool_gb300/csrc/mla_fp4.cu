@@ -332,10 +332,108 @@ __global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
         }
 }
 
+// Merges the splits of a row: a warp per 128 C latent columns of a (row, head), a lane per
+// C four-column pieces, E splits at a time. C E = 16 loads of 16 bytes are under way per
+// lane, whether the splits are many (a few rows) or two (many rows): with C = 1 and two
+// splits the 64-row merge took 11 us, with a block per (row, head) 8. They are asked for
+// before the weights 2^(m_s - max) are known, which the warp takes from the splits' (m, l)
+// pairs, a lane per pair. Sums in split order.
+constexpr int kMergeWarps = 4;
+template <int C>
+__global__ void __launch_bounds__(kMergeWarps * 32) mla_f4_merge_kernel(
+    const float* __restrict__ part_o, const float* __restrict__ part_ml, long long rh, int heads,
+    int ns, float* olat, uint16_t* olat16) {
+    pdl_trigger();  // the projection after it streams weights that do not depend on it
+    pdl_wait();
+    constexpr int E = 16 / C, W = 4 / C;  // splits at a time, warps per (row, head)
+    const int lane = threadIdx.x & 31;
+    const long long u = (long long)blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    const long long i = u / W;  // row * heads + head
+    if (i >= rh) return;
+    const int r = (int)(i / heads), h = (int)(i - (long long)r * heads);
+    const long long first = ((long long)r * ns) * heads + h;  // split 0's entry, + heads each
+    const int col = (int)(u % W) * (32 * C) + lane;           // in pieces of four columns
+    const float4* po = reinterpret_cast<const float4*>(part_o) + first * (KVL / 4) + col;
+    const long long step = (long long)heads * (KVL / 4);
+    float4 o[E][C];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int s = 0; s < E; ++s)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                o[s][c] = s0 + s < ns ? __ldg(po + (s0 + s) * step + 32 * c)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    load(0);
+    float w[2], l[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int s = lane + 32 * k;
+        const float2 ml = s < ns ? __ldg(reinterpret_cast<const float2*>(part_ml) + first +
+                                         (long long)s * heads)
+                                 : make_float2(-INFINITY, 0.f);
+        w[k] = ml.x;
+        l[k] = ml.y;
+    }
+    float top = fmaxf(w[0], w[1]);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        w[k] = w[k] == -INFINITY ? 0.f : exp2f(w[k] - top);
+        sum += w[k] * l[k];  // NaN where a split's sum is NaN
+    }
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    float4 acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < ns; s0 += E) {
+        if (s0 > 0) load(s0);
+#pragma unroll
+        for (int s = 0; s < E; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, s0 + s < 32 ? w[0] : w[1], (s0 + s) & 31);
+            if (s0 + s < ns) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    acc[c].x = fmaf(ws, o[s][c].x, acc[c].x);
+                    acc[c].y = fmaf(ws, o[s][c].y, acc[c].y);
+                    acc[c].z = fmaf(ws, o[s][c].z, acc[c].z);
+                    acc[c].w = fmaf(ws, o[s][c].w, acc[c].w);
+                }
+            }
+        }
+    }
+    const float k = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const long long at = i * KVL + 4 * (col + 32 * c);
+        const float4 x = make_float4(acc[c].x * k, acc[c].y * k, acc[c].z * k, acc[c].w * k);
+        if (olat) *reinterpret_cast<float4*>(olat + at) = x;
+        if (olat16)
+            *reinterpret_cast<uint2*>(olat16 + at) =
+                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    }
+}
+
+template <int C>
+int launch_merge(const MlaF4Args& a, float* olat, uint16_t* olat16, cudaStream_t st) {
+    const long long rh = (long long)a.rows * a.heads, warps = rh * (4 / C);
+    cudaError_t e = launch_pdl(mla_f4_merge_kernel<C>,
+                               dim3((unsigned)((warps + kMergeWarps - 1) / kMergeWarps)),
+                               dim3(kMergeWarps * 32), 0, st, (const float*)a.part_o,
+                               (const float*)a.part_ml, rh, a.heads, a.ns, olat, olat16);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_sparse_mla_decode_fp4 merge launch");
+    return DSA_OK;
+}
+
 // ---------------------------------------------------------------------------
 struct F4Plan {
     bool tc;  // the tcgen05 kernel (mla_fp4_tc.cu), else the mma.sync kernel above
     int mt, hgroups, ns, tps;
+    long long cost;  // estimated time, tenths of a microsecond
     size_t off_part_o, off_part_ml, off_xbf, off_proj, bytes;
 };
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -350,16 +448,23 @@ F4Plan f4_plan(bool tc, int rows, int heads, int ow, int hidden, bool with_oabs,
     const long long cpr = ow > 0 ? (ow + chunk - 1) / chunk : 1;  // chunks per row
     p.tps = (int)cpr * chunk;
     p.ns = 1;
-    // The busiest CTA walks ceil(units / sms) units of ceil(chunks / ns) chunks, plus about
-    // a chunk's time per unit for Q, the epilogue and the combine: the split count that
-    // makes this smallest, the fewest splits on ties.
-    long long best = -1;
+    // Estimated time, in tenths of a microsecond, fitted to a sweep of 1 to 128 heads, 1 to
+    // 2,048 rows and 64 to 2,048 tokens: the busiest CTA walks ceil(units / sms) units of
+    // ceil(chunks / ns) chunks. A chunk takes the tcgen05 kernel (128 tokens, any number
+    // of heads up to 64) 2.8 us and a unit 4.5 us more (its first chunk's latencies, Q)
+    // plus up to 2 for the output; the mma.sync kernel 2.8 us (64 tokens, 16 heads) or 4.4
+    // (32 heads) and a unit 1 or 1.5. Splitting costs the merge, 1.8 us and its bytes at
+    // 6 TB/s. The split count that makes this smallest, the fewest on ties.
+    const long long per_chunk = tc ? 28 : p.mt == 1 ? 28 : 44;
+    const long long per_unit = tc ? 45 + 20 * (heads < 64 ? heads : 64) / 64 : p.mt == 1 ? 10 : 15;
+    p.cost = -1;
     for (long long t = 1; t <= cpr && t <= kMaxSplits; ++t) {
         const long long tps = (cpr + t - 1) / t;
         const long long ns = (cpr + tps - 1) / tps;
-        const long long cost = (base * ns + sms - 1) / sms * (tps + 1);
-        if (best < 0 || cost < best) {
-            best = cost;
+        long long cost = (tc ? 15 : 20) + (base * ns + sms - 1) / sms * (tps * per_chunk + per_unit);
+        if (ns > 1) cost += 18 + rows * ns * heads * (KVL * 4LL) / 600000;
+        if (p.cost < 0 || cost < p.cost) {
+            p.cost = cost;
             p.tps = (int)tps * chunk;
             p.ns = (int)ns;
         }
@@ -384,13 +489,18 @@ size_t f4_bytes(int rows, int heads, int ow, int hidden, bool with_oabs, int sms
     return b0 > b1 ? b0 : b1;
 }
 
-// Which kernel: DSA_OPT_MLA_KERNEL's, else the tcgen05 kernel above 32 heads.
-bool f4_use_tc(int heads, int ow, long long cache_rows) {
+// Which kernel: DSA_OPT_MLA_KERNEL's, else the one with the smaller estimate. Measured, mma
+// against tcgen05: 16 heads, 8 rows of 2,048 tokens 10.7 us against 11.9; 24 heads 13.3
+// against 12.2; 4 heads, 64 rows of 256 tokens 10.0 against 11.6, of 1,000 26 against 19;
+// 64 heads, 8 rows of 256 tokens 9.9 against 12.8, of 2,048 21 against 14.3.
+bool f4_use_tc(int rows, int heads, int ow, long long cache_rows, int sms) {
     if (ow < 1 || cache_rows > 0x7fffffffLL) return false;
     switch (mla_kernel_choice()) {
         case DSA_MLA_KERNEL_TCGEN05: return true;
         case DSA_MLA_KERNEL_MMA: return false;
-        default: return heads > 32;
+        default:
+            return f4_plan(true, rows, heads, ow, 0, false, sms).cost <
+                   f4_plan(false, rows, heads, ow, 0, false, sms).cost;
     }
 }
 
@@ -479,7 +589,7 @@ extern "C" int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int hea
     if (sms <= 0) return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4: no CUDA device");
     const long long cache_rows = P.block_table ? P.num_blocks * P.block_size
                                                : (long long)P.batch * P.max_seq_len;
-    const F4Plan p = f4_plan(f4_use_tc(heads, out_width, cache_rows), rows, heads, out_width,
+    const F4Plan p = f4_plan(f4_use_tc(rows, heads, out_width, cache_rows, sms), rows, heads, out_width,
                              hidden, with_oabs, sms);
     const size_t need = f4_bytes(rows, heads, out_width, hidden, with_oabs, sms);
     if (need > 0 && (!workspace || workspace_bytes < need))
@@ -514,7 +624,9 @@ extern "C" int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int hea
               : p.mt == 1 ? launch_split<1>(a, p, st) : launch_split<2>(a, p, st);
     if (rc) return rc;
     if (p.ns > 1) {
-        rc = mla_combine_launch(a.part_o, a.part_ml, rows, heads, p.ns, olat, x16, st);
+        rc = p.ns <= 4   ? launch_merge<4>(a, olat, x16, st)
+             : p.ns <= 8 ? launch_merge<2>(a, olat, x16, st)
+                         : launch_merge<1>(a, olat, x16, st);
         if (rc) return rc;
     }
     if (with_oabs)

@@ -54,42 +54,55 @@ __device__ __forceinline__ void page_release(int32_t* refs, long long num_pages,
     }
 }
 
-// Whether any of list[lo, hi) equals v (block-wide).
-__device__ __forceinline__ bool block_any_equal(const int32_t* list, int lo, int hi, int v) {
+// Whether list[0, i) holds a, or list[0, n) holds b (block-wide).
+__device__ __forceinline__ bool block_finds(const int32_t* list, int i, int a, int n, int b) {
     bool hit = false;
-    for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) hit = hit || __ldg(list + j) == v;
+    for (int j = threadIdx.x; j < max(i, n); j += blockDim.x) {
+        const int v = __ldg(list + j);
+        hit = hit || (j < i && v == a) || (j < n && v == b);
+    }
     return __syncthreads_or(hit) != 0;
 }
 
-// Exclusive scan of one int per thread over the block; *total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int* total) {
+// Two sums at once: the high and the low 32 bits (each sum below 2^31).
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair_of(int hi, int lo) {
+    return ((Pair)(uint32_t)hi << 32) | (uint32_t)lo;
+}
+__device__ __forceinline__ int pair_hi(Pair p) { return (int)(p >> 32); }
+__device__ __forceinline__ int pair_lo(Pair p) { return (int)(uint32_t)p; }
+
+// Exclusive scan of one pair per thread over the block; *total gets the sum.
+__device__ __forceinline__ Pair block_scan(Pair v, Pair* warp_sums, Pair* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int x = v;
+    Pair x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        const Pair y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();  // warp_sums is reused by consecutive calls
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    int w = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
+    Pair w = warp_sums[lane];
+    static_assert(kPlanThreads == 1024, "a lane per warp sum");
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, w, o);
+        const Pair y = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o) w += y;
     }
     *total = __shfl_sync(0xffffffffu, w, 31);
-    const int before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
+    const Pair before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
     return before + x - v;
 }
 
-// Every CTA's value to all CTAs of the cluster: before = the sum over lower ranks, *all
-// = the sum over the cluster. slot: a [kPlanCtas] array used by this exchange alone.
-__device__ __forceinline__ int cluster_scan(cg::cluster_group& cl, int v, int* slot, int* all) {
+// Every CTA's value to all CTAs of the cluster: returns the sum over lower ranks, *all is
+// the sum over the cluster. slot: a [kPlanCtas] array used by this exchange alone.
+__device__ __forceinline__ Pair cluster_scan(cg::cluster_group& cl, Pair v, Pair* slot,
+                                             Pair* all) {
     if (threadIdx.x < kPlanCtas) cl.map_shared_rank(slot, threadIdx.x)[cl.block_rank()] = v;
     cl.sync();
-    int before = 0, sum = 0;
+    Pair before = 0, sum = 0;
 #pragma unroll
     for (int k = 0; k < kPlanCtas; ++k) {
         if (k < (int)cl.block_rank()) before += slot[k];
@@ -122,37 +135,66 @@ struct PageArrays {
     int first[DSA_MAX_PAGE_ARRAYS];        // index of the array's first piece
 };
 
-// One piece of one page copied by a warp.
-__device__ __forceinline__ void copy_piece(const PageArrays& A, int piece, long long src,
+// A warp's walk over pieces: pair (which copied page), piece within the page, and the array
+// that holds it. Consecutive pieces cost additions only; the start a division and a search.
+struct PieceWalk {
+    int pair, piece, array;
+    __device__ __forceinline__ PieceWalk(const PageArrays& A, long long u) {
+        const int per = max(A.pieces, 1);
+        pair = (int)(u / per);
+        piece = (int)(u - (long long)pair * per);
+        int lo = 0, hi = A.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (A.first[mid] <= piece)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        array = lo;
+    }
+    __device__ __forceinline__ void next(const PageArrays& A) {
+        if (++piece >= max(A.pieces, 1)) {
+            piece = 0;
+            array = 0;
+            ++pair;
+        } else if (array + 1 < A.n && A.first[array + 1] == piece) {
+            ++array;
+        }
+    }
+};
+// The walk's piece of page src to page dst, by a warp.
+__device__ __forceinline__ void copy_piece(const PageArrays& A, const PieceWalk& w, long long src,
                                            long long dst) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = A.n - 1;
-    while (lo < hi) {  // the array whose pieces hold this one
-        const int mid = (lo + hi + 1) >> 1;
-        if (A.first[mid] <= piece)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    const long long stride = A.bytes[lo] < 0 ? -A.bytes[lo] : A.bytes[lo];
-    const long long off = (long long)(piece - A.first[lo]) * kPiece;
+    const long long bytes = A.bytes[w.array];
+    const long long stride = bytes < 0 ? -bytes : bytes;
+    const long long off = (long long)(w.piece - A.first[w.array]) * kPiece;
     const int n = (int)min((long long)kPiece, stride - off);
-    const uint8_t* s = A.base[lo] + src * stride + off;
-    uint8_t* d = A.base[lo] + dst * stride + off;
-    if (A.bytes[lo] >= 0) {
+    const uint8_t* s = A.base[w.array] + src * stride + off;
+    uint8_t* d = A.base[w.array] + dst * stride + off;
+    if (bytes >= 0) {
         const uint4* s4 = reinterpret_cast<const uint4*>(s);
         uint4* d4 = reinterpret_cast<uint4*>(d);
         const int m = n / 16;
         uint4 v[kPiece / 512];
 #pragma unroll
         for (int k = 0; k < kPiece / 512; ++k)
-            if (lane + 32 * k < m) v[k] = s4[lane + 32 * k];
+            if (lane + 32 * k < m) v[k] = __ldcs(s4 + lane + 32 * k);
 #pragma unroll
         for (int k = 0; k < kPiece / 512; ++k)
-            if (lane + 32 * k < m) d4[lane + 32 * k] = v[k];
+            if (lane + 32 * k < m) __stcs(d4 + lane + 32 * k, v[k]);
     } else {
         for (int i = lane; i < n; i += 32) d[i] = s[i];
     }
+}
+// This warp's share [*u0, *u1) of `total` pieces: equal runs of consecutive ones.
+__device__ __forceinline__ void warp_share(long long total, long long* u0, long long* u1) {
+    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
+    const long long w = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+    const long long each = (total + warps - 1) / warps;
+    *u0 = min(total, w * each);
+    *u1 = min(total, *u0 + each);
 }
 
 // ---------------------------------------------------------------------------
@@ -168,6 +210,7 @@ struct SeqArgs {
 };
 
 __global__ void __launch_bounds__(kRowThreads) pages_free_kernel(SeqArgs a) {
+    pdl_trigger();  // short kernels that often follow one another: the next may be resident
     pdl_wait();
     const int i = blockIdx.x;
     const int b = __ldg(a.list + i);
@@ -176,7 +219,7 @@ __global__ void __launch_bounds__(kRowThreads) pages_free_kernel(SeqArgs a) {
         if (threadIdx.x == 0) flag_status(a.status, DSA_STATUS_BAD_SEQ);
         return;
     }
-    if (block_any_equal(a.list, 0, i, b)) return;  // listed before: freed by that entry
+    if (block_finds(a.list, i, b, 0, 0)) return;  // listed before: freed by that entry
     int32_t* row = a.table + (long long)b * a.pg.max_blocks;
     const int e1 = min(a.pg.max_blocks, ((int)blockIdx.y + 1) * kRowChunk);
     for (int e = blockIdx.y * kRowChunk + threadIdx.x; e < e1; e += kRowThreads) {
@@ -189,14 +232,14 @@ __global__ void __launch_bounds__(kRowThreads) pages_free_kernel(SeqArgs a) {
 }
 
 __global__ void __launch_bounds__(kRowThreads) pages_fork_kernel(SeqArgs a) {
+    pdl_trigger();
     pdl_wait();
     const int i = blockIdx.x;
     const int c = __ldg(a.list + i), p = __ldg(a.parents + i);
     if (c == -1) return;  // padding
     bool bad = c < 0 || c >= a.pg.batch || p < 0 || p >= a.pg.batch;
     // a child twice (the first pair counts), or a parent that the call overwrites
-    bad = block_any_equal(a.list, 0, i, c) || bad;
-    bad = block_any_equal(a.list, 0, a.n, p) || bad;
+    bad = block_finds(a.list, i, c, a.n, p) || bad;
     if (bad) {
         if (threadIdx.x == 0) flag_status(a.status, DSA_STATUS_BAD_SEQ);
         return;
@@ -292,17 +335,29 @@ __device__ __forceinline__ int entry_need(const ReserveArgs& a, const Window& w,
     return 0;
 }
 
-// G lanes per sequence (1 or 32): 32 where a call's window spans many pages.
-template <int G>
+// G lanes per sequence (1 or 32): 32 where a call's window spans many pages. With one lane
+// and at most one sequence per thread (kOne), what the first look at a sequence found
+// stays in registers. The free pages are counted from loads issued before the sequences
+// are looked at, and both sums travel together, so that a decode step's reservation waits
+// for one chain of loads (length, table entry, count), one exchange and one barrier.
+template <int G, bool kOne>
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads, 1)
     pages_reserve_kernel(ReserveArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();  // every CTA has started: their shared memory may be written
+    pdl_trigger();
     pdl_wait();
-    __shared__ int warp_sums[kPlanThreads / 32];
-    __shared__ int slots[2][kPlanCtas];
+    __shared__ Pair warp_sums[kPlanThreads / 32];
+    __shared__ Pair slots[kPlanCtas];
     const int rank = cl.block_rank();
     const int t = threadIdx.x;
+
+    // this CTA's slice of the counts; its first tile stays in registers
+    const long long num = a.pg.num_blocks;
+    const long long slice = ((num + kPlanCtas - 1) / kPlanCtas + 3) & ~3LL;
+    const long long s0 = min(num, rank * slice), s1 = min(num, s0 + slice);
+    int4 c0 = make_int4(1, 1, 1, 1);
+    if (s0 + 4LL * t < s1) c0 = load_counts(a.refs, s0 + 4LL * t, s1, 1);
 
     if (a.list) {  // the first entry that names a sequence serves it
         for (int b = rank * kPlanThreads + t; b < a.pg.batch; b += kPlanCtas * kPlanThreads)
@@ -328,55 +383,67 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     const int sub = t % G;  // lane within the sequence's group
 
     // ---- pages that each sequence of this CTA's slice needs
-    for (int i = i0 + t / G; i < i1; i += kPlanThreads / G) {
-        const int b = seq_of(i);
-        int need = 0;
+    int mine_need = 0, seq = -1, lo0 = 0, page0 = -1;
+    uint32_t need_mask = 0;  // kOne: entries lo0 + bit; page0: the first one's page
+    int run = 0;             // !kOne: the slice's sum
+    if constexpr (kOne) {
         Window w;
-        if (b >= 0 && window_of(a, b, &w)) {
-            const int32_t* row = a.table + (long long)b * a.pg.max_blocks;
-            const int lo = w.p0 <= w.p1 ? min(w.p0, w.t0) : w.t0;
-            for (int j = lo + sub; j <= w.t1; j += G) {
+        if (i0 + t < i1 && (seq = seq_of(i0 + t)) >= 0 && window_of(a, seq, &w)) {
+            const int32_t* row = a.table + (long long)seq * a.pg.max_blocks;
+            lo0 = w.p0 <= w.p1 ? min(w.p0, w.t0) : w.t0;
+            for (int j = lo0; j <= w.t1; ++j) {
                 int page;
-                need += entry_need(a, w, row, j, &page) != 0 ? 1 : 0;
+                if (entry_need(a, w, row, j, &page) != 0) {
+                    if (need_mask == 0) page0 = page;
+                    need_mask |= 1u << (j - lo0);
+                }
             }
+            mine_need = __popc(need_mask);
         }
-        if (G > 1) need = __reduce_add_sync(0xffffffffu, need);
-        if (sub == 0) a.need[i] = need;
+    } else {
+        for (int i = i0 + t / G; i < i1; i += kPlanThreads / G) {
+            const int b = seq_of(i);
+            int need = 0;
+            Window w;
+            if (b >= 0 && window_of(a, b, &w)) {
+                const int32_t* row = a.table + (long long)b * a.pg.max_blocks;
+                const int lo = w.p0 <= w.p1 ? min(w.p0, w.t0) : w.t0;
+                for (int j = lo + sub; j <= w.t1; j += G) {
+                    int page;
+                    need += entry_need(a, w, row, j, &page) != 0 ? 1 : 0;
+                }
+            }
+            if (G > 1) need = __reduce_add_sync(0xffffffffu, need);
+            if (sub == 0) a.need[i] = need;
+        }
+        __syncthreads();
+        for (int i = i0; i < i1; i += kPlanThreads) {  // first ranks within the slice
+            const bool in = i + t < i1;
+            Pair total;
+            const Pair before = block_scan(pair_of(in ? a.need[i + t] : 0, 0), warp_sums, &total);
+            if (in) a.need[i + t] = run + pair_hi(before);
+            run += pair_hi(total);
+        }
+        mine_need = t == 0 ? run : 0;
     }
-    __syncthreads();
-    // ---- first ranks within the slice, then over the cluster
-    int run = 0;
-    for (int i = i0; i < i1; i += kPlanThreads) {
-        const bool in = i + t < i1;
-        int total;
-        const int before = block_scan(in ? a.need[i + t] : 0, warp_sums, &total);
-        if (in) a.need[i + t] = run + before;
-        run += total;
+
+    // ---- needs and free pages summed over the block and the cluster
+    const int free0 = (c0.x == 0) + (c0.y == 0) + (c0.z == 0) + (c0.w == 0);
+    int mine_free = free0;
+    for (long long p = s0 + 4LL * (kPlanThreads + t); p < s1; p += 4LL * kPlanThreads) {
+        const int4 c = load_counts(a.refs, p, s1, 1);
+        mine_free += (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0);
     }
-    int want;
-    const int base = cluster_scan(cl, run, slots[0], &want);
-    if (rank == 0 && t == 0) *a.count = (int)min((long long)want, a.pg.num_blocks);
+    Pair here, all;
+    const Pair mine = block_scan(pair_of(mine_need, mine_free), warp_sums, &here);
+    const Pair before = cluster_scan(cl, here, slots, &all);
+    const int want = pair_hi(all), free_all = pair_lo(all), base = pair_hi(before);
+    if (rank == 0 && t == 0) *a.count = (int)min((long long)want, num);
     if (want == 0) return;  // every CTA of the cluster agrees
 
-    // ---- free pages: counted per slice, then listed in ascending order up to `want`
-    const long long num = a.pg.num_blocks;
-    const long long slice = ((num + kPlanCtas - 1) / kPlanCtas + 3) & ~3LL;
-    const long long s0 = min(num, rank * slice), s1 = min(num, s0 + slice);
-    int mine = 0;
-    for (long long p = s0 + 4LL * t; p < s1; p += 4LL * kPlanThreads) {
-        const int4 c = load_counts(a.refs, p, s1, 1);
-        mine += (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0);
-    }
-    int free_here, free_all;
-    block_scan(mine, warp_sums, &free_here);
-    int at = cluster_scan(cl, free_here, slots[1], &free_all);
-    for (long long p = s0; p < s1 && at < want; p += 4LL * kPlanThreads) {
-        const long long q = p + 4LL * t;
-        int4 c = make_int4(1, 1, 1, 1);
-        if (q < s1) c = load_counts(a.refs, q, s1, 1);
-        const int n = (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0);
-        int total;
-        int r = at + block_scan(n, warp_sums, &total);
+    // ---- free pages in ascending order, up to `want`
+    int at = pair_lo(before);
+    auto list_free = [&](const int4& c, long long q, int r) {
         if (c.x == 0 && r < want) a.free_list[r] = (int)q;
         r += c.x == 0;
         if (c.y == 0 && r < want) a.free_list[r] = (int)q + 1;
@@ -384,51 +451,86 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
         if (c.z == 0 && r < want) a.free_list[r] = (int)q + 2;
         r += c.z == 0;
         if (c.w == 0 && r < want) a.free_list[r] = (int)q + 3;
-        at += total;
+    };
+    if (slice <= 4LL * kPlanThreads) {
+        list_free(c0, s0 + 4LL * t, at + pair_lo(mine));
+    } else {
+        for (long long p = s0; p < s1 && at < want; p += 4LL * kPlanThreads) {
+            const long long q = p + 4LL * t;
+            int4 c = make_int4(1, 1, 1, 1);
+            if (q < s1) c = load_counts(a.refs, q, s1, 1);
+            Pair total;
+            const Pair r = block_scan(
+                pair_of(0, (c.x == 0) + (c.y == 0) + (c.z == 0) + (c.w == 0)), warp_sums, &total);
+            list_free(c, q, at + pair_lo(r));
+            at += pair_lo(total);
+        }
     }
     cl.sync();  // the list is complete and visible to the cluster
 
-    // ---- hand the pages out. Counts of shared pages are lowered by the apply step, so
-    // that every decision here sees the counts the needs were taken from.
-    for (int i = i0 + t / G; i < i1; i += kPlanThreads / G) {
-        const int b = seq_of(i);
-        Window w;
-        if (b < 0 || !window_of(a, b, &w)) continue;
-        int32_t* row = a.table + (long long)b * a.pg.max_blocks;
-        const int lo = w.p0 <= w.p1 ? min(w.p0, w.t0) : w.t0;
-        const int r0 = base + a.need[i];
-        // all of the sequence's pages, or none: the first pass decides, the second writes
-        int total = 0;
-        for (int pass = 0; pass < 2; ++pass) {
-            const bool granted = r0 + total <= free_all;
-            int k = 0;
-            for (int j0 = lo; j0 <= w.t1; j0 += G) {
-                const int j = j0 + sub;
-                int page = -1;
-                const int kind = j <= w.t1 ? entry_need(a, w, row, j, &page) : 0;
-                int mineat = k, step = kind != 0 ? 1 : 0;
-                if (G > 1) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, kind != 0);
-                    mineat = k + __popc(m & ((1u << sub) - 1u));
-                    step = __popc(m);
-                }
-                if (pass == 1 && kind != 0) {
-                    const int r = r0 + mineat;
-                    if (granted) {
-                        const int fresh = __ldcg(a.free_list + r);
-                        row[j] = fresh;
-                        a.refs[fresh] = 1;
-                        a.src[r] = kind == 2 ? page : -1;
-                    } else if (r < num) {
-                        a.src[r] = -1;
-                    }
-                }
-                k += step;
+    // ---- hand the pages out: all of a sequence's, or none. Counts of shared pages are
+    // lowered by the apply step, so that every decision here sees the counts the needs were
+    // taken from.
+    if constexpr (kOne) {
+        if (mine_need == 0) return;
+        int32_t* row = a.table + (long long)seq * a.pg.max_blocks;
+        int r = base + pair_hi(mine);
+        const bool granted = r + mine_need <= free_all;
+        if (!granted) flag_status(a.status, DSA_STATUS_NO_PAGES);
+        bool first = true;
+        for (uint32_t m = need_mask; m != 0; m &= m - 1, ++r, first = false) {
+            const int j = lo0 + __ffs(m) - 1;
+            const int page = first ? page0 : row[j];
+            if (granted) {
+                const int fresh = __ldcg(a.free_list + r);
+                row[j] = fresh;
+                a.refs[fresh] = 1;
+                a.src[r] = page;  // -1: an unmapped entry, nothing to copy
+            } else if (r < num) {
+                a.src[r] = -1;
             }
-            if (pass == 0) total = k;
         }
-        if (r0 + total > free_all && total > 0 && sub == 0)
-            flag_status(a.status, DSA_STATUS_NO_PAGES);
+    } else {
+        for (int i = i0 + t / G; i < i1; i += kPlanThreads / G) {
+            const int b = seq_of(i);
+            Window w;
+            if (b < 0 || !window_of(a, b, &w)) continue;
+            int32_t* row = a.table + (long long)b * a.pg.max_blocks;
+            const int lo = w.p0 <= w.p1 ? min(w.p0, w.t0) : w.t0;
+            const int r0 = base + a.need[i];
+            // the first pass counts, the second writes
+            int total = 0;
+            for (int pass = 0; pass < 2; ++pass) {
+                const bool granted = r0 + total <= free_all;
+                int k = 0;
+                for (int j0 = lo; j0 <= w.t1; j0 += G) {
+                    const int j = j0 + sub;
+                    int page = -1;
+                    const int kind = j <= w.t1 ? entry_need(a, w, row, j, &page) : 0;
+                    int mineat = k, step = kind != 0 ? 1 : 0;
+                    if (G > 1) {
+                        const uint32_t m = __ballot_sync(0xffffffffu, kind != 0);
+                        mineat = k + __popc(m & ((1u << sub) - 1u));
+                        step = __popc(m);
+                    }
+                    if (pass == 1 && kind != 0) {
+                        const int r = r0 + mineat;
+                        if (granted) {
+                            const int fresh = __ldcg(a.free_list + r);
+                            row[j] = fresh;
+                            a.refs[fresh] = 1;
+                            a.src[r] = kind == 2 ? page : -1;
+                        } else if (r < num) {
+                            a.src[r] = -1;
+                        }
+                    }
+                    k += step;
+                }
+                if (pass == 0) total = k;
+            }
+            if (r0 + total > free_all && total > 0 && sub == 0)
+                flag_status(a.status, DSA_STATUS_NO_PAGES);
+        }
     }
 }
 
@@ -436,16 +538,14 @@ __global__ void __launch_bounds__(kCopyThreads)
     pages_reserve_apply(const __grid_constant__ PageArrays A, const int32_t* count,
                         const int32_t* dst, const int32_t* src, int32_t* refs) {
     pdl_wait();
-    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
-    const int n = *count;
-    const int per = max(A.pieces, 1);
-    for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
-         u < (long long)n * per; u += warps) {
-        const int r = (int)(u / per), piece = (int)(u - (long long)r * per);
-        const int s = __ldg(src + r);
+    long long u, end;
+    warp_share((long long)*count * max(A.pieces, 1), &u, &end);
+    if (u >= end) return;
+    for (PieceWalk w(A, u); u < end; ++u, w.next(A)) {
+        const int s = __ldg(src + w.pair);
         if (s < 0) continue;
-        if (piece == 0 && (threadIdx.x & 31) == 0) atomicSub(refs + s, 1);
-        if (piece < A.pieces) copy_piece(A, piece, s, __ldg(dst + r));
+        if (w.piece == 0 && (threadIdx.x & 31) == 0) atomicSub(refs + s, 1);
+        if (w.piece < A.pieces) copy_piece(A, w, s, __ldg(dst + w.pair));
     }
 }
 
@@ -470,32 +570,41 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
     pages_compact_kernel(CompactArgs a) {
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();  // every CTA has started: their shared memory may be written
+    pdl_trigger();
     pdl_wait();
-    __shared__ int warp_sums[kPlanThreads / 32];
-    __shared__ int slots[kPlanCtas];
+    __shared__ Pair warp_sums[kPlanThreads / 32];
+    __shared__ Pair slots[kPlanCtas];
     const int rank = cl.block_rank();
     const int t = threadIdx.x;
     const long long num = a.pg.num_blocks;
     const long long slice = ((num + kPlanCtas - 1) / kPlanCtas + 3) & ~3LL;
     const long long s0 = min(num, rank * slice), s1 = min(num, s0 + slice);
-    int mine = 0;
-    for (long long p = s0 + 4LL * t; p < s1; p += 4LL * kPlanThreads) {
-        const int4 c = load_counts(a.refs, p, s1, 0);
-        mine += (c.x > 0) + (c.y > 0) + (c.z > 0) + (c.w > 0);
-    }
-    int here, live;
-    block_scan(mine, warp_sums, &here);
-    int at = cluster_scan(cl, here, slots, &live);
+    auto live_in = [](const int4& c) { return (c.x > 0) + (c.y > 0) + (c.z > 0) + (c.w > 0); };
+    int4 c0 = make_int4(0, 0, 0, 0);  // the slice's first tile stays in registers
+    if (s0 + 4LL * t < s1) c0 = load_counts(a.refs, s0 + 4LL * t, s1, 0);
+    int mine = live_in(c0);
+    for (long long p = s0 + 4LL * (kPlanThreads + t); p < s1; p += 4LL * kPlanThreads)
+        mine += live_in(load_counts(a.refs, p, s1, 0));
+    Pair here, all;
+    const Pair scan0 = block_scan(pair_of(0, mine), warp_sums, &here);
+    int at = pair_lo(cluster_scan(cl, here, slots, &all));
+    const int live = pair_lo(all);
     // `before` live pages lie below page p: a free p < live is hole p - before, a live
     // p >= live has rank before; the moved pages are the last (live - those below `live`).
     for (long long p = s0; p < s1; p += 4LL * kPlanThreads) {
         const long long q = p + 4LL * t;
-        int4 c4 = make_int4(0, 0, 0, 0);
-        if (q < s1) c4 = load_counts(a.refs, q, s1, 0);
+        int4 c4 = c0;
+        int before = at + pair_lo(scan0);
+        if (slice > 4LL * kPlanThreads) {
+            if (p > s0) {
+                c4 = make_int4(0, 0, 0, 0);
+                if (q < s1) c4 = load_counts(a.refs, q, s1, 0);
+            }
+            Pair total;
+            before = at + pair_lo(block_scan(pair_of(0, live_in(c4)), warp_sums, &total));
+            at += pair_lo(total);
+        }
         const int c[4] = {c4.x, c4.y, c4.z, c4.w};
-        int total;
-        int before = at + block_scan((c[0] > 0) + (c[1] > 0) + (c[2] > 0) + (c[3] > 0), warp_sums,
-                                     &total);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const int page = (int)(q + k);
@@ -514,7 +623,6 @@ __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads
                 before += alive;
             }
         }
-        at += total;
     }
     if (rank == 0 && t == 0) {
         a.head[0] = live;
@@ -543,18 +651,17 @@ __global__ void __launch_bounds__(kCopyThreads)
         else
             a.table[e] = to;
     }
-    const long long warps = (long long)gridDim.x * (kCopyThreads / 32);
-    const int per = max(A.pieces, 1);
-    for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
-         u < (long long)moved * per; u += warps) {
-        const int k = (int)(u / per), piece = (int)(u - (long long)k * per);
-        const int s = a.live[first + k], d = a.hole[k];
-        if (piece == 0 && (threadIdx.x & 31) == 0) {
+    long long u, end;
+    warp_share((long long)moved * max(A.pieces, 1), &u, &end);
+    if (u >= end) return;
+    for (PieceWalk w(A, u); u < end; ++u, w.next(A)) {
+        const int s = a.live[first + w.pair], d = a.hole[w.pair];
+        if (w.piece == 0 && (threadIdx.x & 31) == 0) {
             a.refs[d] = a.refs[s];
             a.refs[s] = 0;
             if (a.remap) a.remap[s] = d;
         }
-        if (piece < A.pieces) copy_piece(A, piece, s, d);
+        if (w.piece < A.pieces) copy_piece(A, w, s, d);
     }
 }
 
@@ -751,9 +858,14 @@ extern "C" int dsa_pages_reserve(const int32_t* seqs, int n, const dsa_paging* p
     a.owner = reinterpret_cast<int32_t*>(ws + w.owner);
     cudaStream_t st = (cudaStream_t)stream;
     // one lane per sequence while its window is a few pages (a decode step), a warp where
-    // it may be many (the pages of a prompt)
+    // it may be many (the pages of a prompt); with one lane a sequence's entries, from its
+    // pooled-key page to its last token page, have to fit a mask to stay in registers
     const bool wide = new_tokens / a.pg.block_size >= 4;
-    auto plan = wide ? pages_reserve_kernel<32> : pages_reserve_kernel<1>;
+    const long long span = first_key / a.pg.block_size + new_tokens / a.pg.block_size + 3;
+    const bool one = !wide && (long long)n <= (long long)kPlanCtas * kPlanThreads && span <= 32;
+    auto plan = wide  ? pages_reserve_kernel<32, false>
+                : one ? pages_reserve_kernel<1, true>
+                      : pages_reserve_kernel<1, false>;
     cudaError_t e = launch_pdl(plan, dim3(kPlanCtas), dim3(kPlanThreads), 0, st, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_pages_reserve launch");
@@ -796,7 +908,7 @@ extern "C" int dsa_pages_compact(const dsa_paging* pg, int32_t* block_table, int
     cudaError_t e = launch_pdl(pages_compact_kernel, dim3(kPlanCtas), dim3(kPlanThreads), 0, st, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_pages_compact launch");
-    e = launch_pdl(pages_compact_apply, dim3((unsigned)sms * 4), dim3(kCopyThreads), 0, st, A, a);
+    e = launch_pdl(pages_compact_apply, dim3((unsigned)sms * 8), dim3(kCopyThreads), 0, st, A, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_pages_compact copy launch");
     return DSA_OK;

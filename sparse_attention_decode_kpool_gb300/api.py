@@ -444,8 +444,8 @@ _FP4_BLOCK = 16  # channels under one scale
 
 def _fp4_cache(codes, scales) -> int:
     """Channels of an FP4 latent cache (codes [.., kvl/2], scales [.., kvl/16])."""
-    kvl = 2 * int(codes.shape[-1])
-    if int(scales.shape[-1]) * _FP4_BLOCK != kvl or scales.numel() * 8 != codes.numel():
+    kvl = 2 * codes.size(-1)
+    if scales.size(-1) * _FP4_BLOCK != kvl or scales.numel() * 8 != codes.numel():
         raise ValueError("codes must be [.., kvl/2] and scales [.., kvl/16] of the same rows")
     return kvl
 
@@ -460,36 +460,41 @@ def _dev_ptr(t: Optional[torch.Tensor], dtype, dev: int, name: str) -> Optional[
     raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}: one device per call ({p:#x})")
 
 
+# The current device and its current stream by their raw handles: the GPU work of these
+# calls is often shorter than making a Stream object takes.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _run(dev: int, stream, fn, *args) -> None:
-    """One library call with device ``dev`` current, on its current stream by default (by
-    its raw handle: the GPU work of these calls is often shorter than making a Stream
-    object takes)."""
-    if torch._C._cuda_getDevice() != dev:
+    """One library call with device ``dev`` current, on its current stream by default."""
+    if _current_device() != dev:
         with torch.cuda.device(dev):
             check(fn(*args, _stream(stream)))
         return
-    rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    rc = fn(*args, _current_stream(dev) if stream is None else _stream(stream))
     if rc:
         check(rc)
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+    return dev
 
 
 def dsa_quantize_latent_fp4(x, codes, scales, cache_exp: int = 0, stream=None) -> None:
     """FP4 latent cache from bf16 rows: codes [..., kvl/2] u8 (two E2M1 codes a byte),
     scales [..., kvl/16] u8 (E4M3), under 2^cache_exp (see include/dsa.h)."""
-    kvl = int(x.shape[-1])
-    if _fp4_cache(codes, scales) != kvl or codes.numel() * 2 != x.numel():
+    kvl, n = x.size(-1), x.numel()
+    if _fp4_cache(codes, scales) != kvl or codes.numel() * 2 != n:
         raise ValueError("codes [.., kvl/2] and scales [.., kvl/16] must match x [.., kvl]")
-    if x.numel() == 0:
+    if n == 0:
         return
     dev = _device_of(x, "x")
     _run(dev, stream, _lib.load().dsa_quantize_latent_fp4,
-         _dev_ptr(x, torch.bfloat16, dev, "x"), x.numel() // kvl, kvl, int(cache_exp),
+         _dev_ptr(x, torch.bfloat16, dev, "x"), n // kvl, kvl, int(cache_exp),
          _dev_ptr(codes, torch.uint8, dev, "codes"), _dev_ptr(scales, torch.uint8, dev, "scales"))
 
 
@@ -498,7 +503,7 @@ def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None,
     """Rows of an FP4 latent cache back as bf16, exactly: all of them in order, or the
     cache rows named by ``rows`` (i32, one per row of out)."""
     kvl = _fp4_cache(codes, scales)
-    if int(out.shape[-1]) != kvl:
+    if out.size(-1) != kvl:
         raise ValueError(f"out must be [.., {kvl}]")
     n, cache_rows = out.numel() // kvl, codes.numel() * 2 // kvl
     if rows is not None and rows.numel() != n:
@@ -521,11 +526,12 @@ def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float,
     """dsa_decode_append that also encodes the staged latent row into the FP4 cache
     (same codec and bytes as dsa_quantize_latent_fp4); the bf16 cache ``ckv`` is
     optional."""
-    batch, ihd = (int(x) for x in k_new.shape)
-    if tuple(gate_new.shape) != (batch, ihd):
+    batch, ihd = k_new.shape
+    if gate_new.shape != k_new.shape:
         raise ValueError(f"gate_new must be [{batch}, {ihd}]")
-    kvl = int(ckv_new.shape[-1])
-    if tuple(ckv_new.shape) != (batch, kvl) or _fp4_cache(ckv_codes, ckv_scales) != kvl:
+    kvl = ckv_new.size(-1)
+    if (ckv_new.dim() != 2 or ckv_new.size(0) != batch
+            or _fp4_cache(ckv_codes, ckv_scales) != kvl):
         raise ValueError(f"ckv_new must be [{batch}, kvl], ckv_codes [.., kvl/2] and "
                          "ckv_scales [.., kvl/16]")
     if batch != pg.batch:
@@ -560,10 +566,10 @@ def dsa_sparse_mla_decode_fp4(qlat, row_seq, ckv_codes, ckv_scales, cache_exp: i
                               stream=None) -> None:
     """dsa_sparse_mla_decode over an FP4 latent cache (see dsa_quantize_latent_fp4).
     ``olat`` [rows, heads, 512] may be float32 or bfloat16."""
-    rows, heads, kvl = (int(x) for x in qlat.shape)
-    if token_ids.dim() != 2 or int(token_ids.shape[0]) != rows:
+    rows, heads, kvl = qlat.shape
+    if token_ids.dim() != 2 or token_ids.size(0) != rows:
         raise ValueError(f"token_ids must be [{rows}, out_width]")
-    ow = int(token_ids.shape[1])
+    ow = token_ids.size(1)
     if _fp4_cache(ckv_codes, ckv_scales) != kvl:
         raise ValueError(f"ckv_codes must be [.., {kvl // 2}] and ckv_scales [.., {kvl // 16}]")
     need = (pg.num_blocks * pg.block_size if pg.block_table else pg.batch * pg.max_seq_len)
@@ -577,7 +583,7 @@ def dsa_sparse_mla_decode_fp4(qlat, row_seq, ckv_codes, ckv_scales, cache_exp: i
         raise ValueError(f"o_absorb must be [hidden, {heads * kvl}]")
     if y is not None and tuple(y.shape) != (rows, hidden):
         raise ValueError(f"y must be [{rows}, {hidden}]")
-    if olat is not None and tuple(olat.shape) != (rows, heads, kvl):
+    if olat is not None and olat.shape != qlat.shape:
         raise ValueError(f"olat must be [{rows}, {heads}, {kvl}]")
     if olat is not None and olat.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"olat must be float32 or bfloat16, got {olat.dtype}")
@@ -623,7 +629,7 @@ def dsa_pages_workspace(num_blocks: int, batch: int) -> int:
 
 def _pool(pg: DsaPaging, block_table, refs) -> int:
     """The pool's device."""
-    if tuple(block_table.shape) != (pg.batch, pg.max_blocks):
+    if block_table.shape != (pg.batch, pg.max_blocks):
         raise ValueError(f"block_table must be [{pg.batch}, {pg.max_blocks}]")
     if refs.numel() != pg.num_blocks:
         raise ValueError(f"refs must be [{pg.num_blocks}]")

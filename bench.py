@@ -8,7 +8,7 @@ flushed (a 256 MiB write) between timed steps, outside the timed events.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
                   [--workload 3] [--no-cpu-baseline] [--no-e2e] [--always-select-tail]
-                  [--decode-append] [--latent-fp8] [--frontend [--q-lora-rank Q]]
+                  [--decode-append] [--latent-fp8 | --latent-fp4] [--frontend [--q-lora-rank Q]]
 
 --impl reference times the CPU oracle (the plain float64 restatement of the
 method) on the host, one query row per step, single-threaded.
@@ -164,6 +164,15 @@ class ClockSampler:
 # algorithmic bytes (the roofline numerator)
 
 
+def latent_row_bytes(layer) -> int:
+    """Bytes of a cached latent row: bf16, E4M3 codes plus one f32 scale per 128 channels,
+    or E2M1 codes (two a byte) plus one E4M3 scale per 16 channels."""
+    kvl = layer.geom.kv_lora_rank
+    if layer.latent_fp4:
+        return kvl // 2 + kvl // 16
+    return kvl + kvl // 128 * 4 if layer.latent_fp8 else kvl * 2
+
+
 def algorithmic_bytes(wl, layer) -> dict:
     """Per step: pooled keys of candidate pools + pool flags, indexer q and w,
     selected latent rows, absorbed Q, o_absorb once, the output."""
@@ -183,9 +192,7 @@ def algorithmic_bytes(wl, layer) -> dict:
     keys = cand * g.index_head_dim * 2
     q = wl.rows * g.index_heads * (g.index_head_dim * 2 + 4)
     sel_tokens = int((layer.token_ids >= 0).sum().item())
-    # a gathered latent row: bf16, or E4M3 codes plus one f32 scale per 128 channels
-    row_bytes = (g.kv_lora_rank + g.kv_lora_rank // 128 * 4 if layer.latent_fp8
-                 else g.kv_lora_rank * 2)
+    row_bytes = latent_row_bytes(layer)
     latent = sel_tokens * row_bytes
     qlat = wl.rows * g.heads * g.kv_lora_rank * 2
     oabs = g.hidden * g.heads * g.kv_lora_rank * 2 if layer.o_absorb is not None else 0
@@ -198,9 +205,7 @@ def algorithmic_bytes(wl, layer) -> dict:
     app = 0
     if layer.decode_from is not None:
         ihd, kp = g.index_head_dim, g.index_kpool
-        # the latent row goes out as bf16, or (FP8 cache) as codes and scales
-        ckv_out = (g.kv_lora_rank + g.kv_lora_rank // 128 * 4 if layer.latent_fp8
-                   else g.kv_lora_rank * 2)
+        ckv_out = latent_row_bytes(layer)  # the latent row in the cache's format
         app = wl.batch * ((2 * ihd + g.kv_lora_rank) * 2 + 2 * ihd * 2 + ckv_out + 1
                           + kp * (2 * ihd * 2 + 1) + ihd * 2 + 1)
     # --frontend: every front-end weight once, the hidden state in, and its outputs
@@ -269,12 +274,13 @@ class OracleRunner:
     """Times the oracle's decode_row on rows of the workload. The oracle's own
     pooled-key cache of a sequence is built once, untimed (it is layer state)."""
 
-    def __init__(self, wl, with_project: bool = True, latent_fp8: bool = False):
+    def __init__(self, wl, with_project: bool = True, latent_fp8: bool = False,
+                 latent_fp4: bool = False):
         from oracle import dsa_oracle as O
 
         self.O, self.wl = O, wl
         self.with_project = with_project
-        self.latent_fp8 = latent_fp8
+        self.latent_fp8, self.latent_fp4 = latent_fp8, latent_fp4
         self._pools = {}
         self._A = None
 
@@ -300,6 +306,9 @@ class OracleRunner:
             ckv = self._tokens(wl.ckv, b)
             if self.latent_fp8:  # the FP8 cache, encoded and decoded once (layer state)
                 ckv = O.dequantize_latent_fp8(*O.quantize_latent_fp8(ckv))
+            if self.latent_fp4:  # the FP4 cache likewise, 4,096 rows at a time
+                ckv = np.concatenate([O.dequantize_latent_fp4(*O.quantize_latent_fp4(c, -8), -8)
+                                      for c in np.array_split(ckv, -(-len(ckv) // 4096))])
             self._pools[b] = (keys, pv, ckv)
         if self._A is None and wl.o_absorb is not None and self.with_project:
             self._A = wl.o_absorb.float().numpy()
@@ -320,9 +329,11 @@ class OracleRunner:
         return time.perf_counter() - t0
 
 
-def cpu_baseline(wl, budget_s: float = 12.0, max_rows: int = 2, latent_fp8: bool = False) -> dict:
+def cpu_baseline(wl, budget_s: float = 12.0, max_rows: int = 2, latent_fp8: bool = False,
+                 latent_fp4: bool = False) -> dict:
     prefill = wl.name.startswith("prefill")
-    runner = OracleRunner(wl, with_project=not prefill, latent_fp8=latent_fp8)
+    runner = OracleRunner(wl, with_project=not prefill, latent_fp8=latent_fp8,
+                          latent_fp4=latent_fp4)
     # one thread, held on one core for the timed rows
     old_aff = os.sched_getaffinity(0) if hasattr(os, "sched_getaffinity") else None
     core = min(old_aff) if old_aff else None
@@ -373,7 +384,8 @@ def run_reference(args, ws, rank):
         return
     wl = make_wl(args)
     prefill = args.workload == PREFILL_WORKLOAD
-    runner = OracleRunner(wl, with_project=not prefill, latent_fp8=args.latent_fp8)
+    runner = OracleRunner(wl, with_project=not prefill, latent_fp8=args.latent_fp8,
+                          latent_fp4=args.latent_fp4)
     rows = [r % wl.rows for r in range(min(2, wl.rows))]
     for r in rows:
         runner._prep(r)
@@ -414,7 +426,8 @@ def workload_config(wl, args) -> dict:
             "paged_block": wl.block_size, "seed": wl.seed,
             "always_select_tail": bool(g.always_select_tail),
             "decode_append": bool(getattr(args, "decode_append", False)),
-            "latent_cache": "fp8-e4m3" if getattr(args, "latent_fp8", False) else "bf16",
+            "latent_cache": ("fp8-e4m3" if getattr(args, "latent_fp8", False)
+                             else "fp4-e2m1" if getattr(args, "latent_fp4", False) else "bf16"),
             "frontend": ({"q_lora_rank": args.q_lora_rank}
                          if getattr(args, "frontend", False) else None),
             "o_absorb_l2_prefetch_mib": getattr(args, "l2_prefetch_mib_used", 0.0),
@@ -446,6 +459,9 @@ def main():
     ap.add_argument("--latent-fp8", action="store_true",
                     help="attention reads an FP8 latent cache (E4M3 codes + power-of-two "
                          "scales per 128 channels) encoded once from the bf16 cache")
+    ap.add_argument("--latent-fp4", action="store_true",
+                    help="attention reads an FP4 latent cache (E2M1 codes + E4M3 scales per "
+                         "16 channels under 2^-8) encoded once from the bf16 cache")
     ap.add_argument("--l2-prefetch-mb", type=float, default=None,
                     help="MiB of o_absorb prefetched into L2 on a second graph branch "
                          "while top-k and the gather run (default: the layer's choice, "
@@ -488,6 +504,7 @@ def main():
         fe = W.make_frontend(wl.geom, wl.rows, q_lora_rank=args.q_lora_rank, seed=wl.seed + 100)
     layer = DsaDecodeLayer(wl, device=str(dev), with_o_absorb=not prefill, keep_olat=prefill,
                            decode_from=decode_from, latent_fp8=args.latent_fp8, frontend=fe,
+                           latent_fp4=args.latent_fp4, fp4_exp=-8,
                            l2_prefetch_bytes=(None if args.l2_prefetch_mb is None
                                               else int(args.l2_prefetch_mb * (1 << 20))))
     args.l2_prefetch_mib_used = layer.l2_prefetch_bytes / (1 << 20)
@@ -864,7 +881,8 @@ def main():
     if e2e is not None:
         line["e2e"] = e2e
     if not args.no_cpu_baseline and ws == 1:
-        line["cpu_baseline"] = cpu_baseline(wl, latent_fp8=args.latent_fp8)
+        line["cpu_baseline"] = cpu_baseline(wl, latent_fp8=args.latent_fp8,
+                                            latent_fp4=args.latent_fp4)
     print(json.dumps(line), flush=True)
 
 

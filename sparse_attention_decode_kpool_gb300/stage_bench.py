@@ -7,7 +7,7 @@ Stages: compress, score, select, expand, attend, project, step, append, frontend
 quantize. ``--rows`` shrinks the prefill chunk (workload 4), ``--seq-len`` the
 long-context sequences (workload 3) or caps the paged lengths (workload 2);
 ``--always-select-tail`` widens the index rows by the trailing partial pool;
-``--latent-fp8`` gives attention the FP8 latent cache. Workload 5 is a contiguous
+``--latent-fp8`` (``--latent-fp4``) gives attention the FP8 (FP4) latent cache. Workload 5 is a contiguous
 batch of ``--batch`` sequences of ``--seq-len`` tokens whose geometry ``--geom
 key=value`` overrides (e.g. index_heads=64, hidden=96). ``--unfused`` runs expand
 and append as separate calls; ``--select-kernel``, ``--mla-kernel`` and
@@ -70,6 +70,7 @@ def main(argv=None) -> None:
     ap.add_argument("--warmup", type=int, default=1)
     ap.add_argument("--always-select-tail", action="store_true")
     ap.add_argument("--latent-fp8", action="store_true")
+    ap.add_argument("--latent-fp4", action="store_true")
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--geom", action="append", default=[])
     ap.add_argument("--unfused", action="store_true")
@@ -95,7 +96,8 @@ def main(argv=None) -> None:
         kw["fuse_append"] = not args.unfused
     if args.stage == "frontend":
         kw["frontend"] = W.make_frontend(wl.geom, wl.rows, seed=wl.seed + 100)
-    layer = DsaDecodeLayer(wl, latent_fp8=args.latent_fp8, fuse_expand=not args.unfused, **kw)
+    layer = DsaDecodeLayer(wl, latent_fp8=args.latent_fp8, latent_fp4=args.latent_fp4,
+                           fuse_expand=not args.unfused, **kw)
     layer.compress()
     if args.stage == "append":
         layer.stage(0)
@@ -105,9 +107,13 @@ def main(argv=None) -> None:
     torch.cuda.synchronize()
     if args.stage == "quantize":
         if layer.ckv_codes is None:
-            raise SystemExit("--stage quantize needs --latent-fp8")
-        layer.quantize = lambda: api.dsa_quantize_latent(layer.ckv, layer.ckv_codes,
-                                                          layer.ckv_scales)
+            raise SystemExit("--stage quantize needs --latent-fp8 or --latent-fp4")
+        if args.latent_fp4:
+            layer.quantize = lambda: api.dsa_quantize_latent_fp4(
+                layer.ckv, layer.ckv_codes, layer.ckv_scales, layer.fp4_exp)
+        else:
+            layer.quantize = lambda: api.dsa_quantize_latent(layer.ckv, layer.ckv_codes,
+                                                              layer.ckv_scales)
     flush_w = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
     flush_r = torch.ones(64 << 20, dtype=torch.float32, device="cuda")
     fn = getattr(layer, args.stage)

@@ -102,7 +102,8 @@ typedef struct dsa_paging {
  */
 typedef struct dsa_page_arrays {
     int32_t n;
-    int32_t reserved; /* 0 */
+    int32_t reserved;  /* 0 */
+    int64_t num_pages; /* of every cache; has to be the paging descriptor's num_blocks */
     void* base[DSA_MAX_PAGE_ARRAYS];
     int64_t page_bytes[DSA_MAX_PAGE_ARRAYS];
 } dsa_page_arrays;

@@ -57,6 +57,7 @@ class DsaPageArrays(ctypes.Structure):
     _fields_ = [
         ("n", ctypes.c_int32),
         ("reserved", ctypes.c_int32),
+        ("num_pages", ctypes.c_int64),
         ("base", ctypes.c_void_p * DSA_MAX_PAGE_ARRAYS),
         ("page_bytes", ctypes.c_int64 * DSA_MAX_PAGE_ARRAYS),
     ]

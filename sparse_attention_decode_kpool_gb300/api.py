@@ -450,6 +450,14 @@ def _fp4_cache(codes, scales) -> int:
     return kvl
 
 
+def _fp4_covers(codes, kvl: int, pg: DsaPaging) -> None:
+    """The cache holds every row that the paging descriptor can name."""
+    need = pg.num_blocks * pg.block_size if pg.block_table else pg.batch * pg.max_seq_len
+    if codes.numel() * 2 < need * kvl:
+        raise ValueError(f"the cache holds {codes.numel() * 2 // kvl} rows, the paging "
+                         f"descriptor names {need}")
+
+
 def _dev_ptr(t: Optional[torch.Tensor], dtype, dev: int, name: str) -> Optional[int]:
     """_ptr for the calls whose tensors must all live on one device, ``dev``."""
     if t is None:
@@ -536,6 +544,7 @@ def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float,
                          "ckv_scales [.., kvl/16]")
     if batch != pg.batch:
         raise ValueError(f"one staged row per sequence: {batch} rows, {pg.batch} sequences")
+    _fp4_covers(ckv_codes, kvl, pg)
     dev = _device_of(k_new, "k_new")
     bf16, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
     _run(dev, stream, _lib.load().dsa_decode_append_fp4,
@@ -572,10 +581,7 @@ def dsa_sparse_mla_decode_fp4(qlat, row_seq, ckv_codes, ckv_scales, cache_exp: i
     ow = token_ids.size(1)
     if _fp4_cache(ckv_codes, ckv_scales) != kvl:
         raise ValueError(f"ckv_codes must be [.., {kvl // 2}] and ckv_scales [.., {kvl // 16}]")
-    need = (pg.num_blocks * pg.block_size if pg.block_table else pg.batch * pg.max_seq_len)
-    if ckv_codes.numel() * 2 < need * kvl:
-        raise ValueError(f"the cache holds {ckv_codes.numel() * 2 // kvl} rows, the paging "
-                         f"descriptor names {need}")
+    _fp4_covers(ckv_codes, kvl, pg)
     if row_seq is not None and row_seq.numel() != rows:
         raise ValueError(f"row_seq must be [{rows}]")
     hidden = int(o_absorb.shape[0]) if o_absorb is not None else 0
@@ -612,7 +618,7 @@ def page_arrays(caches, num_blocks: int) -> DsaPageArrays:
     if len(caches) > _lib.DSA_MAX_PAGE_ARRAYS:
         raise ValueError(f"{len(caches)} caches: at most {_lib.DSA_MAX_PAGE_ARRAYS}")
     pa = DsaPageArrays()
-    pa.n = len(caches)
+    pa.n, pa.num_pages = len(caches), int(num_blocks)
     for i, c in enumerate(caches):
         if c.dim() < 1 or int(c.shape[0]) != int(num_blocks):
             raise ValueError(f"cache {i} must be [{num_blocks}, ...], got {tuple(c.shape)}")

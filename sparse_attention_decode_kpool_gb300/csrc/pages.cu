@@ -699,13 +699,17 @@ int check_pages(const char* name, const dsa_paging* pg, const int32_t* table,
     return DSA_OK;
 }
 
-int check_arrays(const char* name, const dsa_page_arrays* in, PageArrays* out) {
+int check_arrays(const char* name, const dsa_page_arrays* in, long long num_pages,
+                 PageArrays* out) {
     out->n = 0;
     out->pieces = 0;
     if (!in) return DSA_OK;
     if (in->n < 0 || in->n > DSA_MAX_PAGE_ARRAYS)
         return fail(DSA_ERR_INVALID_ARG, "%s: %d page arrays (at most %d)", name, in->n,
                     DSA_MAX_PAGE_ARRAYS);
+    if (in->n > 0 && in->num_pages != num_pages)
+        return fail(DSA_ERR_INVALID_ARG, "%s: page arrays of %lld pages, the pool has %lld", name,
+                    (long long)in->num_pages, num_pages);
     long long pieces = 0;
     for (int i = 0; i < in->n; ++i) {
         if (!in->base[i] || in->page_bytes[i] < 1)
@@ -832,7 +836,7 @@ extern "C" int dsa_pages_reserve(const int32_t* seqs, int n, const dsa_paging* p
         return fail(DSA_ERR_UNSUPPORTED, "dsa_pages_reserve: %d sequences of %d new tokens", n,
                     new_tokens);
     PageArrays A;
-    rc = check_arrays("dsa_pages_reserve", arrays, &A);
+    rc = check_arrays("dsa_pages_reserve", arrays, a.pg.num_blocks, &A);
     if (rc) return rc;
     const PagesWs w = pages_ws(a.pg.num_blocks, a.pg.batch);
     if (!workspace || workspace_bytes < w.bytes || ((uintptr_t)workspace & 15))
@@ -885,7 +889,7 @@ extern "C" int dsa_pages_compact(const dsa_paging* pg, int32_t* block_table, int
     int rc = check_pages("dsa_pages_compact", pg, block_table, refs, &a.pg);
     if (rc) return rc;
     PageArrays A;
-    rc = check_arrays("dsa_pages_compact", arrays, &A);
+    rc = check_arrays("dsa_pages_compact", arrays, a.pg.num_blocks, &A);
     if (rc) return rc;
     const PagesWs w = pages_ws(a.pg.num_blocks, a.pg.batch);
     if (!workspace || workspace_bytes < w.bytes || ((uintptr_t)workspace & 15))

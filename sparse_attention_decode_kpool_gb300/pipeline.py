@@ -207,6 +207,7 @@ class DsaDecodeLayer:
         """End sequences: their pages lose a reference, their length becomes 0."""
         api.dsa_pages_free(self._seq_list(seqs, stream), self.pg, self.block_table,
                            self.seq_lens, self.refs, self.status, stream=stream)
+        self._write_geom(stream)
 
     def fork_sequences(self, parents, children, stream=None) -> None:
         """children[i] continues from a copy of parents[i] (the pages are shared until one
@@ -214,6 +215,11 @@ class DsaDecodeLayer:
         api.dsa_pages_fork(self._seq_list(parents, stream), self._seq_list(children, stream),
                            self.pg, self.block_table, self.seq_lens, self.refs, self.status,
                            stream=stream)
+        self._write_geom(stream)
+
+    def _write_geom(self, stream) -> None:
+        """The rows see their sequences' new lengths."""
+        api.dsa_write_geom(self.seq_lens, self.row_seq, self.row_ctx, self.status, stream=stream)
 
     def reserve_pages(self, new_tokens: int = 1, seqs=None, stream=None) -> None:
         """Pages for the next tokens of each sequence (append() does it for its one)."""

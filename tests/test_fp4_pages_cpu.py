@@ -268,6 +268,7 @@ def test_pages_refusals(lib):
             assert "workspace" in _err(lib)
         assert call(pg=_pg(paged=False)) == DSA_ERR_INVALID_ARG
         assert call(table=FAKE + 64) == DSA_ERR_INVALID_ARG
+        pa.num_pages = 16
         pa.n = 129
         assert call(arrays=ref(pa)) == DSA_ERR_INVALID_ARG
         pa.n = 1
@@ -276,6 +277,9 @@ def test_pages_refusals(lib):
         pa.base[0], pa.page_bytes[0] = FAKE, 0
         assert call(arrays=ref(pa)) == DSA_ERR_INVALID_ARG
         assert "page array 0" in _err(lib)
+        pa.num_pages = 15
+        assert call(arrays=ref(pa)) == DSA_ERR_INVALID_ARG
+        assert "15 pages" in _err(lib)
 
 
 def test_binding_refusals():

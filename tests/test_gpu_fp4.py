@@ -281,6 +281,27 @@ def test_fp4_attention_query_magnitudes(q_mul):
     _check(Case(17, 3, 64, 260, [300], q_mul=q_mul, scale=scale), KERNELS)
 
 
+@pytest.mark.parametrize("scale", [0.0, -1 / 16, 1e-30])
+def test_fp4_attention_scales(scale):
+    """No scale (equal weights), a negative and a vanishing one."""
+    _check(Case(18, 3, 64, 260, [300], scale=scale), KERNELS)
+
+
+def test_fp4_attention_both_outputs_and_no_status():
+    """f32 and bf16 results of one call, and calls without a status word or row_seq."""
+    c = Case(20, 4, 64, 700, [900, 50, 300, 7], row_seq=[0, 1, 2, 3]).cuda()
+    a = torch.empty((4, 64, KVL), dtype=torch.float32, device="cuda")
+    b = torch.empty((4, 64, KVL), dtype=torch.bfloat16, device="cuda")
+    for which in KERNELS:
+        with api.mla_kernel(which):
+            c.run(a)
+            c.run(b, row_seq=None)
+            assert torch.equal(a.to(torch.bfloat16), b)
+            api.dsa_sparse_mla_decode_fp4(c.d_q, c.d_seq, c.d_codes, c.d_scales, c.exp, c.pg, c.d_ids,
+                                          c.scale, olat=b, workspace=c.ws)
+            assert torch.equal(a.to(torch.bfloat16), b)
+
+
 @pytest.mark.parametrize("exp", [-30, -3, 0, 20])
 def test_fp4_attention_cache_exp(exp):
     c = Case(19, 3, 64, 260, [300], exp=-8)
@@ -515,6 +536,24 @@ def test_fp4_layer_decode(paged):
         # the projection's inputs: 2^-9 relative would be a bf16 weight's error
         got = grow.olat[r].cpu().numpy()
         assert np.abs(got - o).max() <= 2.0 ** -10 * np.abs(o).max()
+
+
+def test_fp4_refuses_mixed_devices_and_small_caches():
+    c = Case(61, 2, 8, 64, [100]).cuda()
+    out = torch.empty((2, 8, KVL), dtype=torch.float32, device="cuda")
+    with pytest.raises(ValueError, match="CUDA"):
+        api.dsa_sparse_mla_decode_fp4(c.q, c.d_seq, c.d_codes, c.d_scales, c.exp, c.pg, c.d_ids, c.scale,
+                                      olat=out, workspace=c.ws)
+    with pytest.raises(ValueError, match="holds 99 rows"):
+        api.dsa_sparse_mla_decode_fp4(c.d_q, c.d_seq, c.d_codes[:99], c.d_scales[:99], c.exp, c.pg,
+                                      c.d_ids, c.scale, olat=out, workspace=c.ws)
+    with pytest.raises(ValueError, match="contiguous"):
+        api.dsa_sparse_mla_decode_fp4(c.d_q, c.d_seq, c.d_codes, c.d_scales, c.exp, c.pg, c.d_ids,
+                                      c.scale, olat=out.transpose(0, 1).contiguous().transpose(0, 1),
+                                      workspace=c.ws)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        api.dsa_sparse_mla_decode_fp4(c.d_q, c.d_seq, c.d_codes, c.d_scales, c.exp, c.pg, c.d_ids,
+                                      c.scale, olat=out.half(), workspace=c.ws)
 
 
 def test_fp4_layer_rejects_two_formats():

@@ -351,6 +351,20 @@ def test_pages_graph_replay_and_streams():
     assert not p.ref.bad
 
 
+def test_pages_on_a_stream_of_their_own():
+    """Lists made on the stream that reads them, calls ordered on it."""
+    p = Pool(23, [40, 100, 3, 64, 0, 17], 16, 10, 30)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        p.fork([1, 3], [4, 2])
+    p.reserve(5, stream=s)
+    with torch.cuda.stream(s):
+        p.free([0])
+    s.synchronize()
+    p.check()
+
+
 def test_pages_layer_life():
     """A decode layer with the FP4 cache and managed pages: forked sequences fed the same
     tokens give the parent's bits at every step, wherever their pages are."""
@@ -406,6 +420,8 @@ def test_pages_layer_life():
         assert torch.equal(lay.olat[r], before[r])
     # divergence: different tokens from here on
     lay.fork_sequences([0], [3])
+    lay.step()  # the child sees the parent's context before any append
+    same(0, 3, "at the fork")
     stage(10)
     lay.ckv_new[3] = lay.ckv_new[3].flip(0)
     lay.k_new[3] = lay.k_new[3].flip(0)

@@ -56,7 +56,8 @@ extern "C" {
 #define DSA_STATUS_TIMEOUT 4   /* a pipeline wait gave up after ~1 s (results invalid) */
 #define DSA_STATUS_CACHE_FULL 8 /* dsa_indexer_store: a sequence's cache was full (not stored) */
 #define DSA_STATUS_BAD_SEQ 16   /* dsa_pages_*: a listed sequence was skipped (see the calls)  */
-#define DSA_STATUS_NO_PAGES 32  /* dsa_pages_reserve: too few free pages for a sequence        */
+#define DSA_STATUS_NO_PAGES 32  /* dsa_pages_reserve: too few free pages for a sequence;
+                                   dsa_decode_append_guarded: its next page is still shared   */
 
 #define DSA_KV_LORA_RANK 512 /* latent width the attention kernels are built for */
 #define DSA_MAX_KPOOL 16     /* most slots per pool dsa_compress handles         */
@@ -585,6 +586,37 @@ int dsa_decode_append_fp4(const dsa_bf16* k_new, const dsa_bf16* gate_new,
                           int32_t* status, void* stream);
 
 /*
+ * dsa_decode_append_guarded -- the decode-time append of a pool whose pages may be shared
+ * (see the page operators below): dsa_decode_append, _fp8 or _fp4 as `latent` says, for the
+ * sequences that may be written. The other appends know no counts and write a shared page
+ * as any other.
+ *
+ * refs [num_blocks] i32 (device, nullable): the counts of the pool's pages. A sequence whose
+ * next token, or the pooled key of the pool that token completes, lies in a page with
+ * refs > 1 (one that dsa_pages_reserve had no free page to copy to) is left as it is, its
+ * length included, and sets DSA_STATUS_NO_PAGES.
+ * serving [batch] i32 (device, nullable): a sequence whose entry is negative is left as it
+ * is, without a status bit. row_ctx[b] is the sequence's length in every case.
+ *
+ * ckv_codes, ckv_scales: the FP8 cache (scales f32), the FP4 cache (scales u8, under
+ * 2^cache_exp), or NULL for DSA_LATENT_BF16. Everything else, limits included, as in the
+ * append that `latent` names.
+ */
+#define DSA_LATENT_BF16 0
+#define DSA_LATENT_FP8 1
+#define DSA_LATENT_FP4 2
+int dsa_decode_append_guarded(const int32_t* refs, const int32_t* serving, int latent,
+                              const dsa_bf16* k_new, const dsa_bf16* gate_new,
+                              const dsa_bf16* ckv_new, const float* ape, const dsa_bf16* ln_w,
+                              const dsa_bf16* ln_b, float eps, const dsa_paging* pg,
+                              int32_t* seq_lens, int first_key, int kpool, int ihd,
+                              int kv_lora_rank, dsa_bf16* k_raw, dsa_bf16* gate,
+                              uint8_t* token_valid, dsa_bf16* ckv, uint8_t* ckv_codes,
+                              void* ckv_scales, int cache_exp, dsa_bf16* kpool_out,
+                              uint8_t* pool_valid, int32_t* pool_idx, int32_t* row_ctx,
+                              int32_t* status, void* stream);
+
+/*
  * dsa_sparse_mla_decode_fp4 -- dsa_sparse_mla_decode over an FP4 latent cache (see
  * dsa_quantize_latent_fp4): the latent row of token t is its decoded row, everything
  * else, the equations included, is dsa_sparse_mla_decode's. Each gathered row is 288
@@ -619,9 +651,10 @@ int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int heads, int kv_
  * read and written on the device, so a captured graph stays valid as sequences come, grow
  * and go. Pages are handed out lowest id first, so results do not depend on timing.
  *
- * Pages may be shared after dsa_pages_fork. A shared page is never written: before
- * tokens are appended, dsa_pages_reserve gives each sequence its own copy of the pages
- * they will be written to.
+ * Pages may be shared after dsa_pages_fork. No page operator writes a shared page, and
+ * before tokens are appended dsa_pages_reserve gives each sequence its own copy of the
+ * pages they will be written to. Where it runs out of free pages a sequence keeps its
+ * shared page: append with dsa_decode_append_guarded, which then leaves the sequence alone.
  *
  * Common arguments: pg must be paged; block_table and seq_lens must be the descriptor's
  * own (writable) tensors; refs [pg->num_blocks] i32. Lists of sequences are device i32

@@ -594,6 +594,14 @@ class PagePool:
                       for p in pools_completed(L, L + new, first_key, kpool)}
         return sorted(pages)
 
+    def holds_alone(self, b: int, first_key: int = 0, kpool: int = 0) -> bool:
+        """Whether b's next token can be stored: every page it is written to is mapped and
+        has no other holder."""
+        if not 0 <= int(self.lens[b]) < self.table.shape[1] * self.bs:
+            return False
+        pages = [int(self.table[b, j]) for j in self.written_pages(b, 1, first_key, kpool)]
+        return all(0 <= p < self.n and self.refs[p] <= 1 for p in pages)
+
     def reserve(self, new: int, first_key: int = 0, kpool: int = 0, seqs=None):
         start = self.refs.copy()
         free = [p for p in range(self.n) if start[p] == 0]

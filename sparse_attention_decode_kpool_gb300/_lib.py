@@ -24,6 +24,9 @@ DSA_STATUS_CACHE_FULL = 8
 DSA_STATUS_BAD_SEQ = 16
 DSA_STATUS_NO_PAGES = 32
 DSA_MAX_PAGE_ARRAYS = 128
+DSA_LATENT_BF16 = 0
+DSA_LATENT_FP8 = 1
+DSA_LATENT_FP4 = 2
 DSA_ABI_VERSION = 8
 DSA_OPT_PDL = 0
 DSA_OPT_MLA_KERNEL = 1
@@ -107,6 +110,8 @@ SIGNATURES = {
     "dsa_dequantize_latent_fp4": (_I, [_P, _P, _LL, _P, _LL, _I, _I, _P, _P, _P]),
     "dsa_decode_append_fp4": (_I, [_P, _P, _P, _P, _P, _P, _F, _PG, _P, _I, _I, _I, _I, _P, _P,
                                    _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
+    "dsa_decode_append_guarded": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _F, _PG, _P, _I, _I, _I,
+                                       _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
     "dsa_sparse_mla_decode_fp4_workspace": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "dsa_sparse_mla_decode_fp4": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _PG, _P, _I, _F, _P, _I,
                                        _P, _P, _P, _P, _P, _SZ, _P]),

@@ -221,13 +221,21 @@ def dsa_write_geom(seq_lens, row_seq, row_ctx, status=None, stream=None) -> None
 def dsa_decode_append(k_new, gate_new, ape, ln_w, ln_b, eps: float, pg: DsaPaging, seq_lens,
                       first_key: int, kpool: int, k_raw, gate, token_valid, kpool_out, pool_valid,
                       ckv_new=None, ckv=None, pool_idx=None, row_ctx=None, status=None,
-                      stream=None) -> None:
+                      stream=None, refs=None, serving=None) -> None:
     """dsa_indexer_store + dsa_write_geom + dsa_compress_append(new_tokens=1) in one
-    launch (identical results)."""
+    launch (identical results). With ``refs`` (the pool's counts) a sequence whose next
+    page is shared, with ``serving`` one whose entry is negative, is left as it is
+    (dsa_decode_append_guarded)."""
     batch, ihd = (int(x) for x in k_new.shape)
     if tuple(gate_new.shape) != (batch, ihd):
         raise ValueError(f"gate_new must be [{batch}, {ihd}]")
     kvl = int(ckv_new.shape[-1]) if ckv_new is not None else 0
+    if refs is not None or serving is not None:
+        _append_guarded(refs, serving, _lib.DSA_LATENT_BF16, k_new, gate_new, ckv_new, ape, ln_w,
+                        ln_b, eps, pg, seq_lens, first_key, kpool, kvl, k_raw, gate, token_valid,
+                        ckv, None, None, 0, kpool_out, pool_valid, pool_idx, row_ctx, status,
+                        stream)
+        return
     check(_lib.load().dsa_decode_append(
         _ptr(k_new, torch.bfloat16, "k_new"), _ptr(gate_new, torch.bfloat16, "gate_new"),
         _ptr(ckv_new, torch.bfloat16, "ckv_new"), _ptr(ape, torch.float32, "ape"),
@@ -243,15 +251,23 @@ def dsa_decode_append(k_new, gate_new, ape, ln_w, ln_b, eps: float, pg: DsaPagin
 def dsa_decode_append_fp8(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float, pg: DsaPaging,
                           seq_lens, first_key: int, kpool: int, k_raw, gate, token_valid,
                           ckv_codes, ckv_scales, kpool_out, pool_valid, ckv=None, pool_idx=None,
-                          row_ctx=None, status=None, stream=None) -> None:
+                          row_ctx=None, status=None, stream=None, refs=None,
+                          serving=None) -> None:
     """dsa_decode_append that also encodes the staged latent row into the FP8 cache
-    (same codec and bytes as dsa_quantize_latent); the bf16 cache ``ckv`` is optional."""
+    (same codec and bytes as dsa_quantize_latent); the bf16 cache ``ckv`` is optional.
+    ``refs`` and ``serving`` as in dsa_decode_append."""
     batch, ihd = (int(x) for x in k_new.shape)
     if tuple(gate_new.shape) != (batch, ihd):
         raise ValueError(f"gate_new must be [{batch}, {ihd}]")
     kvl = int(ckv_new.shape[-1])
     if int(ckv_codes.shape[-1]) != kvl or int(ckv_scales.shape[-1]) != kvl // 128:
         raise ValueError(f"ckv_codes must be [.., {kvl}] and ckv_scales [.., {kvl // 128}]")
+    if refs is not None or serving is not None:
+        _append_guarded(refs, serving, _lib.DSA_LATENT_FP8, k_new, gate_new, ckv_new, ape, ln_w,
+                        ln_b, eps, pg, seq_lens, first_key, kpool, kvl, k_raw, gate, token_valid,
+                        ckv, ckv_codes, ckv_scales, 0, kpool_out, pool_valid, pool_idx, row_ctx,
+                        status, stream)
+        return
     check(_lib.load().dsa_decode_append_fp8(
         _ptr(k_new, torch.bfloat16, "k_new"), _ptr(gate_new, torch.bfloat16, "gate_new"),
         _ptr(ckv_new, torch.bfloat16, "ckv_new"), _ptr(ape, torch.float32, "ape"),
@@ -530,10 +546,11 @@ def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None,
 def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float, pg: DsaPaging,
                           seq_lens, first_key: int, kpool: int, k_raw, gate, token_valid,
                           ckv_codes, ckv_scales, cache_exp: int, kpool_out, pool_valid, ckv=None,
-                          pool_idx=None, row_ctx=None, status=None, stream=None) -> None:
+                          pool_idx=None, row_ctx=None, status=None, stream=None, refs=None,
+                          serving=None) -> None:
     """dsa_decode_append that also encodes the staged latent row into the FP4 cache
     (same codec and bytes as dsa_quantize_latent_fp4); the bf16 cache ``ckv`` is
-    optional."""
+    optional. ``refs`` and ``serving`` as in dsa_decode_append."""
     batch, ihd = k_new.shape
     if gate_new.shape != k_new.shape:
         raise ValueError(f"gate_new must be [{batch}, {ihd}]")
@@ -545,6 +562,12 @@ def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float,
     if batch != pg.batch:
         raise ValueError(f"one staged row per sequence: {batch} rows, {pg.batch} sequences")
     _fp4_covers(ckv_codes, kvl, pg)
+    if refs is not None or serving is not None:
+        _append_guarded(refs, serving, _lib.DSA_LATENT_FP4, k_new, gate_new, ckv_new, ape, ln_w,
+                        ln_b, eps, pg, seq_lens, first_key, kpool, kvl, k_raw, gate, token_valid,
+                        ckv, ckv_codes, ckv_scales, cache_exp, kpool_out, pool_valid, pool_idx,
+                        row_ctx, status, stream)
+        return
     dev = _device_of(k_new, "k_new")
     bf16, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
     _run(dev, stream, _lib.load().dsa_decode_append_fp4,
@@ -555,6 +578,35 @@ def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float,
          ihd, kvl, _dev_ptr(k_raw, bf16, dev, "k_raw"), _dev_ptr(gate, bf16, dev, "gate"),
          _dev_ptr(token_valid, u8, dev, "token_valid"), _dev_ptr(ckv, bf16, dev, "ckv"),
          _dev_ptr(ckv_codes, u8, dev, "ckv_codes"), _dev_ptr(ckv_scales, u8, dev, "ckv_scales"),
+         int(cache_exp), _dev_ptr(kpool_out, bf16, dev, "kpool_out"),
+         _dev_ptr(pool_valid, u8, dev, "pool_valid"), _dev_ptr(pool_idx, i32, dev, "pool_idx"),
+         _dev_ptr(row_ctx, i32, dev, "row_ctx"), _dev_ptr(status, i32, dev, "status"))
+
+
+def _append_guarded(refs, serving, latent: int, k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps,
+                    pg: DsaPaging, seq_lens, first_key, kpool, kvl: int, k_raw, gate, token_valid,
+                    ckv, codes, scales, cache_exp, kpool_out, pool_valid, pool_idx, row_ctx,
+                    status, stream) -> None:
+    """The dsa_decode_append* of a pool with counts or a serving list."""
+    batch, ihd = k_new.shape
+    if batch != pg.batch:
+        raise ValueError(f"one staged row per sequence: {batch} rows, {pg.batch} sequences")
+    if refs is not None and refs.numel() != pg.num_blocks:
+        raise ValueError(f"refs must be [{pg.num_blocks}]")
+    if serving is not None and serving.numel() != pg.batch:
+        raise ValueError(f"serving must be [{pg.batch}]")
+    dev = _device_of(k_new, "k_new")
+    bf16, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+    _run(dev, stream, _lib.load().dsa_decode_append_guarded,
+         _dev_ptr(refs, i32, dev, "refs"), _dev_ptr(serving, i32, dev, "serving"), latent,
+         _dev_ptr(k_new, bf16, dev, "k_new"), _dev_ptr(gate_new, bf16, dev, "gate_new"),
+         _dev_ptr(ckv_new, bf16, dev, "ckv_new"), _dev_ptr(ape, f32, dev, "ape"),
+         _dev_ptr(ln_w, bf16, dev, "ln_w"), _dev_ptr(ln_b, bf16, dev, "ln_b"), float(eps),
+         ctypes.byref(pg), _dev_ptr(seq_lens, i32, dev, "seq_lens"), int(first_key), int(kpool),
+         ihd, kvl, _dev_ptr(k_raw, bf16, dev, "k_raw"), _dev_ptr(gate, bf16, dev, "gate"),
+         _dev_ptr(token_valid, u8, dev, "token_valid"), _dev_ptr(ckv, bf16, dev, "ckv"),
+         _dev_ptr(codes, u8, dev, "ckv_codes"),
+         _dev_ptr(scales, f32 if latent == _lib.DSA_LATENT_FP8 else u8, dev, "ckv_scales"),
          int(cache_exp), _dev_ptr(kpool_out, bf16, dev, "kpool_out"),
          _dev_ptr(pool_valid, u8, dev, "pool_valid"), _dev_ptr(pool_idx, i32, dev, "pool_idx"),
          _dev_ptr(row_ctx, i32, dev, "row_ctx"), _dev_ptr(status, i32, dev, "status"))

@@ -46,11 +46,6 @@ struct CompressArgs {
 
 constexpr int kThreads = 256;
 
-// Pools whole among the first n tokens.
-__device__ __forceinline__ int whole_pools(int n, int first_key, int kpool) {
-    return n > first_key ? (n - first_key) / kpool : 0;
-}
-
 // 2^x on the special-function unit (x <= 0 here: softmax weights in (0, 1]).
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -250,7 +245,9 @@ __device__ __forceinline__ void compress_unit(const CompressArgs& a, int b, int 
 
 // dsa_decode_append: one CTA per sequence stores the staged token at the live
 // length, advances the length, writes the row context, and (warp 0) pools the pool
-// that token completed, with the same pool_lane arithmetic as compress_kernel.
+// that token completed, with the same pool_lane arithmetic as compress_kernel. With a
+// guard (dsa_decode_append_guarded) it first looks at the sequence's entry of the serving
+// list and at the counts of the pages it is about to write, two loads more in its chain.
 struct AppendArgs {
     const uint16_t* k_new;
     const uint16_t* gate_new;
@@ -274,6 +271,7 @@ struct AppendArgs {
     uint8_t* pvalid;
     int32_t* pidx;
     Paging pg;
+    AppendGuard guard;
     float eps;
     int first_key;
     int kpool;
@@ -288,8 +286,25 @@ __global__ void __launch_bounds__(kAppendThreads) decode_append_kernel(AppendArg
     constexpr int LPP = IHD / 8;
     __shared__ long long s_row;
     __shared__ int s_t;
+    __shared__ bool s_held;  // the guard left the sequence as it was
     const int b = blockIdx.x;
-    if (threadIdx.x == 0) s_row = next_token_row(a.pg, a.seq_lens, b, &s_t, a.status);
+    if (threadIdx.x == 0) {
+        long long row = -1;
+        bool held = a.guard.serving && a.guard.serving[b] < 0;
+        if (held) {
+            s_t = a.seq_lens[b];
+        } else {
+            row = next_token_row(a.pg, a.seq_lens, b, &s_t, a.status);
+            if (row >= 0 && a.guard.refs &&
+                next_page_shared(a.pg, a.guard.refs, b, s_t, a.first_key, a.kpool)) {
+                flag_status(a.status, DSA_STATUS_NO_PAGES);
+                held = true;
+                row = -1;
+            }
+        }
+        s_row = row;
+        s_held = held;
+    }
     __syncthreads();
     const long long row = s_row;
     const int t = s_t;
@@ -325,6 +340,7 @@ __global__ void __launch_bounds__(kAppendThreads) decode_append_kernel(AppendArg
         if (row >= 0) a.seq_lens[b] = L;
         if (a.row_ctx) a.row_ctx[b] = L;
     }
+    if (s_held) return;  // its pools are those of the tokens it had
     const int KP = a.kpool;
     const int Lc = min(L, seq_capacity(a.pg));
     const int P = whole_pools(Lc, a.first_key, KP);
@@ -468,7 +484,7 @@ extern "C" int dsa_compress_append(const dsa_bf16* k_raw, const dsa_bf16* gate,
 
 namespace {
 // dsa_decode_append, dsa_decode_append_fp8 (ckv8 / ckv_scale set) and
-// dsa_decode_append_fp4 (ckv4 / ckv4_scale set).
+// dsa_decode_append_fp4 (ckv4 / ckv4_scale set), with or without a guard.
 int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* gate_new,
                        const dsa_bf16* ckv_new, const float* ape, const dsa_bf16* ln_w,
                        const dsa_bf16* ln_b, float eps, const dsa_paging* pg, int32_t* seq_lens,
@@ -476,7 +492,8 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
                        dsa_bf16* gate, uint8_t* token_valid, dsa_bf16* ckv, uint8_t* ckv8,
                        float* ckv_scale, uint8_t* ckv4, uint8_t* ckv4_scale, int cache_exp,
                        dsa_bf16* kpool_out, uint8_t* pool_valid, int32_t* pool_idx,
-                       int32_t* row_ctx, int32_t* status, void* stream) {
+                       int32_t* row_ctx, int32_t* status, void* stream,
+                       const AppendGuard& guard = AppendGuard{nullptr, nullptr}) {
     if (kpool < 1 || kpool > DSA_MAX_KPOOL)
         return fail(DSA_ERR_UNSUPPORTED, "%s: kpool %d outside [1, %d]", name, kpool,
                     DSA_MAX_KPOOL);
@@ -508,6 +525,8 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
         return fail(DSA_ERR_UNSUPPORTED,
                     "%s: paged layout needs first_key %% kpool == 0 (got %d, %d)", name,
                     first_key, kpool);
+    if (guard.refs && !P.block_table)
+        return fail(DSA_ERR_INVALID_ARG, "%s: refs of a cache that is not paged", name);
     if (!seq_lens || seq_lens != pg->seq_lens)
         return fail(DSA_ERR_INVALID_ARG, "%s: seq_lens must be the descriptor's (writable) lengths",
                     name);
@@ -542,6 +561,7 @@ int decode_append_impl(const char* name, const dsa_bf16* k_new, const dsa_bf16* 
     a.pvalid = pool_valid;
     a.pidx = pool_idx;
     a.pg = P;
+    a.guard = guard;
     a.eps = eps;
     a.first_key = first_key;
     a.kpool = kpool;
@@ -607,4 +627,29 @@ extern "C" int dsa_decode_append_fp4(const dsa_bf16* k_new, const dsa_bf16* gate
                               eps, pg, seq_lens, first_key, kpool, ihd, kv_lora_rank, k_raw, gate,
                               token_valid, ckv, nullptr, nullptr, ckv_codes, ckv_scales, cache_exp,
                               kpool_out, pool_valid, pool_idx, row_ctx, status, stream);
+}
+
+extern "C" int dsa_decode_append_guarded(
+    const int32_t* refs, const int32_t* serving, int latent, const dsa_bf16* k_new,
+    const dsa_bf16* gate_new, const dsa_bf16* ckv_new, const float* ape, const dsa_bf16* ln_w,
+    const dsa_bf16* ln_b, float eps, const dsa_paging* pg, int32_t* seq_lens, int first_key,
+    int kpool, int ihd, int kv_lora_rank, dsa_bf16* k_raw, dsa_bf16* gate, uint8_t* token_valid,
+    dsa_bf16* ckv, uint8_t* ckv_codes, void* ckv_scales, int cache_exp, dsa_bf16* kpool_out,
+    uint8_t* pool_valid, int32_t* pool_idx, int32_t* row_ctx, int32_t* status, void* stream) {
+    const char* name = "dsa_decode_append_guarded";
+    if (latent != DSA_LATENT_BF16 && latent != DSA_LATENT_FP8 && latent != DSA_LATENT_FP4)
+        return fail(DSA_ERR_INVALID_ARG, "%s: latent %d is no DSA_LATENT_*", name, latent);
+    if ((latent == DSA_LATENT_BF16) != (ckv_codes == nullptr) ||
+        (latent == DSA_LATENT_BF16) != (ckv_scales == nullptr))
+        return fail(DSA_ERR_INVALID_ARG,
+                    "%s: ckv_codes and ckv_scales go with the FP8 and FP4 caches", name);
+    const bool fp8 = latent == DSA_LATENT_FP8, fp4 = latent == DSA_LATENT_FP4;
+    return decode_append_impl(name, k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps, pg, seq_lens,
+                              first_key, kpool, ihd, kv_lora_rank, k_raw, gate, token_valid, ckv,
+                              fp8 ? ckv_codes : nullptr,
+                              fp8 ? static_cast<float*>(ckv_scales) : nullptr,
+                              fp4 ? ckv_codes : nullptr,
+                              fp4 ? static_cast<uint8_t*>(ckv_scales) : nullptr,
+                              fp4 ? cache_exp : 0, kpool_out, pool_valid, pool_idx, row_ctx,
+                              status, stream, AppendGuard{refs, serving});
 }

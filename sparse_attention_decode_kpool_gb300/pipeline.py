@@ -25,6 +25,10 @@ class DsaDecodeLayer:
                  fuse_append: bool = True, latent_fp8: bool = False, frontend=None,
                  l2_prefetch_bytes: Optional[int] = None, latent_fp4: bool = False,
                  fp4_exp: Optional[int] = None, manage_pages: bool = False):
+        if manage_pages and not fuse_append:
+            # of the three calls the store cannot see whether the pooled key's page is shared
+            raise ValueError("managed pages are appended to by dsa_decode_append only "
+                             "(fuse_append=True)")
         g = wl.geom
         self.wl = wl
         self.geom = g
@@ -388,7 +392,7 @@ class DsaDecodeLayer:
                                       g.index_kpool, self.k_raw, self.gate, self.valid,
                                       self.ckv_codes, self.ckv_scales, self.fp4_exp, self.kpool,
                                       self.pool_valid, row_ctx=self.row_ctx, status=self.status,
-                                      stream=stream)
+                                      stream=stream, refs=self.refs)
             return
         if self.latent_fp8:  # the token's latent row goes to the FP8 cache only
             api.dsa_decode_append_fp8(self.k_new, self.gate_new, self.ckv_new, self.ape, self.ln_w,
@@ -396,14 +400,14 @@ class DsaDecodeLayer:
                                       g.index_kpool, self.k_raw, self.gate, self.valid,
                                       self.ckv_codes, self.ckv_scales, self.kpool,
                                       self.pool_valid, row_ctx=self.row_ctx, status=self.status,
-                                      stream=stream)
+                                      stream=stream, refs=self.refs)
             return
         if self.fuse_append:
             api.dsa_decode_append(self.k_new, self.gate_new, self.ape, self.ln_w, self.ln_b, g.eps,
                                   self.pg, self.seq_lens, g.first_key, g.index_kpool, self.k_raw,
                                   self.gate, self.valid, self.kpool, self.pool_valid,
                                   ckv_new=self.ckv_new, ckv=self.ckv, row_ctx=self.row_ctx,
-                                  status=self.status, stream=stream)
+                                  status=self.status, stream=stream, refs=self.refs)
             return
         api.dsa_indexer_store(self.k_new, self.gate_new, self.pg, self.seq_lens, self.k_raw,
                               self.gate, self.valid, self.ckv_new, self.ckv, self.status,

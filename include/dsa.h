@@ -689,6 +689,18 @@ int dsa_pages_fork(const int32_t* parents, const int32_t* children, int n, const
                    void* stream);
 
 /*
+ * dsa_pages_serve -- keeps the list of the sequences that grow: serving [batch] i32 (device)
+ * holds b at entry b, or -1 for a sequence that takes no tokens (one that has ended, or a
+ * parent kept for its pages). Such a list is what dsa_pages_reserve takes as seqs and
+ * dsa_decode_append_guarded as serving; without it an ended sequence is given a page and a
+ * token again by the next of these calls. Each listed sequence's entry becomes b (on != 0)
+ * or -1. parents (nullable): with seqs the children of a dsa_pages_fork call; the pairs that
+ * call skips are left out here too, with DSA_STATUS_BAD_SEQ.
+ */
+int dsa_pages_serve(const int32_t* parents, const int32_t* seqs, int n, int batch, int on,
+                    int32_t* serving, int32_t* status, void* stream);
+
+/*
  * dsa_pages_reserve -- room for each listed sequence's next new_tokens tokens (seqs NULL:
  * every sequence of the batch, n ignored). The pages those tokens will be written to are
  * the token pages from seq_lens / block_size on and, with kpool > 0, the pages of the

@@ -118,6 +118,7 @@ SIGNATURES = {
     "dsa_pages_workspace": (_I, [_LL, _I, ctypes.POINTER(_SZ)]),
     "dsa_pages_free": (_I, [_P, _I, _PG, _P, _P, _P, _P, _P]),
     "dsa_pages_fork": (_I, [_P, _P, _I, _PG, _P, _P, _P, _P, _P]),
+    "dsa_pages_serve": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "dsa_pages_reserve": (_I, [_P, _I, _PG, _P, _P, _I, _I, _I, _PA, _P, _P, _SZ, _P]),
     "dsa_pages_compact": (_I, [_PG, _P, _P, _PA, _P, _P, _P, _P, _SZ, _P]),
     "dsa_frontend_workspace": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),

@@ -21,7 +21,7 @@ __all__ = ["paging", "dsa_compress", "dsa_compress_append", "dsa_indexer_store",
            "dsa_quantize_latent_fp4", "dsa_dequantize_latent_fp4", "dsa_decode_append_fp4",
            "dsa_sparse_mla_decode_fp4_workspace", "dsa_sparse_mla_decode_fp4",
            "page_arrays", "dsa_pages_workspace", "dsa_pages_free", "dsa_pages_fork",
-           "dsa_pages_reserve", "dsa_pages_compact", "DsaPageArrays",
+           "dsa_pages_serve", "dsa_pages_reserve", "dsa_pages_compact", "DsaPageArrays",
            "dsa_frontend_workspace", "dsa_frontend", "dsa_latent_project_workspace",
            "dsa_latent_project", "dsa_select_k",
            "dsa_validate_config", "dsa_prefetch_l2", "dsa_set_option", "dsa_get_option", "mla_kernel",
@@ -718,6 +718,21 @@ def dsa_pages_fork(parents, children, pg: DsaPaging, block_table, seq_lens, refs
          _dev_ptr(parents, i32, dev, "parents"), _dev_ptr(children, i32, dev, "children"),
          children.numel(), ctypes.byref(pg), _dev_ptr(block_table, i32, dev, "block_table"),
          _dev_ptr(seq_lens, i32, dev, "seq_lens"), _dev_ptr(refs, i32, dev, "refs"),
+         _dev_ptr(status, i32, dev, "status"))
+
+
+def dsa_pages_serve(seqs, serving, on: bool = True, parents=None, status=None,
+                    stream=None) -> None:
+    """Entry b of ``serving`` [batch] becomes b (``on``) or -1 for each listed sequence b:
+    the list that dsa_pages_reserve takes as ``seqs`` and dsa_decode_append* as
+    ``serving``. With ``parents``, ``seqs`` are the children of a dsa_pages_fork."""
+    if parents is not None and parents.numel() != seqs.numel():
+        raise ValueError("parents and seqs must have the same length")
+    dev = _device_of(serving, "serving")
+    i32 = torch.int32
+    _run(dev, stream, _lib.load().dsa_pages_serve,
+         _dev_ptr(parents, i32, dev, "parents"), _dev_ptr(seqs, i32, dev, "seqs"), seqs.numel(),
+         serving.numel(), 1 if on else 0, _dev_ptr(serving, i32, dev, "serving"),
          _dev_ptr(status, i32, dev, "status"))
 
 

@@ -11,7 +11,7 @@
 //
 // pages_free_kernel, pages_fork_kernel -- one block per (sequence, chunk of its table
 // row). Latency bound: a row's entries are read and written once, with one atomic on
-// each page's count.
+// each page's count. pages_serve_kernel -- one block per listed sequence.
 //
 // pages_reserve_kernel, pages_compact_kernel -- the planning steps. One cluster of eight
 // CTAs scans the counts (4 bytes a page): each CTA sums its slice, the sums are
@@ -266,6 +266,28 @@ __global__ void __launch_bounds__(kRowThreads) pages_fork_kernel(SeqArgs a) {
         if (old != now) child[e] = now;
     }
     if (blockIdx.y == 0 && threadIdx.x == 0) a.seq_lens[c] = L;
+}
+
+// dsa_pages_serve: one block per entry, for the search that fork's rule takes.
+__global__ void __launch_bounds__(kRowThreads)
+    pages_serve_kernel(const int32_t* parents, const int32_t* list, int n, int batch, int on,
+                       int32_t* serving, int32_t* status) {
+    pdl_trigger();
+    pdl_wait();
+    const int i = blockIdx.x;
+    const int b = __ldg(list + i);
+    if (b == -1) return;  // padding
+    bool bad = b < 0 || b >= batch;
+    if (parents) {  // the pairs that pages_fork_kernel skips
+        const int p = __ldg(parents + i);
+        bad = bad || p < 0 || p >= batch;
+        bad = block_finds(list, i, b, n, p) || bad;
+    }
+    if (threadIdx.x != 0) return;
+    if (bad)
+        flag_status(status, DSA_STATUS_BAD_SEQ);
+    else
+        serving[b] = on ? b : -1;
 }
 
 // ---------------------------------------------------------------------------
@@ -805,6 +827,22 @@ extern "C" int dsa_pages_fork(const int32_t* parents, const int32_t* children, i
     a.refs = refs;
     a.status = status;
     return launch_rows("dsa_pages_fork launch", pages_fork_kernel, a, (cudaStream_t)stream);
+}
+
+extern "C" int dsa_pages_serve(const int32_t* parents, const int32_t* seqs, int n, int batch,
+                               int on, int32_t* serving, int32_t* status, void* stream) {
+    if (batch < 1) return fail(DSA_ERR_INVALID_ARG, "dsa_pages_serve: batch %d < 1", batch);
+    if (n < 0 || n > batch)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_pages_serve: %d sequences listed, the batch has %d",
+                    n, batch);
+    if (!serving) return fail(DSA_ERR_INVALID_ARG, "dsa_pages_serve: serving is NULL");
+    if (n == 0) return DSA_OK;
+    if (!seqs) return fail(DSA_ERR_INVALID_ARG, "dsa_pages_serve: NULL sequences");
+    cudaError_t e = launch_pdl(pages_serve_kernel, dim3((unsigned)n), dim3(kRowThreads), 0,
+                               (cudaStream_t)stream, parents, seqs, n, batch, on, serving, status);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_pages_serve launch");
+    return DSA_OK;
 }
 
 extern "C" int dsa_pages_reserve(const int32_t* seqs, int n, const dsa_paging* pg,

@@ -162,9 +162,10 @@ class DsaDecodeLayer:
         self.append_graph: Optional[torch.cuda.CUDAGraph] = None
         if decode_from is not None:
             self._init_append(decode_from)
-        # Pages: with manage_pages the layer keeps a count per page, maps pages as the
-        # sequences grow, and can fork, free and compact them.
+        # Pages: with manage_pages the layer keeps a count per page and a list of the
+        # sequences that grow, maps pages for those, and can fork, free and compact.
         self.refs: Optional[torch.Tensor] = None
+        self.serving: Optional[torch.Tensor] = None
         if manage_pages:
             self._init_pages()
         # Projection front-end (dsa_frontend): the step's query inputs and the token's
@@ -186,6 +187,7 @@ class DsaDecodeLayer:
         self.block_table.masked_fill_(j[None] >= held[:, None], -1)
         ids = self.block_table[self.block_table >= 0].long()
         self.refs = torch.bincount(ids, minlength=wl.num_blocks).int()
+        self.serving = torch.arange(wl.batch, dtype=torch.int32, device=self.device)
         latent = ([self.ckv_codes, self.ckv_scales] if self.latent_fp8 or self.latent_fp4
                   else [self.ckv])
         caches = [self.k_raw, self.gate, self.valid, *latent, self.kpool, self.pool_valid]
@@ -208,17 +210,34 @@ class DsaDecodeLayer:
             return torch.as_tensor(seqs, dtype=torch.int32, device=self.device)
 
     def free_sequences(self, seqs, stream=None) -> None:
-        """End sequences: their pages lose a reference, their length becomes 0."""
-        api.dsa_pages_free(self._seq_list(seqs, stream), self.pg, self.block_table,
-                           self.seq_lens, self.refs, self.status, stream=stream)
+        """End sequences: their pages lose a reference, their length becomes 0, and append()
+        leaves them alone until they are forked over or resumed."""
+        seqs = self._seq_list(seqs, stream)
+        api.dsa_pages_free(seqs, self.pg, self.block_table, self.seq_lens, self.refs, self.status,
+                           stream=stream)
+        api.dsa_pages_serve(seqs, self.serving, False, status=self.status, stream=stream)
         self._write_geom(stream)
+
+    def pause_sequences(self, seqs, stream=None) -> None:
+        """append() leaves these sequences alone: they keep their tokens and pages and take
+        no new ones (a prompt that is only forked from)."""
+        api.dsa_pages_serve(self._seq_list(seqs, stream), self.serving, False,
+                            status=self.status, stream=stream)
+
+    def resume_sequences(self, seqs, stream=None) -> None:
+        """append() serves these sequences again: paused ones where they were, ended ones as
+        new, empty sequences."""
+        api.dsa_pages_serve(self._seq_list(seqs, stream), self.serving, True,
+                            status=self.status, stream=stream)
 
     def fork_sequences(self, parents, children, stream=None) -> None:
         """children[i] continues from a copy of parents[i] (the pages are shared until one
-        of the two writes to them)."""
-        api.dsa_pages_fork(self._seq_list(parents, stream), self._seq_list(children, stream),
-                           self.pg, self.block_table, self.seq_lens, self.refs, self.status,
-                           stream=stream)
+        of the two writes to them); append() serves the children."""
+        parents, children = self._seq_list(parents, stream), self._seq_list(children, stream)
+        api.dsa_pages_fork(parents, children, self.pg, self.block_table, self.seq_lens, self.refs,
+                           self.status, stream=stream)
+        api.dsa_pages_serve(children, self.serving, True, parents, status=self.status,
+                            stream=stream)
         self._write_geom(stream)
 
     def _write_geom(self, stream) -> None:
@@ -226,13 +245,15 @@ class DsaDecodeLayer:
         api.dsa_write_geom(self.seq_lens, self.row_seq, self.row_ctx, self.status, stream=stream)
 
     def reserve_pages(self, new_tokens: int = 1, seqs=None, stream=None) -> None:
-        """Pages for the next tokens of each sequence (append() does it for its one)."""
+        """Pages for the next tokens of each listed sequence, by default of those that
+        append() serves (it does it for its one token)."""
         g = self.geom
         if self.refs is None:
             raise ValueError("the layer was not built with manage_pages")
         api.dsa_pages_reserve(self.pg, self.block_table, self.refs, new_tokens, self.page_arrays,
                               g.first_key, g.index_kpool,
-                              seqs=None if seqs is None else self._seq_list(seqs, stream),
+                              seqs=(self.serving if seqs is None
+                                    else self._seq_list(seqs, stream)),
                               status=self.status, workspace=self.page_workspace, stream=stream)
 
     def compact_pages(self, stream=None) -> None:
@@ -392,7 +413,7 @@ class DsaDecodeLayer:
                                       g.index_kpool, self.k_raw, self.gate, self.valid,
                                       self.ckv_codes, self.ckv_scales, self.fp4_exp, self.kpool,
                                       self.pool_valid, row_ctx=self.row_ctx, status=self.status,
-                                      stream=stream, refs=self.refs)
+                                      stream=stream, refs=self.refs, serving=self.serving)
             return
         if self.latent_fp8:  # the token's latent row goes to the FP8 cache only
             api.dsa_decode_append_fp8(self.k_new, self.gate_new, self.ckv_new, self.ape, self.ln_w,
@@ -400,14 +421,14 @@ class DsaDecodeLayer:
                                       g.index_kpool, self.k_raw, self.gate, self.valid,
                                       self.ckv_codes, self.ckv_scales, self.kpool,
                                       self.pool_valid, row_ctx=self.row_ctx, status=self.status,
-                                      stream=stream, refs=self.refs)
+                                      stream=stream, refs=self.refs, serving=self.serving)
             return
         if self.fuse_append:
             api.dsa_decode_append(self.k_new, self.gate_new, self.ape, self.ln_w, self.ln_b, g.eps,
                                   self.pg, self.seq_lens, g.first_key, g.index_kpool, self.k_raw,
                                   self.gate, self.valid, self.kpool, self.pool_valid,
                                   ckv_new=self.ckv_new, ckv=self.ckv, row_ctx=self.row_ctx,
-                                  status=self.status, stream=stream, refs=self.refs)
+                                  status=self.status, stream=stream, refs=self.refs, serving=self.serving)
             return
         api.dsa_indexer_store(self.k_new, self.gate_new, self.pg, self.seq_lens, self.k_raw,
                               self.gate, self.valid, self.ckv_new, self.ckv, self.status,

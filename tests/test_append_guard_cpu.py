@@ -52,6 +52,18 @@ def test_guarded_append_refusals(lib, kw, code, text):
     assert text in lib.dsa_last_error().decode()
 
 
+def test_pages_serve_refusals(lib):
+    def call(n=1, batch=2, seqs=FAKE, serving=FAKE):
+        return lib.dsa_pages_serve(None, seqs, n, batch, 1, serving, None, None)
+
+    for kw, text in [(dict(batch=0), "batch 0"), (dict(n=-1), "-1 sequences"),
+                     (dict(n=3), "the batch has 2"), (dict(serving=None), "serving"),
+                     (dict(seqs=None), "NULL sequences")]:
+        assert call(**kw) == DSA_ERR_INVALID_ARG, kw
+        assert text in lib.dsa_last_error().decode(), kw
+    assert call(n=0, seqs=None) == _lib.DSA_OK
+
+
 def test_managed_pages_need_the_fused_append():
     with pytest.raises(ValueError, match="fuse_append"):
         DsaDecodeLayer(W.tiny(), device="cpu", manage_pages=True, fuse_append=False)

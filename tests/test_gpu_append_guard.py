@@ -263,3 +263,75 @@ def test_layer_out_of_pages(kw):
     assert int(lay.block_table[0, 3]) != int(lay.block_table[2, 3])
     for name in ("scores", "token_ids", "olat", "y"):
         assert torch.equal(getattr(lay, name)[0], getattr(lay, name)[2]), name
+
+
+def test_pages_serve():
+    """The list against plain loops: padding, repeats, entries out of range, fork's pairs."""
+    B = 600
+    serving, status = torch.arange(B, dtype=torch.int32, device="cuda"), _i32([0])
+    want = np.arange(B)
+    api.dsa_pages_serve(_i32([3, -1, 3, 599, 0]), serving, False, status=status)
+    want[[3, 599, 0]] = -1
+    assert serving.tolist() == want.tolist() and int(status) == 0
+    api.dsa_pages_serve(_i32([0, 5]), serving, status=status)
+    want[0] = 0
+    api.dsa_pages_serve(_i32([]), serving, False, status=status)
+    assert serving.tolist() == want.tolist() and int(status) == 0
+    api.dsa_pages_serve(_i32([600, -2, 7]), serving, False, status=status)
+    want[7] = -1
+    assert serving.tolist() == want.tolist() and int(status) == _lib.DSA_STATUS_BAD_SEQ
+    for parents, children, on in [([1, 2], [3, 599], [3, 599]), ([1, -1], [3, 7], [3]),
+                                  ([1, 3], [3, 7], [3]), ([7], [7], []), ([1, 2], [3, 3], [3]),
+                                  ([1, 700, 1], [-1, 3, 7], [7])]:
+        want[[3, 7, 599]] = -1
+        api.dsa_pages_serve(_i32([3, 7, 599]), serving, False)
+        status.zero_()
+        api.dsa_pages_serve(_i32(children), serving, True, _i32(parents), status)
+        want[on] = on
+        assert serving.tolist() == want.tolist(), (parents, children)
+        bad = len(on) < sum(c != -1 for c in children)
+        assert int(status) == (_lib.DSA_STATUS_BAD_SEQ if bad else 0)
+
+
+@pytest.mark.parametrize("kw", [{}, {"latent_fp8": True}, {"latent_fp4": True}], ids=FORMATS)
+def test_layer_ended_and_paused_sequences(kw):
+    """Through captured steps an ended sequence stays ended and a paused one keeps its
+    tokens, pages and results; forked over and resumed they grow."""
+    g = W.Geometry(index_kpool=4, index_heads=32, index_head_dim=128, index_topk=128, heads=8,
+                   hidden=256)
+    wl = W.make_workload("ended", 52, g, [300, 517, 130, 260], block_size=64, max_seq_len=1024,
+                         invalid_per_seq=0)
+    lay = DsaDecodeLayer(wl, keep_olat=True, decode_from=np.array([200, 260, 60, 190]),
+                         manage_pages=True, **kw)
+    lay.compress()
+    lay.stage(0)
+    lay.capture_append()
+    lay.step()
+    paused = lay.olat[1].clone()
+    gone = lay.block_table[3][lay.block_table[3] >= 0].long()
+    lay.free_sequences([3])
+    lay.pause_sequences([1])
+    live = int((lay.refs > 0).sum())
+    for _ in range(70):  # past a page's end
+        lay.append_graph.replay()
+    torch.cuda.synchronize()
+    assert int(lay.status) == 0
+    assert lay.seq_lens.tolist() == [270, 260, 130, 0] == lay.row_ctx.tolist()
+    assert (lay.block_table[3] == -1).all() and (lay.olat[3] == 0).all()
+    assert torch.equal(lay.olat[1], paused)
+    assert int((lay.refs > 0).sum()) == live + 3  # sequence 0: token 256; 2: 64 and 128
+    lay.fork_sequences([1], [3])
+    lay.resume_sequences([1, -1])
+    lay.append_graph.replay()
+    torch.cuda.synchronize()
+    assert int(lay.status) == 0 and lay.seq_lens.tolist() == [271, 261, 131, 261]
+    lay.free_sequences([2, 3])
+    lay.resume_sequences([3])
+    for _ in range(2):
+        lay.append_graph.replay()
+    torch.cuda.synchronize()
+    assert int(lay.status) == 0 and lay.seq_lens.tolist() == [273, 263, 0, 2]
+    assert int((lay.block_table[3] >= 0).sum()) == 1 and len(gone) == 3
+    lay.fork_sequences([7], [2])  # a refused pair starts nothing
+    lay.append_graph.replay()
+    assert int(lay.status) == _lib.DSA_STATUS_BAD_SEQ and int(lay.seq_lens[2]) == 0

@@ -71,7 +71,9 @@ class DsaDecodeLayer:
             api.dsa_quantize_latent(self.ckv, self.ckv_codes, self.ckv_scales)
         # FP4 latent cache (E2M1 codes, an E4M3 scale per 16 channels, 2^fp4_exp over all):
         # 288 bytes per token. fp4_exp defaults to the smallest power of two under which
-        # no block of the uploaded cache saturates.
+        # rows of 16 times the uploaded cache's largest magnitude do not saturate: tokens
+        # appended later may be larger, and a block whose maximum is above 1/896 of that
+        # magnitude still keeps a full scale (E4M3's normal range is 2^14.8 wide).
         if self.latent_fp4:
             if decode_from is not None and not fuse_append:
                 raise ValueError("the FP4 latent cache is appended by dsa_decode_append_fp4 "
@@ -79,7 +81,7 @@ class DsaDecodeLayer:
             kvl = g.kv_lora_rank
             if fp4_exp is None:
                 amax = float(self.ckv.abs().max()) if self.ckv.numel() else 0.0
-                fp4_exp = math.ceil(math.log2(amax / 2688.0)) if 0.0 < amax < math.inf else 0
+                fp4_exp = 4 + math.ceil(math.log2(amax / 2688.0)) if 0.0 < amax < math.inf else 0
             self.fp4_exp = max(-64, min(64, int(fp4_exp)))
             lead = self.ckv.shape[:-1]
             self.ckv_codes = torch.empty(lead + (kvl // 2,), dtype=torch.uint8, device=dev)

@@ -19,6 +19,8 @@ from .workloads import Workload
 
 
 class DsaDecodeLayer:
+    _FP4_UPLOAD = 1 << 18  # bf16 latent rows on the device at a time (256 MiB)
+
     def __init__(self, wl: Workload, device: str = "cuda", keep_olat: bool = False,
                  with_o_absorb: bool = True, use_drawn_kpool: bool = False,
                  score_path: str = "auto", fuse_expand: bool = True, decode_from=None,
@@ -51,8 +53,8 @@ class DsaDecodeLayer:
         self.step_inputs = self._carve(dev, pinned=False)
         self.row_ctx.copy_(torch.from_numpy(wl.row_ctx))
 
-        # Resident state.
-        self.ckv = up(wl.ckv)
+        # Resident state. With an FP4 latent cache there is no bf16 one on the device.
+        self.ckv = None if latent_fp4 else up(wl.ckv)
         # FP8 latent cache (E4M3 codes + power-of-two scales per 128 channels), encoded
         # once from the bf16 cache; attention then gathers 528 instead of 1,024 bytes
         # per token.
@@ -79,14 +81,19 @@ class DsaDecodeLayer:
                 raise ValueError("the FP4 latent cache is appended by dsa_decode_append_fp4 "
                                  "only (fuse_append=True)")
             kvl = g.kv_lora_rank
+            src = wl.ckv.reshape(-1, kvl)  # uploaded and encoded a part at a time
+            parts = [slice(i, i + self._FP4_UPLOAD) for i in range(0, len(src), self._FP4_UPLOAD)]
             if fp4_exp is None:
-                amax = float(self.ckv.abs().max()) if self.ckv.numel() else 0.0
+                amax = (float(torch.stack([up(src[p]).abs().max() for p in parts]).max())
+                        if parts else 0.0)
                 fp4_exp = 4 + math.ceil(math.log2(amax / 2688.0)) if 0.0 < amax < math.inf else 0
             self.fp4_exp = max(-64, min(64, int(fp4_exp)))
-            lead = self.ckv.shape[:-1]
+            lead = wl.ckv.shape[:-1]
             self.ckv_codes = torch.empty(lead + (kvl // 2,), dtype=torch.uint8, device=dev)
             self.ckv_scales = torch.empty(lead + (kvl // 16,), dtype=torch.uint8, device=dev)
-            api.dsa_quantize_latent_fp4(self.ckv, self.ckv_codes, self.ckv_scales, self.fp4_exp)
+            for p in parts:
+                api.dsa_quantize_latent_fp4(up(src[p]), self.ckv_codes.view(-1, kvl // 2)[p],
+                                            self.ckv_scales.view(-1, kvl // 16)[p], self.fp4_exp)
         self.o_absorb = up(wl.o_absorb) if with_o_absorb else None
         # The step prefetches the first l2_prefetch_bytes of o_absorb into L2 on a
         # second stream while top-k and the gather run (they leave HBM mostly idle);
@@ -363,7 +370,11 @@ class DsaDecodeLayer:
                 self.k_raw.view(-1, g.index_head_dim)[rows] = 0
                 self.gate.view(-1, g.index_head_dim)[rows] = 0
                 self.valid.view(-1)[rows] = 0
-                self.ckv.view(-1, g.kv_lora_rank)[rows] = 0
+                if self.latent_fp4:  # zeros have codes 0 and scales 0
+                    self.ckv_codes.view(-1, g.kv_lora_rank // 2)[rows] = 0
+                    self.ckv_scales.view(-1, g.kv_lora_rank // 16)[rows] = 0
+                else:
+                    self.ckv.view(-1, g.kv_lora_rank)[rows] = 0
         self.seq_lens.copy_(torch.from_numpy(L0.astype(np.int32)))
         B = wl.batch
         self.k_new = torch.zeros((B, g.index_head_dim), dtype=torch.bfloat16, device=dev)
@@ -372,8 +383,6 @@ class DsaDecodeLayer:
         self.row_ctx.copy_(self.seq_lens)
         if self.latent_fp8:  # the FP8 cache of the cut-back bf16 cache
             api.dsa_quantize_latent(self.ckv, self.ckv_codes, self.ckv_scales)
-        if self.latent_fp4:
-            api.dsa_quantize_latent_fp4(self.ckv, self.ckv_codes, self.ckv_scales, self.fp4_exp)
 
     def staged_rows(self, i: int):
         """Host rows (k, gate, ckv) [batch, ...] of the token each sequence appends at

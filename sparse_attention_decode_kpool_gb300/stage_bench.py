@@ -108,9 +108,10 @@ def main(argv=None) -> None:
     if args.stage == "quantize":
         if layer.ckv_codes is None:
             raise SystemExit("--stage quantize needs --latent-fp8 or --latent-fp4")
-        if args.latent_fp4:
+        if args.latent_fp4:  # the layer keeps no bf16 rows
+            rows = wl.ckv.cuda()
             layer.quantize = lambda: api.dsa_quantize_latent_fp4(
-                layer.ckv, layer.ckv_codes, layer.ckv_scales, layer.fp4_exp)
+                rows, layer.ckv_codes, layer.ckv_scales, layer.fp4_exp)
         else:
             layer.quantize = lambda: api.dsa_quantize_latent(layer.ckv, layer.ckv_codes,
                                                               layer.ckv_scales)

@@ -65,3 +65,23 @@ def test_default_exponent_keeps_small_blocks():
     want = O.dequantize_latent_fp4(*O.quantize_latent_fp4(np.ones((1, 512)), 0), 0)[0]
     got = O.dequantize_latent_fp4(codes[:4].cpu().numpy(), scales[:4].cpu().numpy(), lay.fp4_exp)
     np.testing.assert_array_equal(got, np.tile(want, (4, 1)))
+
+
+@pytest.mark.parametrize("paged", [False, True], ids=["contig", "paged"])
+def test_one_latent_cache(paged, monkeypatch):
+    """The layer holds the 4-bit cache alone, the same one whether its rows are uploaded at
+    once or a few at a time, with zeros where tokens are still to come."""
+    wl = _workload(paged=paged)
+    L0 = wl.seq_lens.astype(np.int64) - 5
+    whole = DsaDecodeLayer(wl, latent_fp4=True)
+    want_c, want_s = O.quantize_latent_fp4(H.f(wl.ckv.reshape(-1, 512)), whole.fp4_exp)
+    np.testing.assert_array_equal(whole.ckv_codes.cpu().numpy().reshape(want_c.shape), want_c)
+    np.testing.assert_array_equal(whole.ckv_scales.cpu().numpy().reshape(want_s.shape), want_s)
+    monkeypatch.setattr(DsaDecodeLayer, "_FP4_UPLOAD", 100)
+    lay = DsaDecodeLayer(wl, latent_fp4=True, decode_from=L0, manage_pages=paged)
+    assert lay.ckv is None and lay.fp4_exp == whole.fp4_exp
+    for b in range(wl.batch):
+        at = lay._token_rows(b, int(L0[b]), int(wl.seq_lens[b]))
+        want_c[at], want_s[at] = 0, 0
+    np.testing.assert_array_equal(lay.ckv_codes.cpu().numpy().reshape(want_c.shape), want_c)
+    np.testing.assert_array_equal(lay.ckv_scales.cpu().numpy().reshape(want_s.shape), want_s)

@@ -14,7 +14,7 @@ struct MlaF4Args {
     const uint8_t* scales;  // [cache rows, 32]
     const int32_t* token_ids;
     float* part_o;    // ns > 1: [rows, ns, heads, 512] unnormalised
-    float* part_ml;   // ... and [rows, ns, heads, 2] (maximum in log2 units, sum)
+    float* part_ml;   // ... and [rows, ns, heads, 2]: m and the sum of the weights 2^(s - m)
     float* olat;      // ns == 1, nullable
     uint16_t* olat16; // ns == 1, nullable (bf16)
     int32_t* status;

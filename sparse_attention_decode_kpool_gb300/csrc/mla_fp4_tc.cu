@@ -116,6 +116,12 @@ __device__ __forceinline__ float scatter16(float (&v)[16], int lane, Op op) {
     }
     return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
+// The smaller of the two, NaN where one is.
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p));
 }
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     float f[16];
 #pragma unroll
                     for (int h = 0; h < 16; ++h)
-                        f[h] = valid ? __uint_as_float(sv[h]) * sl2 : NEG_INF;
+                        f[h] = valid ? __fmul_rn(__uint_as_float(sv[h]), sl2) : NEG_INF;
                     const float mine =
                         scatter16(f, lane, [](float x, float y) { return fmaxf(x, y); });
                     if ((lane & 1) == 0) red[qd * kH + hb + (lane >> 1)] = mine;
@@ -510,7 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     tc_ld16(sv, tmem + lrow + hb);
 #pragma unroll
                     for (int h = 0; h < 16; ++h)
-                        sv[h] = __float_as_uint(fmaf(__uint_as_float(sv[h]), sl2, -e[h]));
+                        // The rounded logit that e was taken from, not the exact one: above
+                        // 2^24, where f32's steps are coarser than kUpTc, the largest weight
+                        // would else be anything. So it is 2^0 or more; e itself may round
+                        // down, hence the bound (2^16 overflows f16).
+                        sv[h] = __float_as_uint(
+                            min_nan(__fsub_rn(__fmul_rn(__uint_as_float(sv[h]), sl2), e[h]),
+                                    kUpTc + kLazy));
                     weights();
                 }
                 tc_fence_before();
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
 
             // ---- head sums over the lanes, then over the four lane quarters; the factors
             // of the output follow from them
-            float first = e[0];  // lane h: head hb + h's maximum
+            float first = e[0];  // lane h: head hb + h's
 #pragma unroll
             for (int h = 1; h < 16; ++h) first = lane == h ? e[h] : first;
             const float sum = scatter16(l, lane, [](float x, float y) { return x + y; });
@@ -531,13 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
             if (qd == 0 && lane < 16) {
                 const int h = hb + lane;
                 const float t = (sums[h] + sums[kH + h]) + (sums[2 * kH + h] + sums[3 * kH + h]);
-                // a NaN sum keeps its NaN
-                kout[h] = a.ns > 1 ? a.vscale * exp2f(-kUpTc) : (t == 0.f ? 0.f : a.vscale / t);
+                // a NaN sum keeps its NaN; a split's weights are relative to e itself
+                kout[h] = a.ns > 1 ? a.vscale : (t == 0.f ? 0.f : a.vscale / t);
                 if (a.ns > 1 && h < nh) {
                     const long long p =
                         ((long long)w.r * a.ns + w.split) * a.heads + w.hg * kH + h;
-                    *reinterpret_cast<float2*>(a.part_ml + p * 2) =
-                        make_float2(first + kUpTc, t * exp2f(-kUpTc));
+                    *reinterpret_cast<float2*>(a.part_ml + p * 2) = make_float2(first, t);
                 }
             }
             prev = w;

@@ -621,7 +621,7 @@ int dsa_decode_append_guarded(const int32_t* refs, const int32_t* serving, int l
  * dsa_quantize_latent_fp4): the latent row of token t is its decoded row, everything
  * else, the equations included, is dsa_sparse_mla_decode's. Each gathered row is 288
  * bytes. The matrix products run in f16 (decoded rows are exact in it, q is scaled by a
- * power of two per row, weights are rounded to 11 significant bits), sums in f32.
+ * power of two per row and head, weights are rounded to 11 significant bits), sums in f32.
  *
  * ckv_codes: token cache of width kv_lora_rank / 2 (u8); ckv_scales: token cache of width
  * kv_lora_rank / 16 (u8), laid out as pg says. olat [rows, heads, kv_lora_rank] f32 and

@@ -8,7 +8,7 @@
 //
 // The cache's power of two 2^cache_exp is taken out of v: it multiplies the logits'
 // scale and the output once, and the matrix products run on code * scale, which is exact
-// in f16. Q goes to f16 too, times a power of two per query row (f4_q_exp), and the
+// in f16. Q goes to f16 too, times a power of two per row and head (f4_q_exp), and the
 // probabilities are kept in f16 shifted up by kUp (they reach 2^kUp): a weight is then
 // rounded by at most 2^-12 of itself down to 2^-14 - kUp of the row's largest, where bf16
 // weights would carry 2^-9. Sums, maxima and the output accumulate in f32.
@@ -57,8 +57,8 @@ struct Smem {
     static constexpr int P = RAW + STAGES * CH * RAWB;
     static constexpr int RED = P + HP * CH * 2;   // [NW][HP] f32
     static constexpr int MASK = RED + NW * HP * 4;  // [STAGES][CH]
-    static constexpr int QMAX = MASK + STAGES * CH;
-    static constexpr int BYTES = QMAX + NW * 4;
+    static constexpr int SCALE = MASK + STAGES * CH;  // [HP] factors of the scores
+    static constexpr int BYTES = SCALE + HP * 4;
 };
 
 template <int MT>
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
     uint8_t* Ps = smem + S::P;
     float* red = reinterpret_cast<float*>(smem + S::RED);
     uint8_t* vmask = smem + S::MASK;
-    uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + S::QMAX);
+    float* scale = reinterpret_cast<float*>(smem + S::SCALE);
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q = lane & 3;
@@ -124,36 +124,44 @@ __global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
         cp_async_commit();
     }
 
-    // Q rows to f16 (zero rows past the last head), times 2^qe.
-    int qe;
+    // Q to f16 (zero rows past the last head), each head times its power of two; warp w has
+    // heads 2 MT w .. + 2 MT - 1, a lane two pieces of each.
     {
         const uint16_t* qb = a.qlat + ((long long)r * a.heads + head0) * KVL;
-        uint4 v[HP * 64 / NTH];
-        uint32_t m = 0;
+        const float base = a.scale * kLog2e4 * a.vscale;
+        uint4 v[2 * MT][2];
 #pragma unroll
-        for (int k = 0; k < HP * 64 / NTH; ++k) {
-            const int i = tid + k * NTH, row = i >> 6, c = i & 63;
-            v[k] = row < nh ? ldg16(qb + row * KVL + c * 8) : make_uint4(0, 0, 0, 0);
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[k].x), f4_finite_abs2(v[k].y)),
-                                     __vmaxu2(f4_finite_abs2(v[k].z), f4_finite_abs2(v[k].w))));
+        for (int i = 0; i < 2 * MT; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int h = 2 * MT * warp + i;
+                v[i][k] = h < nh ? ldg16(qb + h * KVL + (lane + 32 * k) * 8) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(v[i][k].x), f4_finite_abs2(v[i][k].y)),
+                                         __vmaxu2(f4_finite_abs2(v[i][k].z), f4_finite_abs2(v[i][k].w))));
+            const int h = 2 * MT * warp + i;
+            const int qe = f4_q_exp(__reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16)));
+            const float mul = pow2f(qe);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4*>(Qs + swz(h, lane + 32 * k)) =
+                    make_uint4(f4_q_half2(v[i][k].x, mul), f4_q_half2(v[i][k].y, mul),
+                               f4_q_half2(v[i][k].z, mul), f4_q_half2(v[i][k].w, mul));
+            if (lane == 0) scale[h] = base * pow2f(-qe);
         }
-        m = max(m & 0xffffu, m >> 16);
-        m = __reduce_max_sync(0xffffffffu, m);
-        if (lane == 0) qmax[warp] = m;
         __syncthreads();
-#pragma unroll
-        for (int w = 0; w < NW; ++w) m = max(m, qmax[w]);
-        qe = f4_q_exp(m);
-        const float mul = pow2f(qe);
-#pragma unroll
-        for (int k = 0; k < HP * 64 / NTH; ++k) {
-            const int i = tid + k * NTH, row = i >> 6, c = i & 63;
-            *reinterpret_cast<uint4*>(Qs + swz(row, c)) =
-                make_uint4(f4_q_half2(v[k].x, mul), f4_q_half2(v[k].y, mul),
-                           f4_q_half2(v[k].z, mul), f4_q_half2(v[k].w, mul));
-        }
     }
-    const float sl2 = a.scale * kLog2e4 * a.vscale * pow2f(-qe);
+    float sl0[MT], sl1[MT];  // scores to logits in log2 units, heads 16 i + g and + 8
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        sl0[i] = scale[16 * i + g];
+        sl1[i] = scale[16 * i + g + 8];
+    }
 
     float m0[MT], m1[MT], l0[MT], l1[MT];  // heads 16 i + g and + 8: running max, this warp's sums
     float oacc[MT][8][4];
@@ -212,10 +220,10 @@ __global__ void __launch_bounds__(NTH, 1) mla_f4_split_kernel(MlaF4Args a) {
         const bool ok1 = vmask[st * CH + warp * 8 + 2 * q + 1] != 0;
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
-            sacc[i][0] = ok0 ? sacc[i][0] * sl2 : -INFINITY;
-            sacc[i][1] = ok1 ? sacc[i][1] * sl2 : -INFINITY;
-            sacc[i][2] = ok0 ? sacc[i][2] * sl2 : -INFINITY;
-            sacc[i][3] = ok1 ? sacc[i][3] * sl2 : -INFINITY;
+            sacc[i][0] = ok0 ? sacc[i][0] * sl0[i] : -INFINITY;
+            sacc[i][1] = ok1 ? sacc[i][1] * sl0[i] : -INFINITY;
+            sacc[i][2] = ok0 ? sacc[i][2] * sl1[i] : -INFINITY;
+            sacc[i][3] = ok1 ? sacc[i][3] * sl1[i] : -INFINITY;
             float x0 = fmaxf(sacc[i][0], sacc[i][1]), x1 = fmaxf(sacc[i][2], sacc[i][3]);
             x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));

@@ -45,9 +45,11 @@ __device__ __forceinline__ long long f4_token_row(const MlaF4Args& a, int seq, i
     return -1;
 }
 
-// The power of two that brings a query row's largest finite magnitude (bf16 bits amax)
-// to [2^14, 2^15), where bf16 values convert to f16 without overflow and lose nothing
-// that the f32 sums would keep. 0 where the row is all zeros.
+// The power of two that brings the largest finite magnitude (bf16 bits amax) of one head's
+// query to [2^14, 2^15): its values convert to f16 without overflow, and exactly from there
+// down to 2^-28 of it. Below, they lose bits that the head's f32 sums have no room for. One
+// per head: heads of one row may differ by any factor, and each has a softmax of its own. 0
+// where the head is all zeros.
 __device__ __forceinline__ int f4_q_exp(uint32_t amax) {
     if (amax == 0u) return 0;
     const int e = max((int)(amax >> 7), 1) - 127;  // subnormals: their largest exponent

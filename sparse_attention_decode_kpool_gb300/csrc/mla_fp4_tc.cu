@@ -46,8 +46,10 @@ constexpr uint32_t kOffRows = kOffP + kT * 128;         // [kRing][kT] cache row
 constexpr uint32_t kOffRed = kOffRows + kRing * kT * 4;  // [4][kH] chunk maxima
 constexpr uint32_t kOffSums = kOffRed + 4 * kH * 4;      // [4][kH] head sums
 constexpr uint32_t kOffK = kOffSums + 4 * kH * 4;        // [kH] factors of the output
-constexpr uint32_t kOffQmax = kOffK + kH * 4;            // [16] per-warp maxima of |q|
-constexpr uint32_t kOffBar = kOffQmax + 16 * 4;
+constexpr uint32_t kOffQmax = kOffK + kH * 4;            // [16] a warp's largest and smallest head
+constexpr uint32_t kOffScale = kOffQmax + 16 * 4;        // [kH] factors of the scores
+constexpr uint32_t kOffOwn = kOffScale + kH * 4;         // [16] whether `scale` counts
+constexpr uint32_t kOffBar = kOffOwn + 16 * 4;
 constexpr int ROWS_FULL = 0;                    // [kRing]
 constexpr int ROWS_EMPTY = ROWS_FULL + kRing;   // [kRing]
 constexpr int LAT_FULL = ROWS_EMPTY + kRing;    // [4] quarter decoded
@@ -63,7 +65,7 @@ constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
 constexpr uint32_t kBytes = kOffMisc + 16;
 constexpr uint32_t kDyn = kBytes + 1024;
 static_assert(kDyn <= 227 * 1024, "shared memory");
-static_assert(kOffBar % 8 == 0 && kOffRows % 16 == 0, "alignment");
+static_assert(kOffBar % 8 == 0 && kOffRows % 16 == 0 && kOffScale % 16 == 0, "alignment");
 constexpr uint32_t kTmemCols = 512;  // S^T: columns [0, 64); O^T tile i: [64 + 64 i, + 64)
 constexpr int kWorkers = 16;
 constexpr int kThreads = (kWorkers + 4) * 32;
@@ -72,6 +74,9 @@ constexpr int kThreads = (kWorkers + 4) * 32;
 constexpr int kRegLow = 64, kRegHigh = 104;
 static_assert(4 * kRegHigh + kRegLow <= 5 * 96, "register split");
 constexpr float kLazy = 8.f;
+// Heads whose maxima of |q| are within 2^kSame share one power of two: the smallest one's
+// values are then exact in f16 down to 2^-23 of its maximum and off by 2^-31 of it below.
+constexpr int kSame = 8;
 constexpr float kUpTc = 7.f;  // weights reach 2^(kUpTc + kLazy) = 2^15
 
 // The descriptor `bytes` further on (an operand's next 16 columns or rows).
@@ -180,6 +185,16 @@ __device__ __forceinline__ void warp_wait_or_go(uint64_t* bar, uint32_t parity,
     }
 }
 
+// The 16 heads of S^T at taddr times their factors, in place. A function of its own: seldom
+// needed, and within the loop over chunks its instructions cost 0.3 % of a prefill.
+__device__ __noinline__ void own_scores(uint32_t taddr, const float* scale) {
+    uint32_t v[16];
+    tc_ld16(v, taddr);
+#pragma unroll
+    for (int h = 0; h < 16; ++h) v[h] = __float_as_uint(__uint_as_float(v[h]) * scale[h]);
+    tc_st16(taddr, v);
+    tc_wait_st();
+}
 struct Unit {
     int r, hg, split, t_begin, t_end, nch;
 };
@@ -203,6 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
     float* sums = reinterpret_cast<float*>(smem + kOffSums);
     float* kout = reinterpret_cast<float*>(smem + kOffK);
     uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + kOffQmax);
+    float* scale = reinterpret_cast<float*>(smem + kOffScale);
+    int* owns = reinterpret_cast<int*>(smem + kOffOwn);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
@@ -255,7 +272,6 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
         const int dj = 8 * warp + (lane >> 2), dp = lane & 3;
         const uint32_t drow = smem_u32(smem + kOffLat) + (dp >> 1) * kLatAtom + dj * 128;
         const float NEG_INF = __int_as_float(0xff800000);
-
         // This thread's part of a chunk's undecoded rows: per quarter k 16 bytes of codes
         // (channels 128 k + 32 dp .. + 31), and the eight scales of channels 128 dp .. + 127
         // (quarter dp; the token's four lanes exchange them at the decode).
@@ -318,56 +334,92 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++ku) {
             const Unit w = unit_of(a, hgroups, u);
             const int nh = min(kH, a.heads - w.hg * kH);
-            // ---- Q of the unit: f16, times 2^qe. The last unit's score products are
-            // complete (its last S^T was read), so the buffer is free; its value product
-            // may still run, and its output is written after this unit's first decode.
-            int qe;
+            // ---- Q of the unit: f16, times a power of two; warp w has heads 4 w .. 4 w + 3.
+            // One power for all heads, that of the largest, unless a head's own is more than
+            // 2^kSame above it; then every head has its own, and each chunk's scores are first
+            // multiplied by their heads' factors. (A factor per head throughout made a prefill
+            // 6 % slower, this 2 %.) The last unit's score products are complete (its last
+            // S^T was read), so the buffer is free; its value product may still run, and its
+            // output is written after this unit's first decode.
+            float sl2;  // scores to logits in log2 units
             {
                 const uint16_t* qb = a.qlat + ((long long)w.r * a.heads + w.hg * kH) * kKVL;
+                auto piece = [&](int k) {  // head 4 warp + k / 2, channels 8 lane + 256 (k & 1)
+                    return ldg16(qb + (4 * warp + (k >> 1)) * kKVL + 8 * lane + 256 * (k & 1));
+                };
+                auto store = [&](int k, const uint4& x, float mul) {
+                    const int h = 4 * warp + (k >> 1), c = lane + 32 * (k & 1);
+                    sts16(smem_u32(smem + kOffQ) + (c >> 3) * kQAtom + h * 128 +
+                              (((c & 7) ^ (h & 7)) << 4),
+                          make_uint4(f4_q_half2(x.x, mul), f4_q_half2(x.y, mul),
+                                     f4_q_half2(x.z, mul), f4_q_half2(x.w, mul)));
+                };
+                auto finite = [&](int h) {  // the largest finite |q| of head 4 warp + h
+                    uint32_t x = 0;
+                    for (int k = 2 * h; k < 2 * h + 2 && 4 * warp + h < nh; ++k) {
+                        const uint4 y = piece(k);
+                        x = __vmaxu2(x, __vmaxu2(__vmaxu2(f4_finite_abs2(y.x), f4_finite_abs2(y.y)),
+                                                 __vmaxu2(f4_finite_abs2(y.z), f4_finite_abs2(y.w))));
+                    }
+                    return __reduce_max_sync(0xffffffffu, max(x & 0xffffu, x >> 16));
+                };
                 uint4 v[8];
-                uint32_t m = 0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int i = threadIdx.x + 512 * k;
-                    v[k] = (i >> 6) < nh ? ldg16(qb + (long long)i * 8) : make_uint4(0, 0, 0, 0);
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (4 * warp + (k >> 1) < nh) v[k] = piece(k);
                 }
                 if (ku == 0) {  // the first chunk's rows, beside the first Q
                     wait(ROWS_FULL, 0);
                     request(0);
                 }
+                // the largest |q| of the warp's heads, and the smallest but for all-zero ones
+                uint32_t hi = 0, lo = 0x7fffu;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
-                                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
-                if (max(m & 0xffffu, m >> 16) >= 0x7f80u) {  // an Inf or NaN: the finite ones
-                    m = 0;
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t x = 0;
+#pragma unroll
+                    for (int k = 2 * h; k < 2 * h + 2; ++k)
+                        x = __vmaxu2(x, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                                                 __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+                    x = __reduce_max_sync(0xffffffffu, max(x & 0xffffu, x >> 16));
+                    hi = max(hi, x);
+                    lo = min(lo, x ? x : 0x7fffu);
+                }
+                if (hi >= 0x7f80u) {  // an Inf or NaN: the finite ones
+                    hi = 0, lo = 0x7fffu;
 #pragma unroll 1
-                    for (int k = 0; k < 8; ++k) {
-                        const int i = threadIdx.x + 512 * k;
-                        if ((i >> 6) >= nh) break;
-                        const uint4 x = ldg16(qb + (long long)i * 8);
-                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(f4_finite_abs2(x.x), f4_finite_abs2(x.y)),
-                                                 __vmaxu2(f4_finite_abs2(x.z), f4_finite_abs2(x.w))));
+                    for (int h = 0; h < 4; ++h) {
+                        const uint32_t x = finite(h);
+                        hi = max(hi, x);
+                        lo = min(lo, x ? x : 0x7fffu);
                     }
                 }
-                m = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
-                if (lane == 0) qmax[warp] = m;
+                if (lane == 0) qmax[warp] = hi << 16 | lo;
                 bar_sync(1, kWorkers * 32);
-                m = qmax[lane & 15];
-                qe = f4_q_exp(__reduce_max_sync(0xffffffffu, m));
-                const float mul = pow2f(qe);
+                const uint32_t hl = qmax[lane & 15];
+                const int qe = f4_q_exp(__reduce_max_sync(0xffffffffu, hl >> 16));
+                const float base = a.scale * kLog2e4 * a.vscale, mul = pow2f(qe);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int i = threadIdx.x + 512 * k, h = i >> 6, c = i & 63;
-                    sts16(smem_u32(smem + kOffQ) + (c >> 3) * kQAtom + h * 128 +
-                              (((c & 7) ^ (h & 7)) << 4),
-                          make_uint4(f4_q_half2(v[k].x, mul), f4_q_half2(v[k].y, mul),
-                                     f4_q_half2(v[k].z, mul), f4_q_half2(v[k].w, mul)));
+                for (int k = 0; k < 8; ++k) store(k, v[k], mul);
+                const bool own = f4_q_exp(__reduce_min_sync(0xffffffffu, hl & 0xffffu)) - qe > kSame;
+                sl2 = own ? 1.f : base * pow2f(-qe);
+                if (lane == 0) owns[warp] = own;  // read by this warp alone
+                if (own) {
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        const int x = f4_q_exp(finite(h));
+                        if (4 * warp + h < nh) {
+                            store(2 * h, piece(2 * h), pow2f(x));
+                            store(2 * h + 1, piece(2 * h + 1), pow2f(x));
+                        }
+                        if (lane == 0) scale[4 * warp + h] = base * pow2f(-x);
+                    }
+                    bar_sync(1, kWorkers * 32);  // `scale` is in place
                 }
                 fence_async_smem();
                 arrive(Q_FULL);
             }
-            const float sl2 = a.scale * kLog2e4 * a.vscale * pow2f(-qe);
             if (u + (int)gridDim.x < units) {  // the next unit's Q into L2, a line a thread
                 const Unit x = unit_of(a, hgroups, u + gridDim.x);
                 const int i = threadIdx.x;  // 64 channels of head i / 8
@@ -450,8 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     sts16(pc1, make_uint4(pk[4], pk[5], pk[6], pk[7]));
                     fence_async_smem();
                 };
+                const bool own = owns[warp] != 0;
                 wait(S_FULL, (uint32_t)(n & 1));
                 tc_fence_after();
+                if (own) {  // this warp's part of S^T times its heads' factors, in place
+                    own_scores(tmem + lrow + hb, scale + hb);
+                }
                 tc_ld16(sv, tmem + lrow + hb);
                 bool moving = c == 0;
                 if (!moving) {
@@ -514,12 +570,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                         tc_wait_st();
                     }
                     tc_ld16(sv, tmem + lrow + hb);
+                    // The rounded logits that e was taken from, not the exact ones: above
+                    // 2^24, where f32's steps are coarser than kUpTc, the largest weight
+                    // would else be anything. So it is 2^0 or more; e itself may round
+                    // down, hence the bound (2^16 overflows f16).
 #pragma unroll
                     for (int h = 0; h < 16; ++h)
-                        // The rounded logit that e was taken from, not the exact one: above
-                        // 2^24, where f32's steps are coarser than kUpTc, the largest weight
-                        // would else be anything. So it is 2^0 or more; e itself may round
-                        // down, hence the bound (2^16 overflows f16).
                         sv[h] = __float_as_uint(
                             min_nan(__fsub_rn(__fmul_rn(__uint_as_float(sv[h]), sl2), e[h]),
                                     kUpTc + kLazy));

@@ -629,11 +629,18 @@ int dsa_decode_append_guarded(const int32_t* refs, const int32_t* serving, int l
  * the projection of olat16. A row without a token gives zeros. A row of the cache that
  * is not selected is never read; a NaN in a selected row or in q stays in the results.
  * Limits: kv_lora_rank == 512; rows <= 65535; heads <= 4096; with o_absorb hidden % 64
- * == 0; 16-byte aligned tensors and workspace. The workspace's contents need not be
+ * == 0; 16-byte aligned tensors and workspace. The workspace is enough for either kernel
+ * (DSA_OPT_MLA_KERNEL may change between the query and the call). Its contents need not be
  * kept between calls; calls that overlap in time need one each.
+ *
+ * dsa_sparse_mla_decode_fp4_splits: how many parts the call cuts each row's tokens into,
+ * over a cache of cache_rows rows and with the option as it is: with one, the attention is
+ * one launch, else two.
  */
 int dsa_sparse_mla_decode_fp4_workspace(int rows, int heads, int kv_lora_rank, int out_width,
                                         int hidden, int with_o_absorb, size_t* bytes);
+int dsa_sparse_mla_decode_fp4_splits(int rows, int heads, int kv_lora_rank, int out_width,
+                                     long long cache_rows, int* splits);
 int dsa_sparse_mla_decode_fp4(const dsa_bf16* qlat, int rows, int heads, int kv_lora_rank,
                               const int32_t* row_seq, const uint8_t* ckv_codes,
                               const uint8_t* ckv_scales, int cache_exp, const dsa_paging* pg,

@@ -113,6 +113,7 @@ SIGNATURES = {
     "dsa_decode_append_guarded": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _F, _PG, _P, _I, _I, _I,
                                        _I, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P]),
     "dsa_sparse_mla_decode_fp4_workspace": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "dsa_sparse_mla_decode_fp4_splits": (_I, [_I, _I, _I, _I, _LL, ctypes.POINTER(_I)]),
     "dsa_sparse_mla_decode_fp4": (_I, [_P, _I, _I, _I, _P, _P, _P, _I, _PG, _P, _I, _F, _P, _I,
                                        _P, _P, _P, _P, _P, _SZ, _P]),
     "dsa_pages_workspace": (_I, [_LL, _I, ctypes.POINTER(_SZ)]),

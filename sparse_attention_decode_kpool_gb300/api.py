@@ -19,7 +19,8 @@ __all__ = ["paging", "dsa_compress", "dsa_compress_append", "dsa_indexer_store",
            "dsa_sparse_mla_decode_workspace", "dsa_sparse_mla_decode",
            "dsa_sparse_mla_decode_noalloc", "dsa_sparse_mla_decode_fp8", "dsa_quantize_latent",
            "dsa_quantize_latent_fp4", "dsa_dequantize_latent_fp4", "dsa_decode_append_fp4",
-           "dsa_sparse_mla_decode_fp4_workspace", "dsa_sparse_mla_decode_fp4",
+           "dsa_sparse_mla_decode_fp4_workspace", "dsa_sparse_mla_decode_fp4_splits",
+           "dsa_sparse_mla_decode_fp4",
            "page_arrays", "dsa_pages_workspace", "dsa_pages_free", "dsa_pages_fork",
            "dsa_pages_serve", "dsa_pages_reserve", "dsa_pages_compact", "DsaPageArrays",
            "dsa_frontend_workspace", "dsa_frontend", "dsa_latent_project_workspace",
@@ -618,6 +619,17 @@ def dsa_sparse_mla_decode_fp4_workspace(rows: int, heads: int, out_width: int, h
     check(_lib.load().dsa_sparse_mla_decode_fp4_workspace(
         int(rows), int(heads), int(kv_lora_rank), int(out_width), int(hidden),
         1 if with_o_absorb else 0, ctypes.byref(n)))
+    return int(n.value)
+
+
+def dsa_sparse_mla_decode_fp4_splits(rows: int, heads: int, out_width: int, cache_rows: int,
+                                     kv_lora_rank: int = 512) -> int:
+    """Parts that dsa_sparse_mla_decode_fp4 cuts each row's tokens into (more than one: a
+    second launch merges them)."""
+    n = ctypes.c_int(0)
+    check(_lib.load().dsa_sparse_mla_decode_fp4_splits(
+        int(rows), int(heads), int(kv_lora_rank), int(out_width), int(cache_rows),
+        ctypes.byref(n)))
     return int(n.value)
 
 

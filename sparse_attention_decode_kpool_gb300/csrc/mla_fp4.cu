@@ -490,7 +490,8 @@ F4Plan f4_plan(bool tc, int rows, int heads, int ow, int hidden, bool with_oabs,
     return p;
 }
 
-// Enough for either kernel: the call's choice depends on the cache's size too.
+// Enough for either kernel: the call's choice depends on the cache's size too, and a
+// workspace serves whichever kernel the option names when it is used.
 size_t f4_bytes(int rows, int heads, int ow, int hidden, bool with_oabs, int sms) {
     const size_t b0 = f4_plan(false, rows, heads, ow, hidden, with_oabs, sms).bytes;
     const size_t b1 = f4_plan(true, rows, heads, ow, hidden, with_oabs, sms).bytes;
@@ -559,6 +560,21 @@ extern "C" int dsa_sparse_mla_decode_fp4_workspace(int rows, int heads, int kv_l
     if (sms <= 0)
         return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4_workspace: no CUDA device");
     *bytes = f4_bytes(rows, heads, out_width, hidden, with_o_absorb != 0, sms);
+    return DSA_OK;
+}
+
+extern "C" int dsa_sparse_mla_decode_fp4_splits(int rows, int heads, int kv_lora_rank,
+                                                int out_width, long long cache_rows,
+                                                int* splits) {
+    if (!splits)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_sparse_mla_decode_fp4_splits: splits is NULL");
+    int rc = check_f4(rows, heads, kv_lora_rank, out_width, 0, false);
+    if (rc) return rc;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return fail(DSA_ERR_CUDA, "dsa_sparse_mla_decode_fp4_splits: no CUDA device");
+    const bool tc = f4_use_tc(rows, heads, out_width, cache_rows, sms);
+    *splits = f4_plan(tc, rows, heads, out_width, 0, false, sms).ns;
     return DSA_OK;
 }
 

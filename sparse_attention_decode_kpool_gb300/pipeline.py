@@ -580,7 +580,12 @@ class DsaDecodeLayer:
         """Library kernel launches one step() makes."""
         R, g = self.wl.rows, self.geom
         n = 3 if self.fuse_expand else 4  # score, select(+expand), [expand], split attention
-        if self._mla_workspace(0, False) > 0:
+        if self.latent_fp4:  # its workspace is for either kernel, whatever this one's splits
+            split = api.dsa_sparse_mla_decode_fp4_splits(
+                R, g.heads, g.out_width, self.ckv_scales.numel() // self.ckv_scales.shape[-1]) > 1
+        else:
+            split = self._mla_workspace(0, False) > 0
+        if split:
             n += 1  # split combine
         if self.o_absorb is not None:
             # tensor-core projection: one launch per 64 query rows; else the stream-K

@@ -4,9 +4,10 @@ import pytest
 import torch
 
 from oracle import dsa_oracle as O
-from sparse_attention_decode_kpool_gb300 import workloads as W
+from sparse_attention_decode_kpool_gb300 import api, workloads as W
 from sparse_attention_decode_kpool_gb300.pipeline import DsaDecodeLayer
 from tests import _harness as H
+from tests.test_gpu_fp4 import Case
 
 pytestmark = pytest.mark.gpu
 
@@ -85,3 +86,34 @@ def test_one_latent_cache(paged, monkeypatch):
         want_c[at], want_s[at] = 0, 0
     np.testing.assert_array_equal(lay.ckv_codes.cpu().numpy().reshape(want_c.shape), want_c)
     np.testing.assert_array_equal(lay.ckv_scales.cpu().numpy().reshape(want_s.shape), want_s)
+
+
+@pytest.mark.parametrize("rows,heads,ow", [(3, 8, 200), (100, 8, 512), (3, 64, 600), (100, 64, 256)])
+def test_splits_say_whether_there_is_a_merge(rows, heads, ow):
+    """The split count is one where the call leaves the workspace alone, and only there,
+    although the workspace is sized for either kernel."""
+    for which in ("auto", "mma", "tcgen05"):
+        with api.mla_kernel(which):
+            c = Case(97, rows, heads, ow, [700, 650]).cuda()
+            need = api.dsa_sparse_mla_decode_fp4_workspace(rows, heads, ow, 0, False)
+            splits = api.dsa_sparse_mla_decode_fp4_splits(rows, heads, ow, c.d_codes.numel() // 256)
+            c.ws = torch.full((need + 256,), 0x5A, dtype=torch.uint8, device="cuda")
+            c.run(torch.empty((rows, heads, 512), dtype=torch.bfloat16, device="cuda"))
+            part = rows * splits * heads * 512 * 4
+            assert bool((c.ws == 0x5A).all()) == (splits == 1), (which, splits)
+            if splits > 1:
+                assert need >= part and (c.ws[need:] == 0x5A).all()
+
+
+def test_layer_counts_its_launches():
+    """100 rows: the attention takes one launch, 3 rows: two; score, selection, projection
+    (one launch per 64 rows) and the prefetch are the same for both."""
+    g = W.Geometry(index_kpool=4, index_heads=32, index_head_dim=128, index_topk=512, heads=8,
+                   hidden=256)
+    for batch, splits in ((100, 1), (3, 8)):
+        wl = W.make_workload("fp4-launches", 67, g, [600] * batch, invalid_per_seq=0)
+        lay = DsaDecodeLayer(wl, latent_fp4=True)
+        rows = lay.ckv_scales.numel() // 32
+        assert api.dsa_sparse_mla_decode_fp4_splits(batch, 8, g.out_width, rows) == splits
+        assert lay._mla_workspace(0, False) > 0
+        assert lay.launches_per_step() == 3 + (splits > 1) + (batch + 63) // 64 + 1

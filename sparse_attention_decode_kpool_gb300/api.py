@@ -142,7 +142,11 @@ def paging(seq_lens: torch.Tensor, max_seq_len: int, block_table: Optional[torch
     pg.batch = int(seq_lens.numel())
     pg.max_seq_len = int(max_seq_len)
     pg.seq_lens = _ptr(seq_lens, torch.int32, "seq_lens")
+    pg.device = seq_lens.get_device()  # beside the C fields: where its tensors live
     if block_table is not None:
+        if block_table.get_device() != pg.device:
+            raise ValueError(f"block_table is on {block_table.device}, seq_lens on "
+                             f"{seq_lens.device}: one device per descriptor")
         pg.block_table = _ptr(block_table, torch.int32, "block_table")
         pg.max_blocks = int(block_table.shape[1])
         pg.block_size = int(block_size)
@@ -502,6 +506,14 @@ def _run(dev: int, stream, fn, *args) -> None:
         check(rc)
 
 
+def _described(d, dev: int, name: str) -> None:
+    """The tensors behind descriptor ``d`` (paging, page_arrays) are on device ``dev``."""
+    at = getattr(d, "device", dev)
+    if at != dev:
+        raise ValueError(f"{name} describes tensors on cuda:{at}, not on cuda:{dev}: one device "
+                         "per call")
+
+
 def _device_of(t: torch.Tensor, name: str) -> int:
     dev = t.get_device()
     if dev < 0:
@@ -570,6 +582,7 @@ def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float,
                         row_ctx, status, stream)
         return
     dev = _device_of(k_new, "k_new")
+    _described(pg, dev, "pg")
     bf16, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
     _run(dev, stream, _lib.load().dsa_decode_append_fp4,
          _dev_ptr(k_new, bf16, dev, "k_new"), _dev_ptr(gate_new, bf16, dev, "gate_new"),
@@ -597,6 +610,7 @@ def _append_guarded(refs, serving, latent: int, k_new, gate_new, ckv_new, ape, l
     if serving is not None and serving.numel() != pg.batch:
         raise ValueError(f"serving must be [{pg.batch}]")
     dev = _device_of(k_new, "k_new")
+    _described(pg, dev, "pg")
     bf16, u8, i32, f32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
     _run(dev, stream, _lib.load().dsa_decode_append_guarded,
          _dev_ptr(refs, i32, dev, "refs"), _dev_ptr(serving, i32, dev, "serving"), latent,
@@ -658,6 +672,7 @@ def dsa_sparse_mla_decode_fp4(qlat, row_seq, ckv_codes, ckv_scales, cache_exp: i
     if olat is not None and olat.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"olat must be float32 or bfloat16, got {olat.dtype}")
     dev = _device_of(ckv_codes, "ckv_codes")
+    _described(pg, dev, "pg")
     bf16, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
     p_olat = _dev_ptr(olat, None, dev, "olat")
     half = olat is not None and olat.dtype is bf16
@@ -683,10 +698,15 @@ def page_arrays(caches, num_blocks: int) -> DsaPageArrays:
         raise ValueError(f"{len(caches)} caches: at most {_lib.DSA_MAX_PAGE_ARRAYS}")
     pa = DsaPageArrays()
     pa.n, pa.num_pages = len(caches), int(num_blocks)
+    if caches:
+        pa.device = caches[0].get_device()  # beside the C fields: where the caches live
     for i, c in enumerate(caches):
         if c.dim() < 1 or int(c.shape[0]) != int(num_blocks):
             raise ValueError(f"cache {i} must be [{num_blocks}, ...], got {tuple(c.shape)}")
         pa.base[i] = _ptr(c, None, f"cache {i}")
+        if c.get_device() != pa.device:
+            raise ValueError(f"cache {i} is on {c.device}, cache 0 on cuda:{pa.device}: one "
+                             "device per descriptor")
         pa.page_bytes[i] = c.numel() // int(num_blocks) * c.element_size()
     return pa
 
@@ -703,7 +723,9 @@ def _pool(pg: DsaPaging, block_table, refs) -> int:
         raise ValueError(f"block_table must be [{pg.batch}, {pg.max_blocks}]")
     if refs.numel() != pg.num_blocks:
         raise ValueError(f"refs must be [{pg.num_blocks}]")
-    return _device_of(refs, "refs")
+    dev = _device_of(refs, "refs")
+    _described(pg, dev, "pg")
+    return dev
 
 
 def dsa_pages_free(seqs, pg: DsaPaging, block_table, seq_lens, refs, status=None,
@@ -756,6 +778,8 @@ def dsa_pages_reserve(pg: DsaPaging, block_table, refs, new_tokens: int,
     dev = _pool(pg, block_table, refs)
     if seqs is not None and seqs.numel() == 0:
         return  # an empty list has no address: to the C call it would mean every sequence
+    if arrays is not None:
+        _described(arrays, dev, "arrays")
     i32 = torch.int32
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _run(dev, stream, _lib.load().dsa_pages_reserve,
@@ -774,6 +798,8 @@ def dsa_pages_compact(pg: DsaPaging, block_table, refs, arrays: Optional[DsaPage
         raise ValueError(f"remap must be [{pg.num_blocks}]")
     if live is not None and live.numel() != 1:
         raise ValueError("live must hold one number")
+    if arrays is not None:
+        _described(arrays, dev, "arrays")
     i32 = torch.int32
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _run(dev, stream, _lib.load().dsa_pages_compact,

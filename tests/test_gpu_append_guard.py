@@ -335,3 +335,44 @@ def test_layer_ended_and_paused_sequences(kw):
     lay.fork_sequences([7], [2])  # a refused pair starts nothing
     lay.append_graph.replay()
     assert int(lay.status) == _lib.DSA_STATUS_BAD_SEQ and int(lay.seq_lens[2]) == 0
+
+
+def test_descriptors_of_another_device_are_refused():
+    """A descriptor whose tensors live on another device than the call's (its note of the
+    device is changed here; nothing is launched)."""
+    p = Shared("fp4", [20, 16], 8, 6, 0)
+    c, new = p.caches, tuple(p._rand((2, w), torch.bfloat16) for w in (IHD, IHD, KVL))
+    before = p.refs.clone()
+
+    def calls():
+        yield lambda: p._call(c, p.pg, p.lens, new)
+        yield lambda: p._call(c, p.pg, p.lens, new, refs=p.refs)
+        yield lambda: api.dsa_pages_free(_i32([0]), p.pg, p.table, p.lens, p.refs)
+        yield lambda: api.dsa_pages_fork(_i32([0]), _i32([1]), p.pg, p.table, p.lens, p.refs)
+        for f in reserve, compact:
+            yield f
+        q = torch.zeros((2, 8, KVL), dtype=torch.bfloat16, device="cuda")
+        yield lambda: api.dsa_sparse_mla_decode_fp4(q, None, c["codes"], c["scales"], -8, p.pg,
+                                                    p.table, 1.0, olat=q)
+
+    def reserve():
+        api.dsa_pages_reserve(p.pg, p.table, p.refs, 1, p.arrays, workspace=p.ws)
+
+    def compact():
+        api.dsa_pages_compact(p.pg, p.table, p.refs, p.arrays, workspace=p.ws)
+
+    assert p.pg.device == p.arrays.device == 0
+    p.pg.device = 1
+    for f in calls():
+        with pytest.raises(ValueError, match="pg describes tensors on cuda:1"):
+            f()
+    p.pg.device, p.arrays.device = 0, 1
+    for f in reserve, compact:
+        with pytest.raises(ValueError, match="arrays describes tensors on cuda:1"):
+            f()
+    torch.cuda.synchronize()
+    assert torch.equal(p.refs, before) and p.lens.tolist() == [20, 16]
+    with pytest.raises(ValueError, match="cache 1 must be a CUDA tensor|cache 1 is on"):
+        api.page_arrays([p.refs, p.refs.cpu()], len(p.refs))
+    with pytest.raises(ValueError, match="block_table"):
+        api.paging(p.lens, 64, p.table.cpu(), BS, 4)

@@ -376,3 +376,28 @@ def test_descriptors_of_another_device_are_refused():
         api.page_arrays([p.refs, p.refs.cpu()], len(p.refs))
     with pytest.raises(ValueError, match="block_table"):
         api.paging(p.lens, 64, p.table.cpu(), BS, 4)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_append_serving_list_contiguous(fmt):
+    """A contiguous cache, where there are no counts: the list alone, on a stream of its own."""
+    p = Shared(fmt, [20, 16, 3], 2, 0, 0)
+    c = {n: torch.stack([o[n] for o in p.own]) for n in p.widths}
+    plain = {n: t.clone() for n, t in c.items()}
+    lens, want = _i32([20, 16, 3]), _i32([20, 16, 3])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for serving in ([0, -1, 2], [-1, 1, -1], [-1, -1, -1]):
+            new = tuple(p._rand((3, w), torch.bfloat16) for w in (IHD, IHD, KVL))
+            p._call(c, api.paging(lens, p.cap), lens, new, serving=_i32(serving), status=status)
+            for b in range(3):
+                if serving[b] >= 0:
+                    p._call({n: t[b:b + 1] for n, t in plain.items()},
+                            api.paging(want[b:b + 1], p.cap), want[b:b + 1],
+                            tuple(x[b:b + 1] for x in new))
+        assert int(status) == 0 and lens.tolist() == want.tolist() == [21, 17, 4]
+        for n in c:
+            assert torch.equal(c[n].view(torch.uint8), plain[n].view(torch.uint8)), n
+    s.synchronize()

@@ -717,7 +717,8 @@ int dsa_pages_serve(const int32_t* parents, const int32_t* seqs, int n, int batc
  *
  * Sequences are served in list order (the first entry that names a sequence counts), all
  * of a sequence's pages or none: one for which the free pages do not suffice, after the
- * needs of those before it, keeps its row and sets DSA_STATUS_NO_PAGES. Pages that lose
+ * needs of those before it, keeps its row, shared pages included, and sets
+ * DSA_STATUS_NO_PAGES (dsa_decode_append_guarded does not write to those). Pages that lose
  * their last reference in the call are free from the next call on. A sequence whose
  * table row cannot hold the tokens is skipped with DSA_STATUS_CACHE_FULL.
  *

@@ -24,10 +24,11 @@ int set_max_smem(const void* kernel, int bytes);  // once per (device, kernel)
 // programmatic dependent of the work before it on the stream, and waits for that
 // work (pdl_wait) before it reads anything that work may have written; the only
 // earlier reads are of weights (the projection's first ring of o_absorb boxes).
-// Two kernels let their dependents start early (pdl_trigger): the split combine, so
-// that the projection fetches o_absorb meanwhile, and the front-end norm kernel,
-// ahead of the q GEMM. Elsewhere, dependent blocks waiting beside a running grid
-// slowed it. dsa_set_option(DSA_OPT_PDL, 0) turns the attribute off (the wait then
+// Some kernels let their dependents start early (pdl_trigger): the split combine and
+// the merge of the FP4 attention's splits, so that the projection fetches o_absorb
+// meanwhile; the front-end norm kernel, ahead of the q GEMM; and the page operators'
+// kernels but for the copies, each one chain of loads. Elsewhere, dependent blocks
+// waiting beside a running grid slowed it. dsa_set_option(DSA_OPT_PDL, 0) turns the attribute off (the wait then
 // returns at once).
 // Bytes of [p, p + bytes), from p on, that the last dsa_prefetch_l2 on this device
 // staged in L2 at evict_last priority (0 if p is outside that range).

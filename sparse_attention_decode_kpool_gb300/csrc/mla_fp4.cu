@@ -10,8 +10,9 @@
 // scale and the output once, and the matrix products run on code * scale, which is exact
 // in f16. Q goes to f16 too, times a power of two per row and head (f4_q_exp), and the
 // probabilities are kept in f16 shifted up by kUp (they reach 2^kUp): a weight is then
-// rounded by at most 2^-12 of itself down to 2^-14 - kUp of the row's largest, where bf16
-// weights would carry 2^-9. Sums, maxima and the output accumulate in f32.
+// rounded by at most 2^-11 of itself down to 2^(-14 - kUp) of the row's largest, where bf16
+// weights would carry 2^-8. Sums (of the rounded weights), maxima and the output
+// accumulate in f32.
 //
 // mla_f4_split_kernel -- one CTA of eight warps per (split of the token list, row, group
 // of up to 32 heads), mma.sync m16n8k16. A chunk is 64 tokens; warp w owns tokens
@@ -499,9 +500,9 @@ size_t f4_bytes(int rows, int heads, int ow, int hidden, bool with_oabs, int sms
 }
 
 // Which kernel: DSA_OPT_MLA_KERNEL's, else the one with the smaller estimate. Measured, mma
-// against tcgen05: 16 heads, 8 rows of 2,048 tokens 10.7 us against 11.9; 24 heads 13.3
-// against 12.2; 4 heads, 64 rows of 256 tokens 10.0 against 11.6, of 1,000 26 against 19;
-// 64 heads, 8 rows of 256 tokens 9.9 against 12.8, of 2,048 21 against 14.3.
+// against tcgen05: 16 heads, 8 rows of 2,048 tokens 10.6 us against 11.8; 24 heads 13.4
+// against 12.0; 4 heads, 64 rows of 256 tokens 9.9 against 11.8, of 1,000 26 against 19;
+// 64 heads, 8 rows of 256 tokens 9.8 against 12.4, of 2,048 21 against 14.0.
 bool f4_use_tc(int rows, int heads, int ow, long long cache_rows, int sms) {
     if (ow < 1 || cache_rows > 0x7fffffffLL) return false;
     switch (mla_kernel_choice()) {

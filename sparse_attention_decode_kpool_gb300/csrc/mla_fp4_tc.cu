@@ -8,7 +8,7 @@
 // swizzle atoms): one tile serves both products, K-major for the scores and MN-major for
 // the values. With Q (64 KB) and P (16 KB) there is no room for a second tile, nor for a
 // stage of undecoded rows; instead the next chunk's 288 bytes per token wait in registers
-// (20 of them in each of 512 threads), loaded a chunk ahead, so the tile's refill is
+// (18 of them in each of 512 threads), loaded a chunk ahead, so the tile's refill is
 // arithmetic and shared-memory stores only. It is refilled a quarter (128 columns) at a
 // time, as the value product of the chunk before leaves it, and the score product starts
 // on a quarter as soon as it is filled.
@@ -19,7 +19,8 @@
 // heads 16 (w >> 2) .. + 15. A head's running maximum is moved only when a score exceeds
 // it by more than kLazy (or there is none yet): one vote per chunk among the four warps
 // of a head group, and only after such a vote are maxima exchanged and O^T rescaled.
-// Weights are held at 2^kUp over the maximum, so with the lag they reach 2^15 in f16.
+// Weights are held at 2^kUpTc over the maximum, so with the lag they reach 2^15 in f16; the
+// sums that divide the output take them unrounded.
 //
 // Warps 16 and 18 resolve token ids to cache rows, chunks ahead; warp 17 issues the MMAs.
 //
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
             // One power for all heads, that of the largest, unless a head's own is more than
             // 2^kSame above it; then every head has its own, and each chunk's scores are first
             // multiplied by their heads' factors. (A factor per head throughout made a prefill
-            // 6 % slower, this 2 %.) The last unit's score products are complete (its last
+            // 6 % slower, this 1.3 %.) The last unit's score products are complete (its last
             // S^T was read), so the buffer is free; its value product may still run, and its
             // output is written after this unit's first decode.
             float sl2;  // scores to logits in log2 units

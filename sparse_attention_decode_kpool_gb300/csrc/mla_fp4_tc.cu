@@ -27,6 +27,8 @@
 // Waits are bounded: one that runs out sets DSA_STATUS_TIMEOUT and a flag that makes all
 // later waits return at once; every role then runs its loops to the end (rows stay
 // checked ones), so named barriers stay matched, and the tensor memory is released.
+#include <float.h>
+
 #include "mla_fp4.cuh"
 #include "tc.cuh"
 
@@ -428,10 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1) mla_f4_tc_kernel(MlaF4Args a, int
                     prefetch_l2(a.qlat + ((long long)x.r * a.heads + x.hg * kH) * kKVL + 64 * i);
             }
 
-            float e[16], l[16];  // maximum less kUpTc, this lane's sum of weights, per head
+            // maximum less kUpTc, this lane's sum of weights, per head. None yet: the lowest
+            // number, so that a logit that overflowed to -inf has weight 0 and not NaN.
+            float e[16], l[16];
 #pragma unroll
             for (int h = 0; h < 16; ++h) {
-                e[h] = NEG_INF;
+                e[h] = -FLT_MAX;
                 l[h] = 0.f;
             }
             for (int c = 0; c < w.nch; ++c, ++n) {

@@ -72,3 +72,34 @@ def test_large_logits(power, order):
             got = run_f32(c, which)
             assert np.isfinite(got).all(), which
             assert check_one_hot(c, got, range(64)) >= 64
+
+
+@pytest.mark.parametrize("order", ["low first", "low last", "mixed", "low only"])
+@pytest.mark.parametrize("rows", [2, 160], ids=["splits", "one split"])
+def test_logits_that_overflow_downwards(rows, order):
+    """Logits below f32's lowest number have no weight, wherever they stand in the list. One
+    channel of q counts: tokens with -1 there have a logit of -5e39, the others of 0 and so
+    equal weights (a power of two each: their mean, up to the f32 sums of at most 300 terms).
+    With no other token the sum of the weights is 0, and so is the result."""
+    c = Case(91, rows, 64, 600, [600], hole=0.0, exp=-8, scale=16.0)
+    x = np.random.default_rng(92).normal(0, 1, (600, KVL))
+    low = np.arange(600) < 300
+    x[:, 0] = np.where(low, -1.0, 0.0)
+    c.codes, c.scales = O.quantize_latent_fp4(H.f(torch.from_numpy(x).to(torch.bfloat16)), -8)
+    v = O.dequantize_latent_fp4(c.codes, c.scales, -8)
+    ids = np.arange(600)
+    if order == "low last":
+        ids = ids[::-1].copy()
+    elif order == "mixed":
+        ids = np.random.default_rng(93).permutation(600)
+    elif order == "low only":
+        ids[300:] = -1
+    c.ids[:] = ids
+    q = torch.zeros((rows, 64, KVL), dtype=torch.bfloat16)
+    q[:, :, 0] = 3e38
+    c.q = q
+    want = np.zeros(KVL) if order == "low only" else v[~low].mean(0)
+    tol = 300 * 2.0 ** -22 * np.abs(v[~low]).mean(0)
+    for which in KERNELS:
+        got = run_f32(c, which)
+        assert (np.abs(got - want) <= tol).all(), (which, got[0, 0, :4], want[:4])

@@ -62,6 +62,8 @@ extern "C" {
 #define DSA_KV_LORA_RANK 512 /* latent width the attention kernels are built for */
 #define DSA_MAX_KPOOL 16     /* most slots per pool dsa_compress handles         */
 #define DSA_MAX_PAGE_ARRAYS 128 /* most caches one dsa_page_arrays names          */
+#define DSA_MAX_EXPERTS 1024 /* most experts dsa_route chooses from               */
+#define DSA_MAX_TOPK 64      /* most experts it chooses for a row                 */
 
 typedef uint16_t dsa_bf16;
 
@@ -511,6 +513,21 @@ int dsa_quantize_latent(const dsa_bf16* x, long long rows, int kv_lora_rank, uin
                         float* scales, void* stream);
 
 /*
+ * dsa_dequantize_latent -- rows of an FP8 latent cache (or of any rows that
+ * dsa_quantize_latent or dsa_rmsnorm encoded) back as bf16, exactly: out row i is cache row
+ * row_ids[i], or row i with row_ids NULL. A row id outside [0, cache_rows) gives a row of
+ * zeros and sets DSA_STATUS_BAD_TOKEN.
+ *
+ * codes [cache_rows, kv_lora_rank] u8; scales [cache_rows, kv_lora_rank / 128] f32; row_ids
+ * [rows] i32 (device, nullable); out [rows, kv_lora_rank] bf16. Limits: kv_lora_rank a
+ * positive multiple of 128; codes and out 16-byte aligned; without row_ids, rows <=
+ * cache_rows.
+ */
+int dsa_dequantize_latent(const uint8_t* codes, const float* scales, long long cache_rows,
+                          const int32_t* row_ids, long long rows, int kv_lora_rank, dsa_bf16* out,
+                          int32_t* status, void* stream);
+
+/*
  * dsa_sparse_mla_decode_fp8 -- dsa_sparse_mla_decode over an FP8 latent cache
  * (mod.rs: the serve's decode kernel glm5next_dsa_mla_decode_fp8 reads the selected
  * tokens through the block table). The latent row of token t is the decoded
@@ -783,6 +800,68 @@ int dsa_frontend(const dsa_bf16* x, int rows, int hidden, const dsa_bf16* w_x, i
                  dsa_bf16* qidx, float* w, dsa_bf16* k_new, dsa_bf16* gate_new,
                  dsa_bf16* ckv_new, int32_t* status, void* workspace, size_t workspace_bytes,
                  void* stream);
+
+/*
+ * The other half of a decoder layer (the pages stop at the attention's output): the residual
+ * stream's norm, the router and the experts.
+ *
+ * dsa_rmsnorm -- a sublayer's output added to the residual stream, and the norm of the sum:
+ *
+ *   v = x + residual (f32; x alone with residual NULL)       residual_out = bf16(v)
+ *   out = bf16(v / sqrt(mean(v^2) + eps) * weight)
+ *   codes, scales = the FP8 rows that dsa_quantize_latent makes of out, byte for byte
+ *
+ * x, residual (nullable), residual_out (nullable), out [rows, width] bf16; weight [width]
+ * bf16; codes [rows, width] u8 and scales [rows, width / 128] f32 (both or neither). out is
+ * nullable with codes. residual_out and out may each be x or residual itself; any other
+ * overlap is refused. The squares are summed in f32: rows whose sum passes 3.4e38 give 0.
+ * Limits: codes need width % 128 == 0.
+ */
+int dsa_rmsnorm(const dsa_bf16* x, const dsa_bf16* residual, const dsa_bf16* weight,
+                long long rows, int width, float eps, dsa_bf16* residual_out, dsa_bf16* out,
+                uint8_t* codes, float* scales, void* stream);
+
+/*
+ * dsa_router_logits -- logits[r, e] = sum_i x[r, i] * w[e, i], bf16 x bf16 in f32, for
+ * dsa_route: the projection kernels of dsa_latent_project with f32 results.
+ *
+ * x [rows, hidden] bf16; w [n, hidden] bf16; logits [rows, n] f32. n may exceed the number of
+ * experts (rows of zeros up to a multiple of 64); dsa_route takes such rows with ld = n.
+ * Limits: hidden % 256 == 0; n % 64 == 0; 16-byte aligned tensors and workspace. w may be
+ * read before the kernel just before this call on the stream has finished, so that kernel
+ * must not write it.
+ */
+int dsa_router_logits_workspace(int rows, int hidden, int n, size_t* bytes);
+int dsa_router_logits(const dsa_bf16* x, int rows, int hidden, const dsa_bf16* w, int n,
+                      float* logits, int32_t* status, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * dsa_route -- the chosen experts of each row and their weights:
+ *
+ *   s_e = sigmoid(logit_e), or the softmax over the row's logits       c_e = s_e + bias_e
+ *   candidates: the experts with logit > -inf and c > -inf
+ *   groups (n_group > 1; group g is experts [g n/n_group, (g+1) n/n_group)): the topk_group
+ *     groups with the largest sum of their group_top best candidates' c, ties to the lowest
+ *   chosen: the topk candidates of those groups with the largest c, ties to the lowest id
+ *   weight_e = scale * s_e, with renorm scale * s_e / (sum of the chosen s)
+ *
+ * ids, weights [rows, topk + shared]: the chosen in ascending id, then -1 and 0 up to topk,
+ * then the `shared` experts n_experts, n_experts + 1, ... that every row takes with weight 1.
+ * The bias decides the choice only. The choice is that of 64-bit arithmetic on these f32
+ * inputs (as dsa_select, equal values go to the lowest id). A NaN logit or bias, and under
+ * softmax a logit of +inf, is no candidate, and makes the row's weights NaN.
+ *
+ * logits [rows, ld] f32, the row's first n_experts are read; bias [n_experts] f32 (nullable);
+ * score: DSA_ROUTE_*; group_top 1 or 2. Limits: n_experts <= DSA_MAX_EXPERTS, a multiple of
+ * n_group <= 32; topk <= DSA_MAX_TOPK and at most the experts of topk_group groups; shared <=
+ * DSA_MAX_TOPK.
+ */
+#define DSA_ROUTE_SIGMOID 0
+#define DSA_ROUTE_SOFTMAX 1
+int dsa_route(const float* logits, int rows, int n_experts, long long ld, int score,
+              const float* bias, int n_group, int topk_group, int group_top, int topk, int renorm,
+              float scale, int shared, int32_t* ids, float* weights, void* stream);
 
 /*
  * dsa_latent_project -- the absorbed output projection on its own (build.rs,

@@ -24,6 +24,10 @@ DSA_STATUS_CACHE_FULL = 8
 DSA_STATUS_BAD_SEQ = 16
 DSA_STATUS_NO_PAGES = 32
 DSA_MAX_PAGE_ARRAYS = 128
+DSA_MAX_EXPERTS = 1024
+DSA_MAX_TOPK = 64
+DSA_ROUTE_SIGMOID = 0
+DSA_ROUTE_SOFTMAX = 1
 DSA_LATENT_BF16 = 0
 DSA_LATENT_FP8 = 1
 DSA_LATENT_FP4 = 2
@@ -104,6 +108,7 @@ SIGNATURES = {
     "dsa_sparse_mla_decode": (_I, [_P, _I, _I, _I, _P, _P, _PG, _P, _I, _F, _P, _I, _P, _P, _P,
                                    _P, _SZ, _P]),
     "dsa_quantize_latent": (_I, [_P, ctypes.c_longlong, _I, _P, _P, _P]),
+    "dsa_dequantize_latent": (_I, [_P, _P, _LL, _P, _LL, _I, _P, _P, _P]),
     "dsa_sparse_mla_decode_fp8": (_I, [_P, _I, _I, _I, _P, _P, _P, _PG, _P, _I, _F, _P, _I, _P,
                                        _P, _P, _P, _SZ, _P]),
     "dsa_quantize_latent_fp4": (_I, [_P, _LL, _I, _I, _P, _P, _P]),
@@ -125,6 +130,10 @@ SIGNATURES = {
     "dsa_frontend_workspace": (_I, [_I, _I, _I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "dsa_frontend": (_I, [_P, _I, _I, _P, _I, _I, _I, _I, _I, _P, _P, _F, _P, _I, _P, _P, _P,
                           _P, _P, _P, _P, _P, _SZ, _P]),
+    "dsa_rmsnorm": (_I, [_P, _P, _P, _LL, _I, _F, _P, _P, _P, _P, _P]),
+    "dsa_router_logits_workspace": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
+    "dsa_router_logits": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _SZ, _P]),
+    "dsa_route": (_I, [_P, _I, _I, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P]),
     "dsa_latent_project_workspace": (_I, [_I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "dsa_latent_project": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _P, _SZ, _P]),
     "dsa_sparse_mla_decode_noalloc": (_I, [_P, _I, _I, _I, _P, _P, _PG, _P, _I, _F, _P, _I, _P,

@@ -18,12 +18,13 @@ __all__ = ["paging", "dsa_compress", "dsa_compress_append", "dsa_indexer_store",
            "dsa_select_expand", "dsa_expand_tail", "dsa_select_expand_tail",
            "dsa_sparse_mla_decode_workspace", "dsa_sparse_mla_decode",
            "dsa_sparse_mla_decode_noalloc", "dsa_sparse_mla_decode_fp8", "dsa_quantize_latent",
-           "dsa_quantize_latent_fp4", "dsa_dequantize_latent_fp4", "dsa_decode_append_fp4",
+           "dsa_dequantize_latent", "dsa_quantize_latent_fp4", "dsa_dequantize_latent_fp4", "dsa_decode_append_fp4",
            "dsa_sparse_mla_decode_fp4_workspace", "dsa_sparse_mla_decode_fp4_splits",
            "dsa_sparse_mla_decode_fp4",
            "page_arrays", "dsa_pages_workspace", "dsa_pages_free", "dsa_pages_fork",
            "dsa_pages_serve", "dsa_pages_reserve", "dsa_pages_compact", "DsaPageArrays",
-           "dsa_frontend_workspace", "dsa_frontend", "dsa_latent_project_workspace",
+           "dsa_frontend_workspace", "dsa_frontend", "dsa_rmsnorm", "dsa_router_logits_workspace",
+           "dsa_router_logits", "dsa_route", "dsa_latent_project_workspace",
            "dsa_latent_project", "dsa_select_k",
            "dsa_validate_config", "dsa_prefetch_l2", "dsa_set_option", "dsa_get_option", "mla_kernel",
            "select_kernel", "project_kernel", "DsaPaging"]
@@ -556,6 +557,35 @@ def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None,
          _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(status, torch.int32, dev, "status"))
 
 
+def _fp8_rows(codes, scales) -> int:
+    """Width of FP8 rows: codes [.., w] with scales [.., w/128] over the same rows."""
+    w = codes.size(-1)
+    if w % 128 or scales.size(-1) * 128 != w or scales.numel() * 128 != codes.numel():
+        raise ValueError("codes must be [.., w] and scales [.., w/128] of the same rows, w a "
+                         "multiple of 128")
+    return w
+
+
+def dsa_dequantize_latent(codes, scales, out, rows=None, status=None, stream=None) -> None:
+    """Rows of an FP8 latent cache back as bf16, exactly: all of them in order, or the cache
+    rows named by ``rows`` (i32, one per row of out)."""
+    kvl = _fp8_rows(codes, scales)
+    if out.size(-1) != kvl:
+        raise ValueError(f"out must be [.., {kvl}]")
+    n, cache_rows = out.numel() // kvl, codes.numel() // kvl
+    if rows is not None and rows.numel() != n:
+        raise ValueError(f"rows must hold {n} row numbers")
+    if rows is None and n != cache_rows:
+        raise ValueError(f"out must hold the cache's {cache_rows} rows")
+    if n == 0:
+        return
+    dev = _device_of(out, "out")
+    _run(dev, stream, _lib.load().dsa_dequantize_latent,
+         _dev_ptr(codes, torch.uint8, dev, "codes"), _dev_ptr(scales, torch.float32, dev, "scales"),
+         cache_rows, _dev_ptr(rows, torch.int32, dev, "rows"), n, kvl,
+         _dev_ptr(out, torch.bfloat16, dev, "out"), _dev_ptr(status, torch.int32, dev, "status"))
+
+
 def dsa_decode_append_fp4(k_new, gate_new, ckv_new, ape, ln_w, ln_b, eps: float, pg: DsaPaging,
                           seq_lens, first_key: int, kpool: int, k_raw, gate, token_valid,
                           ckv_codes, ckv_scales, cache_exp: int, kpool_out, pool_valid, ckv=None,
@@ -842,6 +872,80 @@ def dsa_frontend(x, w_x, q_a_norm, kv_a_norm, eps: float, w_q, qlat, qidx, w, k_
         _ptr(gate_new, torch.bfloat16, "gate_new"), _ptr(ckv_new, torch.bfloat16, "ckv_new"),
         _ptr(status, torch.int32, "status"), _ptr(workspace, None, "workspace"), ws_bytes,
         _stream(stream)))
+
+
+def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=None, codes=None,
+                scales=None, stream=None) -> None:
+    """RMS norm of x + residual (x alone without one) into ``out`` (bf16) and/or the FP8 rows
+    ``codes``, ``scales``; the sum itself into ``residual_out`` (which may be ``residual``)."""
+    shape, width = x.shape, x.size(-1)
+    for name, t in (("out", out), ("residual", residual), ("residual_out", residual_out),
+                    ("codes", codes)):
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {tuple(shape)} as x")
+    if weight.numel() != width:
+        raise ValueError(f"weight must be [{width}]")
+    if codes is not None and scales is not None:
+        _fp8_rows(codes, scales)
+    dev = _device_of(x, "x")
+    bf16 = torch.bfloat16
+    _run(dev, stream, _lib.load().dsa_rmsnorm,
+         _dev_ptr(x, bf16, dev, "x"), _dev_ptr(residual, bf16, dev, "residual"),
+         _dev_ptr(weight, bf16, dev, "weight"), x.numel() // width if width else 0, width,
+         float(eps), _dev_ptr(residual_out, bf16, dev, "residual_out"),
+         _dev_ptr(out, bf16, dev, "out"), _dev_ptr(codes, torch.uint8, dev, "codes"),
+         _dev_ptr(scales, torch.float32, dev, "scales"))
+
+
+def dsa_router_logits_workspace(rows: int, hidden: int, n: int) -> int:
+    b = ctypes.c_size_t(0)
+    check(_lib.load().dsa_router_logits_workspace(int(rows), int(hidden), int(n), ctypes.byref(b)))
+    return int(b.value)
+
+
+def dsa_router_logits(x, w, logits, status=None, workspace=None, stream=None) -> None:
+    """logits = x @ w.T with f32 results (x, w bf16; w's rows padded to a multiple of 64)."""
+    rows, hidden = x.shape
+    n = w.size(0)
+    if w.shape != (n, hidden) or logits.shape != (rows, n):
+        raise ValueError(f"w must be [n, {hidden}] and logits [{rows}, n]")
+    dev = _device_of(x, "x")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(dev, stream, _lib.load().dsa_router_logits,
+         _dev_ptr(x, torch.bfloat16, dev, "x"), rows, hidden, _dev_ptr(w, torch.bfloat16, dev, "w"),
+         n, _dev_ptr(logits, torch.float32, dev, "logits"),
+         _dev_ptr(status, torch.int32, dev, "status"), _dev_ptr(workspace, None, dev, "workspace"),
+         ws_bytes)
+
+
+_ROUTE_SCORE = {"sigmoid": _lib.DSA_ROUTE_SIGMOID, "softmax": _lib.DSA_ROUTE_SOFTMAX}
+
+
+def dsa_route(logits, topk: int, ids, weights, n_experts: Optional[int] = None,
+              score: str = "sigmoid", bias=None, n_group: int = 1, topk_group: int = 1,
+              group_top: int = 2, renorm: bool = True, scale: float = 1.0, shared: int = 0,
+              stream=None) -> None:
+    """The ``topk`` experts of each row of logits and their weights, then ``shared`` ones that
+    every row takes (see dsa_route in include/dsa.h). The row's first ``n_experts`` logits
+    count (all of them by default)."""
+    rows, ld = logits.shape
+    n = ld if n_experts is None else int(n_experts)
+    if n > ld:
+        raise ValueError(f"logits hold {ld} of {n} experts")
+    if score not in _ROUTE_SCORE:
+        raise ValueError(f"score {score!r}: one of {sorted(_ROUTE_SCORE)}")
+    if bias is not None and bias.numel() != n:
+        raise ValueError(f"bias must be [{n}]")
+    width = (rows, int(topk) + int(shared))
+    if ids.shape != width or weights.shape != width:
+        raise ValueError(f"ids and weights must be {list(width)}")
+    dev = _device_of(logits, "logits")
+    f32 = torch.float32
+    _run(dev, stream, _lib.load().dsa_route,
+         _dev_ptr(logits, f32, dev, "logits"), rows, n, ld, _ROUTE_SCORE[score],
+         _dev_ptr(bias, f32, dev, "bias"), int(n_group), int(topk_group), int(group_top), int(topk),
+         1 if renorm else 0, float(scale), int(shared), _dev_ptr(ids, torch.int32, dev, "ids"),
+         _dev_ptr(weights, f32, dev, "weights"))
 
 
 def dsa_latent_project_workspace(rows: int, heads: int, hidden: int,

@@ -58,6 +58,7 @@ extern "C" {
 #define DSA_STATUS_BAD_SEQ 16   /* dsa_pages_*: a listed sequence was skipped (see the calls)  */
 #define DSA_STATUS_NO_PAGES 32  /* dsa_pages_reserve: too few free pages for a sequence;
                                    dsa_decode_append_guarded: its next page is still shared   */
+#define DSA_STATUS_BAD_EXPERT 64 /* dsa_experts: an expert id outside [-1, n_experts) (skipped) */
 
 #define DSA_KV_LORA_RANK 512 /* latent width the attention kernels are built for */
 #define DSA_MAX_KPOOL 16     /* most slots per pool dsa_compress handles         */
@@ -862,6 +863,36 @@ int dsa_router_logits(const dsa_bf16* x, int rows, int hidden, const dsa_bf16* w
 int dsa_route(const float* logits, int rows, int n_experts, long long ld, int score,
               const float* bias, int n_group, int topk_group, int group_top, int topk, int renorm,
               float scale, int shared, int32_t* ids, float* weights, void* stream);
+
+/*
+ * dsa_experts -- the chosen experts' gated products and their weighted sum (what dsa_route
+ * chooses, `shared` experts included):
+ *
+ *   [gate | up] = w13[e] . x[r]       h = silu(gate) * up       (silu(v) = v / (1 + exp(-v)))
+ *   y[r] = bf16(sum_j weights[r, j] * (w2[e] . h)),   e = ids[r, j] >= 0
+ *
+ * with h rounded to bf16 (bf16 weights), or to E4M3 under the smallest 2^k that holds each
+ * 32 channels (FP8); products and sums in f32, in the order of ids. A row without an expert
+ * gives zeros; the same id twice in a row counts twice. An id below -1 or from n_experts on
+ * is skipped and sets DSA_STATUS_BAD_EXPERT. NaN and Inf in a row of x stay in that row.
+ *
+ * x [rows, hidden], w13 [n_experts, 2 inter, hidden] (inter gate rows, then inter up rows),
+ * w2 [n_experts, hidden, inter]: all bf16 with the three scales NULL, or all FP8 codes (u8)
+ * with x_scales [rows, hidden / 128], w13_scales [n_experts, 2 inter, hidden / 128],
+ * w2_scales [n_experts, hidden, inter / 128] f32, as dsa_quantize_latent or dsa_rmsnorm make
+ * them: the scales are powers of two, and only their exponents are read. ids, weights [rows,
+ * topk]; y [rows, hidden] bf16. Limits: hidden and inter multiples of 128; n_experts <=
+ * DSA_MAX_EXPERTS + DSA_MAX_TOPK; rows * topk <= 2^24; 16-byte aligned tensors (4 for scales, ids and
+ * weights) and workspace. The workspace's contents need not be kept between calls; calls
+ * that overlap in time need one each. `status` also gets DSA_STATUS_TIMEOUT if a wait inside
+ * a kernel gives up (about 1 s); y is then incomplete.
+ */
+int dsa_experts_workspace(int rows, int topk, int n_experts, int hidden, int inter, int fp8,
+                          size_t* bytes);
+int dsa_experts(const void* x, const float* x_scales, int rows, int hidden, const int32_t* ids,
+                const float* weights, int topk, const void* w13, const float* w13_scales,
+                const void* w2, const float* w2_scales, int n_experts, int inter, dsa_bf16* y,
+                int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * dsa_latent_project -- the absorbed output projection on its own (build.rs,

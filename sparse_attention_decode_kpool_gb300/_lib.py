@@ -23,6 +23,7 @@ DSA_STATUS_TIMEOUT = 4
 DSA_STATUS_CACHE_FULL = 8
 DSA_STATUS_BAD_SEQ = 16
 DSA_STATUS_NO_PAGES = 32
+DSA_STATUS_BAD_EXPERT = 64
 DSA_MAX_PAGE_ARRAYS = 128
 DSA_MAX_EXPERTS = 1024
 DSA_MAX_TOPK = 64
@@ -134,6 +135,8 @@ SIGNATURES = {
     "dsa_router_logits_workspace": (_I, [_I, _I, _I, ctypes.POINTER(_SZ)]),
     "dsa_router_logits": (_I, [_P, _I, _I, _P, _I, _P, _P, _P, _SZ, _P]),
     "dsa_route": (_I, [_P, _I, _I, _LL, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P]),
+    "dsa_experts_workspace": (_I, [_I, _I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "dsa_experts": (_I, [_P, _P, _I, _I, _P, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P, _SZ, _P]),
     "dsa_latent_project_workspace": (_I, [_I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "dsa_latent_project": (_I, [_P, _I, _I, _I, _P, _I, _P, _P, _P, _SZ, _P]),
     "dsa_sparse_mla_decode_noalloc": (_I, [_P, _I, _I, _I, _P, _P, _PG, _P, _I, _F, _P, _I, _P,

@@ -24,7 +24,8 @@ __all__ = ["paging", "dsa_compress", "dsa_compress_append", "dsa_indexer_store",
            "page_arrays", "dsa_pages_workspace", "dsa_pages_free", "dsa_pages_fork",
            "dsa_pages_serve", "dsa_pages_reserve", "dsa_pages_compact", "DsaPageArrays",
            "dsa_frontend_workspace", "dsa_frontend", "dsa_rmsnorm", "dsa_router_logits_workspace",
-           "dsa_router_logits", "dsa_route", "dsa_latent_project_workspace",
+           "dsa_router_logits", "dsa_route", "dsa_experts_workspace", "dsa_experts",
+           "dsa_latent_project_workspace",
            "dsa_latent_project", "dsa_select_k",
            "dsa_validate_config", "dsa_prefetch_l2", "dsa_set_option", "dsa_get_option", "mla_kernel",
            "select_kernel", "project_kernel", "DsaPaging"]
@@ -946,6 +947,47 @@ def dsa_route(logits, topk: int, ids, weights, n_experts: Optional[int] = None,
          _dev_ptr(bias, f32, dev, "bias"), int(n_group), int(topk_group), int(group_top), int(topk),
          1 if renorm else 0, float(scale), int(shared), _dev_ptr(ids, torch.int32, dev, "ids"),
          _dev_ptr(weights, f32, dev, "weights"))
+
+
+def dsa_experts_workspace(rows: int, topk: int, n_experts: int, hidden: int, inter: int,
+                          fp8: bool = False) -> int:
+    b = ctypes.c_size_t(0)
+    check(_lib.load().dsa_experts_workspace(int(rows), int(topk), int(n_experts), int(hidden),
+                                            int(inter), 1 if fp8 else 0, ctypes.byref(b)))
+    return int(b.value)
+
+
+def dsa_experts(x, ids, weights, w13, w2, y, x_scales=None, w13_scales=None, w2_scales=None,
+                status=None, workspace=None, stream=None) -> None:
+    """The weighted sum of each row's experts' gated products (see dsa_experts in
+    include/dsa.h): x, w13, w2 in bf16, or FP8 codes (u8) with their scales."""
+    rows, hidden = x.shape
+    topk = ids.size(-1)
+    n, _, inter = w2.shape
+    if w13.shape != (n, 2 * inter, hidden) or w2.size(1) != hidden:
+        raise ValueError(f"w13 must be [n, 2 inter, {hidden}] and w2 [n, {hidden}, inter]")
+    if ids.shape != (rows, topk) or weights.shape != (rows, topk):
+        raise ValueError(f"ids and weights must be [{rows}, topk]")
+    if y.shape != (rows, hidden):
+        raise ValueError(f"y must be [{rows}, {hidden}]")
+    dt = torch.bfloat16
+    if x_scales is not None or w13_scales is not None or w2_scales is not None:
+        if x_scales is None or w13_scales is None or w2_scales is None:
+            raise ValueError("FP8 takes the scales of x, w13 and w2, bf16 none")
+        dt = torch.uint8
+        if (x_scales.shape != (rows, hidden // 128) or w13_scales.shape != (n, 2 * inter, hidden // 128)
+                or w2_scales.shape != (n, hidden, inter // 128)):
+            raise ValueError("the scales must be [.., width/128] of the same rows as the codes")
+    dev = _device_of(x, "x")
+    f32 = torch.float32
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(dev, stream, _lib.load().dsa_experts,
+         _dev_ptr(x, dt, dev, "x"), _dev_ptr(x_scales, f32, dev, "x_scales"), rows, hidden,
+         _dev_ptr(ids, torch.int32, dev, "ids"), _dev_ptr(weights, f32, dev, "weights"), topk,
+         _dev_ptr(w13, dt, dev, "w13"), _dev_ptr(w13_scales, f32, dev, "w13_scales"),
+         _dev_ptr(w2, dt, dev, "w2"), _dev_ptr(w2_scales, f32, dev, "w2_scales"), n, inter,
+         _dev_ptr(y, torch.bfloat16, dev, "y"), _dev_ptr(status, torch.int32, dev, "status"),
+         _dev_ptr(workspace, None, dev, "workspace"), ws_bytes)
 
 
 def dsa_latent_project_workspace(rows: int, heads: int, hidden: int,

@@ -67,6 +67,11 @@ struct Paging {
 
 int check_paging(const dsa_paging* pg, int kpool, Paging* out);
 
+// Tiled tensor map of up to five dimensions, innermost first; strides (bytes) of dimensions
+// 1, 2, ... (zero fill out of bounds).
+int make_tmap(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int rank,
+              const uint64_t* dims, const uint64_t* strides, const uint32_t* box,
+              CUtensorMapSwizzle swizzle);
 // 2-D tiled tensor map over a row-major [outer, inner] array (zero fill out of
 // bounds), boxes of box_inner x box_outer elements, stored in shared memory with the
 // given swizzle (128-byte swizzle: box_inner x element size must be 128 bytes).
@@ -287,6 +292,16 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+// The five-dimensional form.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, int c3, int c4, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+        "r"(smem_u32(bar))
         : "memory");
 }
 // tma_load_2d with an L2 cache policy.

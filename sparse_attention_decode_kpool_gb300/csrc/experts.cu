@@ -1,0 +1,713 @@
+// dsa_experts: the chosen experts' gated products and their weighted sum.
+//
+//   z = w13[e] . x[r]  (I gate rows, I up rows)      h = silu(gate) * up
+//   y[r] = bf16(sum_j weight[r, j] * (w2[e_j] . h_j))        e_j = ids[r, j]
+//
+// h is rounded to bf16, or with FP8 weights to E4M3 under one 2^k per 32 channels: it is
+// the second product's tensor-core operand. All sums are f32.
+//
+// Four launches. (1) dispatch: one block per expert finds its (row, j) pairs in order and
+// how many pairs lie before them. (2) gate and up products with the activation, (3) the
+// down products, both by the same persistent tensor-core kernel, (4) the weighted sums.
+//
+// Each product has the weights as the MMA's M operand and the pairs as N: D^T [128 weight
+// rows x N pairs], N a multiple of 16 up to the tile's limit, so that few pairs cost few
+// tensor-core cycles and no padding, and the weights stream as in the projection. A work
+// item is 128 weight rows times up to kN pairs of one expert over all of K; items go to
+// the blocks round robin, the weight rows of one expert and pair tile next to each other
+// in time. The gate and up rows of the first product are interleaved 16 by 16 in the tile
+// (a five-dimensional TMA box), so both halves of a hidden channel lie in one warp's
+// lanes, 16 apart. The rows of x are gathered by TMA (four rows a copy), those of h are
+// contiguous in the pairs' order.
+//
+// Roles: warp 0 copies, warp 1 issues the MMAs, warps 4-7 take the accumulators (two, so
+// that the tensor cores run on meanwhile), with FP8 warps 8-11 put the scales into tensor
+// memory: one byte (the exponent) per row and 32 K values, for the block-scaled MMA. Waits
+// are bounded; one that gives up sets DSA_STATUS_TIMEOUT and every role leaves its loop.
+#include "fp8.cuh"
+#include "tc.cuh"
+
+namespace dsa {
+namespace {
+
+constexpr uint32_t kABytes = 128 * 128;  // 128 weight rows x 128 bytes of K
+constexpr int kStgLd = 80;               // floats per pair in the activation's staging
+
+template <bool F8, int N>
+struct EL {  // shared and tensor memory of one block
+    static constexpr uint32_t STAGE = kABytes + N * 128;
+    static constexpr int S = (int)((200u * 1024u) / STAGE);  // ring stages
+    static constexpr uint32_t RING = S * STAGE;
+    static constexpr uint32_t STG = RING;  // activation staging, 32 pairs x 64 channels
+    static constexpr uint32_t BARS = STG + 32 * kStgLd * 4;
+    static constexpr int NBARS = 3 * S + 5;  // full, empty, scales; 2 + 2 accumulators; drain
+    static constexpr uint32_t MISC = BARS + 8 * NBARS;
+    static constexpr uint32_t TAB = MISC + 16;  // int[2][n_experts + 1]
+    static constexpr int SFB = N <= 32 ? 1 : N <= 64 ? 2 : N <= 128 ? 4 : 8;  // columns of N scales
+    static constexpr int SFW = F8 ? 4 + (SFB < 4 ? 4 : SFB) : 0;              // of a stage's scales
+    static constexpr int COLS = 2 * N + S * SFW;
+    static constexpr uint32_t TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(COLS <= 512, "tensor memory");
+    static_assert(STAGE % 1024 == 0, "stage alignment");
+};
+
+struct GemmArgs {
+    const int32_t* counts;   // [E] pairs of each expert
+    const int32_t* starts;   // [E] pairs before them
+    const int32_t* pair_of;  // [pairs] pair (row * topk + j) at a place of the order
+    int n_experts, topk, pairs;
+    int hidden, inter;
+    int n_m;   // items per pair tile (row tiles of the weights)
+    int nst;   // K stages
+    // first product
+    uint16_t* h;         // bf16 [pairs, inter]
+    uint8_t* h8;         // E4M3 [pairs, inter]
+    uint8_t* h_scales;   // [pairs, inter / 32]
+    // second product
+    float* part;  // [pairs (row, j), hidden]
+    // FP8 scales
+    const float* a_scales;  // weights, [E * rows, K / 128]
+    const float* x_scales;  // [rows, hidden / 128]
+    int32_t* status;
+};
+
+struct Item {
+    int e, m, pos, n;  // expert, weight row tile, first place in the order, pairs
+};
+// Item w: tab[e] pair tiles lie before expert e's.
+template <int N>
+__device__ __forceinline__ Item item_of(const GemmArgs& a, const int* tab, const int* start, int w) {
+    Item it;
+    const int tile = w / a.n_m;
+    it.m = w - tile * a.n_m;
+    int lo = 0, hi = a.n_experts;  // tab[lo] <= tile < tab[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (tab[mid] <= tile)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    it.e = lo;
+    const int off = (tile - tab[lo]) * N;
+    it.pos = start[lo] + off;
+    it.n = min(N, start[lo + 1] - it.pos);
+    return it;
+}
+
+__device__ __forceinline__ void bar_sync_epilogue() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+
+template <int W>
+__device__ __forceinline__ void tc_st_cols(uint32_t t, const uint32_t* v) {
+    if constexpr (W == 1)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(t), "r"(v[0]) : "memory");
+    else if constexpr (W == 2)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};\n" ::"r"(t), "r"(v[0]), "r"(v[1]) : "memory");
+    else if constexpr (W == 4)
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(t), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3])
+                     : "memory");
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(t), "r"(v[0]),
+                     "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                     : "memory");
+}
+
+// Instruction descriptor, kind::mxf8f6f4: E4M3 x E4M3 -> f32, both K-major, UE8M0 scales,
+// byte `id` of each scale word.
+__device__ __forceinline__ uint32_t idesc_mxf8(int N, int id) {
+    return ((uint32_t)id << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | ((uint32_t)id << 29);
+}
+__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                          uint32_t sb, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(
+            d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+
+// UP: the first product (rows of x gathered, activation); else the second.
+template <bool F8, bool UP, int N>
+__global__ void __launch_bounds__(F8 ? 384 : 256, 1)
+    experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs a) {
+    using L = EL<F8, N>;
+    constexpr int S = L::S;
+    constexpr int kBox = N < 32 ? N : 32;  // rows of h per copy
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
+    uint64_t* empty = full + S;
+    uint64_t* sfull = empty + S;
+    uint64_t* acc_full = sfull + S;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    int* tab = reinterpret_cast<int*>(smem + L::TAB);
+    int* start = tab + a.n_experts + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+            mbar_init(sfull + s, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 4);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tc_alloc(tmem_slot, L::TMEM);
+    // The tables of the dispatch. The first product waits for it; the second starts early
+    // (its predecessor lets it once it has itself seen the dispatch finished) and waits
+    // below, before it touches h.
+    if constexpr (UP) {
+        pdl_wait();
+        pdl_trigger();
+    }
+    for (int i = threadIdx.x; i < a.n_experts; i += blockDim.x) {
+        tab[i] = (a.counts[i] + N - 1) / N;
+        start[i] = a.starts[i];
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive scan of the tile counts
+        int run = 0;
+        for (int i0 = 0; i0 < a.n_experts; i0 += 32) {
+            const int i = i0 + lane;
+            const int v = i < a.n_experts ? tab[i] : 0;
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (i < a.n_experts) tab[i] = run + x - v;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            tab[a.n_experts] = run;
+            const int last = a.n_experts - 1;
+            start[a.n_experts] = start[last] + a.counts[last];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int items = tab[a.n_experts] * a.n_m;
+
+    if (warp == 0) {
+        // ---------------- copies ----------------
+        int i = 0;  // stages issued
+        bool ok = true;
+        if constexpr (!UP) pdl_wait();
+        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const Item it = item_of<N>(a, tab, start, w);
+            int row[N / 4 <= 32 ? 4 : 8];
+            if constexpr (UP) {
+#pragma unroll
+                for (int q = 0; q < (N / 4 <= 32 ? 1 : 2); ++q)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int p = (lane + 32 * q) * 4 + j;
+                        row[4 * q + j] = a.pair_of[it.pos + (p < it.n ? p : 0)] / a.topk;
+                    }
+            }
+            const int quads = (it.n + 3) >> 2, boxes = (it.n + kBox - 1) / kBox;
+            const uint32_t bytes = kABytes + (UP ? quads * 512 : boxes * kBox * 128);
+            for (int st = 0; st < a.nst; ++st, ++i) {
+                const int s = i % S;
+                int go = 1;
+                if (lane == 0) {
+                    go = poll_wait(empty + s, (uint32_t)(((i / S) & 1) ^ 1), abort_flag, a.status);
+                    if (go) mbar_arrive_expect_tx(full + s, bytes);
+                }
+                go = __shfl_sync(0xffffffffu, go, 0);
+                if (!go) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = smem_u32(smem + s * L::STAGE);
+                const int k = st * (F8 ? 128 : 64);
+                if constexpr (UP) {
+                    if (lane == 0) tma_load_5d(dst, &tmA, k, 0, 0, it.m * 4, it.e, full + s);
+#pragma unroll
+                    for (int q = 0; q < (N / 4 <= 32 ? 1 : 2); ++q)
+                        if (lane + 32 * q < quads)
+                            tma_gather4(dst + kABytes + (lane + 32 * q) * 512, &tmB, k, row[4 * q], row[4 * q + 1],
+                                        row[4 * q + 2], row[4 * q + 3], full + s);
+                } else {
+                    if (lane == 0) tma_load_2d(dst, &tmA, k, it.e * a.hidden + it.m * 128, full + s);
+                    if (lane < boxes)
+                        tma_load_2d(dst + kABytes + lane * kBox * 128, &tmB, k, it.pos + lane * kBox, full + s);
+                }
+            }
+        }
+        // the copies issued have landed before the block may leave its memory
+        if (lane == 0)
+            for (int j = i > S ? i - S : 0; j < i; ++j)
+                if (!mbar_wait(full + (j % S), (uint32_t)((j / S) & 1))) break;
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issue ----------------
+        if (lane == 0) {
+            int i = 0, t = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; w < items && ok; w += gridDim.x, ++t) {
+                const Item it = item_of<N>(a, tab, start, w);
+                const int n = (it.n + 15) & ~15;
+                const uint32_t d = tmem + (t & 1) * N;
+                if (!poll_wait(acc_empty + (t & 1), (uint32_t)(((t >> 1) & 1) ^ 1), abort_flag, a.status)) break;
+                for (int st = 0; st < a.nst; ++st, ++i) {
+                    const int s = i % S;
+                    const uint32_t par = (uint32_t)((i / S) & 1);
+                    ok = poll_wait(full + s, par, abort_flag, a.status);
+                    if constexpr (F8) ok = ok && poll_wait(sfull + s, par, abort_flag, a.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + s * L::STAGE), sb = sa + kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        if constexpr (F8) {
+                            const uint32_t sf = tmem + 2 * N + s * L::SFW;
+                            tc_mma_mx(d, sw128_desc(sa + 32 * kk), sw128_desc(sb + 32 * kk), idesc_mxf8(n, kk), sf,
+                                      sf + 4, (st | kk) != 0);
+                        } else {
+                            tc_mma(d, sw128_desc(sa + 32 * kk), sw128_desc(sb + 32 * kk), idesc_bf16(128, n),
+                                   (st | kk) != 0);
+                        }
+                    }
+                    tc_commit(empty + s);
+                }
+                if (ok) tc_commit(acc_full + (t & 1));
+            }
+            tc_commit(drain);  // every MMA issued: all of them, or those before an abort
+            if (!mbar_wait(drain, 0)) flag_status(a.status, DSA_STATUS_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 8) {
+        // ---------------- accumulators ----------------
+        const int ew = warp - 4, et = threadIdx.x - 128;
+        float* stg = reinterpret_cast<float*>(smem + L::STG);
+        int t = 0;
+        for (int w = blockIdx.x; w < items; w += gridDim.x, ++t) {
+            const Item it = item_of<N>(a, tab, start, w);
+            int got = 1;
+            if (lane == 0) got = poll_wait(acc_full + (t & 1), (uint32_t)((t >> 1) & 1), abort_flag, a.status);
+            got = __shfl_sync(0xffffffffu, got, 0);
+            if constexpr (UP) {  // the four warps share barriers below: they leave together
+                int all;
+                asm volatile(
+                    "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\n"
+                    "barrier.cta.red.and.pred q, 1, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+                    : "=r"(all)
+                    : "r"(got)
+                    : "memory");
+                got = all;
+            }
+            if (!got) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + ((uint32_t)(32 * ew) << 16) + (t & 1) * N;
+            const int n16 = (it.n + 15) & ~15;
+            for (int c0 = 0; c0 < it.n; c0 += 32) {
+                uint32_t v[32];
+                if (N >= 32 && n16 - c0 > 16) {
+                    tc_ld32(v, acc + c0);
+                    tc_wait_ld(v);
+                } else {
+                    uint32_t (&u)[32] = v;
+                    asm volatile(
+                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
+                        "%12,%13,%14,%15}, [%16];\n"
+                        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+                          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+                          "=r"(u[14]), "=r"(u[15])
+                        : "r"(acc + c0));
+#pragma unroll
+                    for (int j = 16; j < 32; ++j) v[j] = 0u;
+                    tc_wait_ld(v);
+                }
+                if (c0 + 32 >= it.n) {  // the last columns are in registers
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(acc_empty + (t & 1));
+                }
+                if constexpr (UP) {
+                    bar_sync_epilogue();  // the staging is free
+                    const bool hi = lane >= 16;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2) {
+                        // lanes below 16 hold gates and take column c, the others hold ups and take c + 1
+                        const float mine = __uint_as_float(hi ? v[c + 1] : v[c]);
+                        const float other =
+                            __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? v[c] : v[c + 1]), 16);
+                        const float g = hi ? other : mine, u = hi ? mine : other;
+                        stg[(c + (hi ? 1 : 0)) * kStgLd + 16 * ew + (lane & 15)] = g / (1.f + __expf(-g)) * u;
+                    }
+                    bar_sync_epilogue();
+                    const int p = et >> 2, seg = et & 3;  // pair, 16 channels
+                    float f[16];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 q = *reinterpret_cast<const float4*>(stg + p * kStgLd + seg * 16 + 4 * j);
+                        f[4 * j] = q.x;
+                        f[4 * j + 1] = q.y;
+                        f[4 * j + 2] = q.z;
+                        f[4 * j + 3] = q.w;
+                    }
+                    const bool live = c0 + p < it.n;
+                    const long long at = (long long)(it.pos + c0 + p) * a.inter + it.m * 64 + seg * 16;
+                    if constexpr (F8) {
+                        float m = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[j]));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        const int e = fp8_scale_exp(m);
+                        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            o[j] = e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
+                                   (e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16);
+                        if (live) {
+                            *reinterpret_cast<uint4*>(a.h8 + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (!(seg & 1)) a.h_scales[at >> 5] = (uint8_t)(e + 127);
+                        }
+                    } else if (live) {
+                        uint4 o[2];
+                        o[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                          pack_bf16x2(f[6], f[7]));
+                        o[1] = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]),
+                                          pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
+                        uint4* dst = reinterpret_cast<uint4*>(a.h + at);
+                        dst[0] = o[0];
+                        dst[1] = o[1];
+                    }
+                } else {
+                    const int mine = a.pair_of[it.pos + (c0 + lane < it.n ? c0 + lane : 0)];
+                    float* to = a.part + it.m * 128 + 32 * ew + lane;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const int pair = __shfl_sync(0xffffffffu, mine, c);
+                        if (c0 + c < it.n) to[(long long)pair * a.hidden] = __uint_as_float(v[c]);
+                    }
+                }
+            }
+        }
+    } else if (F8 && warp >= 8) {
+        // ---------------- scales ----------------
+        // Each warp writes all scales of a stage to its own lane quarter (the block-scaled
+        // MMA reads a copy in each): word j of lane l is row 32 j + l. Four stages' scales
+        // are requested ahead.
+        const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * N;
+        constexpr int NB = N <= 32 ? 1 : N / 32;
+        int i = 0;
+        bool ok = true;
+        if constexpr (!UP) pdl_wait();
+        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+            const Item it = item_of<N>(a, tab, start, w);
+            const float* pa[4];
+            const float* pb[NB];
+            const long long ks = a.nst;  // scales per row: one per stage
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long r = UP ? (long long)it.e * 2 * a.inter + (lane >> 4) * a.inter + it.m * 64 + 16 * j + (lane & 15)
+                                       : (long long)it.e * a.hidden + it.m * 128 + 32 * j + lane;
+                pa[j] = a.a_scales + r * ks;
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const int p = it.pos + (32 * j + lane < it.n ? 32 * j + lane : 0);
+                pb[j] = UP ? a.x_scales + (a.pair_of[p] / a.topk) * ks
+                           : reinterpret_cast<const float*>(a.h_scales) + p * ks;  // four exponents a word
+            }
+            for (int st0 = 0; st0 < a.nst && ok; st0 += 4) {
+                uint32_t va[4][4], vb[4][L::SFB];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (st0 + q < a.nst) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            va[q][j] = ((__float_as_uint(__ldg(pa[j] + st0 + q)) >> 23) & 255u) * 0x01010101u;
+#pragma unroll
+                        for (int j = 0; j < L::SFB; ++j) {
+                            const uint32_t b = j < NB ? __float_as_uint(pb[j < NB ? j : 0][st0 + q]) : 0u;
+                            vb[q][j] = UP ? ((b >> 23) & 255u) * 0x01010101u : b;
+                        }
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (st0 + q >= a.nst || !ok) break;
+                    const int s = i % S;
+                    int go = 1;
+                    if (lane == 0)
+                        go = poll_wait(empty + s, (uint32_t)(((i / S) & 1) ^ 1), abort_flag, a.status);
+                    go = __shfl_sync(0xffffffffu, go, 0);
+                    if (!go) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    tc_st_cols<4>(quarter + s * L::SFW, va[q]);
+                    tc_st_cols<L::SFB>(quarter + s * L::SFW + 4, vb[q]);
+                    tc_wait_st();
+                    tc_fence_before();
+                    if (lane == 0) mbar_arrive(sfull + s);
+                    ++i;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tc_dealloc(tmem, L::TMEM);
+    }
+}
+
+// One block per expert: its pairs in ascending order behind those of the experts before it.
+// Each warp looks at one contiguous part of the ids twice: how many are its expert's (and,
+// over the block, how many belong to lower ones), then which.
+__global__ void __launch_bounds__(1024) dispatch_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts,
+                                                        int32_t* counts, int32_t* starts, int32_t* pair_of,
+                                                        int32_t* status) {
+    __shared__ int eq_w[32], lt_w[32];
+    pdl_wait();
+    const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int per = (int)(((long long)pairs + 32 * warps - 1) / (32 * warps)) * 32;
+    const long long p0 = (long long)warp * per;
+    const int lo = (int)(p0 < pairs ? p0 : pairs), hi = (int)(p0 + per < pairs ? p0 + per : pairs);
+    int eq = 0, lt = 0;
+    bool bad = false;
+    for (int p = lo + lane; p < hi; p += 32) {
+        const int id = __ldg(ids + p);
+        eq += id == e;
+        lt += id >= 0 && id < e;
+        bad |= id < -1 || id >= n_experts;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        eq += __shfl_xor_sync(0xffffffffu, eq, o);
+        lt += __shfl_xor_sync(0xffffffffu, lt, o);
+    }
+    if (lane == 0) {
+        eq_w[warp] = eq;
+        lt_w[warp] = lt;
+    }
+    if (e == 0 && bad) flag_status(status, DSA_STATUS_BAD_EXPERT);
+    __syncthreads();
+    int before = 0, all = 0, base = 0;
+    for (int i = 0; i < warps; ++i) {
+        if (i < warp) before += eq_w[i];
+        all += eq_w[i];
+        base += lt_w[i];
+    }
+    if (threadIdx.x == 0) {
+        counts[e] = all;
+        starts[e] = base;
+    }
+    int at = base + before;
+    if (eq == 0) return;
+    for (int p = lo; p < hi; p += 32) {
+        const bool mine = p + lane < hi && __ldg(ids + p + lane) == e;
+        const uint32_t who = __ballot_sync(0xffffffffu, mine);
+        if (mine) pair_of[at + __popc(who & ((1u << lane) - 1u))] = p + lane;
+        at += __popc(who);
+    }
+}
+
+// y[r] = sum over the row's experts, in their order in ids, of weight times partial.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) combine_kernel(const float* __restrict__ part,
+                                                              const int32_t* __restrict__ ids,
+                                                              const float* __restrict__ weights, int rows,
+                                                              int topk, int n_experts, int hidden,
+                                                              uint16_t* __restrict__ y) {
+    pdl_wait();
+    const int per_row = hidden / 4;
+    const long long n = (long long)rows * per_row;
+    for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kSumThreads) {
+        const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j = 0; j < topk; ++j) {
+            const long long p = (long long)r * topk + j;
+            const int id = __ldg(ids + p);
+            if (id < 0 || id >= n_experts) continue;
+            const float w = __ldg(weights + p);
+            const float4 v = __ldg(reinterpret_cast<const float4*>(part + p * hidden) + c);
+            s.x = fmaf(w, v.x, s.x);
+            s.y = fmaf(w, v.y, s.y);
+            s.z = fmaf(w, v.z, s.z);
+            s.w = fmaf(w, v.w, s.w);
+        }
+        reinterpret_cast<uint2*>(y)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+}
+
+size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct Plan {
+    size_t counts, starts, pair_of, h, h_scales, part, bytes;
+};
+Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
+    Plan p;
+    size_t at = 0;
+    p.counts = at;
+    at += al256((size_t)n_experts * 4);
+    p.starts = at;
+    at += al256((size_t)n_experts * 4);
+    p.pair_of = at;
+    at += al256((size_t)pairs * 4);
+    p.h = at;
+    at += al256((size_t)pairs * inter * (f8 ? 1 : 2));
+    p.h_scales = at;
+    at += f8 ? al256((size_t)pairs * (inter / 32)) : 0;
+    p.part = at;
+    at += al256((size_t)pairs * hidden * 4);
+    p.bytes = at;
+    return p;
+}
+
+int check_experts(const char* name, int rows, int topk, int n_experts, int hidden, int inter) {
+    if (rows < 0 || topk < 1 || n_experts < 1 || hidden < 1 || inter < 1)
+        return fail(DSA_ERR_INVALID_ARG, "%s: rows %d, topk %d, n_experts %d, hidden %d, inter %d", name, rows, topk,
+                    n_experts, hidden, inter);
+    if (hidden % 128 != 0 || inter % 128 != 0)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: hidden %d and inter %d must be multiples of 128", name, hidden, inter);
+    if (n_experts > DSA_MAX_EXPERTS + DSA_MAX_TOPK || (long long)n_experts * 2 * inter > 0x7fffffffLL ||
+        (long long)n_experts * hidden > 0x7fffffffLL)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: too many experts (%d)", name, n_experts);
+    if ((long long)rows * topk > (1 << 24))
+        return fail(DSA_ERR_UNSUPPORTED, "%s: rows * topk %lld > %d", name, (long long)rows * topk, 1 << 24);
+    return DSA_OK;
+}
+
+template <bool F8, bool UP, int N>
+int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_rows, int sms, cudaStream_t st) {
+    using L = EL<F8, N>;
+    static_assert(L::TAB + 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1) + 1024 <= 227 * 1024, "shared memory");
+    const int dyn = (int)(L::TAB + 8 * (a.n_experts + 1) + 1024);
+    int rc = set_max_smem((const void*)experts_kernel<F8, UP, N>, 227 * 1024);
+    if (rc) return rc;
+    const CUtensorMapDataType dt = F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t es = F8 ? 1 : 2, H = a.hidden, I = a.inter, E = a.n_experts;
+    const uint32_t bk = F8 ? 128 : 64;
+    CUtensorMap tmA, tmB;
+    if (UP) {
+        const uint64_t dims[5] = {H, 16, 2, I / 16, E};
+        const uint64_t strides[4] = {H * es, I * H * es, 16 * H * es, 2 * I * H * es};
+        const uint32_t box[5] = {bk, 16, 2, 4, 1};
+        rc = make_tmap(&tmA, dt, weights, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (rc) return rc;
+        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+        rc = make_tmap_2d(&tmA, dt, weights, I, E * H, I * es, bk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (rc) return rc;
+        rc = make_tmap_2d(&tmB, dt, b, I, (uint64_t)b_rows, I * es, bk, N < 32 ? N : 32, CU_TENSOR_MAP_SWIZZLE_128B);
+    }
+    if (rc) return rc;
+    cudaError_t e = launch_pdl(experts_kernel<F8, UP, N>, dim3((unsigned)sms), dim3(F8 ? 384 : 256), (size_t)dyn, st,
+                               tmA, tmB, a);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_experts launch");
+    return DSA_OK;
+}
+
+template <bool F8, bool UP>
+int gemm_dispatch(const GemmArgs& a, const void* weights, const void* b, int b_rows, int sms, cudaStream_t st) {
+    // Pairs per tile: what an expert gets on average. Fewer leave more of the ring to the
+    // weights in flight; an expert with more pairs takes several tiles.
+    const long long mean = (a.pairs + a.n_experts - 1) / a.n_experts;
+    if (mean <= 8) return gemm_launch<F8, UP, 16>(a, weights, b, b_rows, sms, st);
+    if (mean <= 24) return gemm_launch<F8, UP, 32>(a, weights, b, b_rows, sms, st);
+    if (mean <= 48) return gemm_launch<F8, UP, 64>(a, weights, b, b_rows, sms, st);
+    if (mean <= 96) return gemm_launch<F8, UP, 128>(a, weights, b, b_rows, sms, st);
+    return gemm_launch<F8, UP, F8 ? 192 : 256>(a, weights, b, b_rows, sms, st);
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+extern "C" int dsa_experts_workspace(int rows, int topk, int n_experts, int hidden, int inter, int fp8,
+                                     size_t* bytes) {
+    if (!bytes) return fail(DSA_ERR_INVALID_ARG, "dsa_experts_workspace: bytes is NULL");
+    int rc = check_experts("dsa_experts_workspace", rows, topk, n_experts, hidden, inter);
+    if (rc) return rc;
+    *bytes = plan_of((long long)rows * topk, n_experts, hidden, inter, fp8 != 0).bytes;
+    return DSA_OK;
+}
+
+extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int hidden, const int32_t* ids,
+                           const float* weights, int topk, const void* w13, const float* w13_scales, const void* w2,
+                           const float* w2_scales, int n_experts, int inter, dsa_bf16* y, int32_t* status,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_experts("dsa_experts", rows, topk, n_experts, hidden, inter);
+    if (rc) return rc;
+    const bool f8 = x_scales || w13_scales || w2_scales;
+    if (rows == 0) return DSA_OK;
+    if (!x || !ids || !weights || !w13 || !w2 || !y) return fail(DSA_ERR_INVALID_ARG, "dsa_experts: NULL tensor");
+    if (f8 && (!x_scales || !w13_scales || !w2_scales))
+        return fail(DSA_ERR_INVALID_ARG, "dsa_experts: FP8 takes the scales of x, w13 and w2, bf16 none");
+    if ((((uintptr_t)x) | ((uintptr_t)w13) | ((uintptr_t)w2) | ((uintptr_t)y) | ((uintptr_t)workspace)) & 15)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_experts: tensors must be 16-byte aligned");
+    if ((((uintptr_t)x_scales) | ((uintptr_t)w13_scales) | ((uintptr_t)w2_scales) | ((uintptr_t)ids) |
+         ((uintptr_t)weights)) & 3)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_experts: misaligned tensor");
+    const int pairs = rows * topk;
+    const Plan p = plan_of(pairs, n_experts, hidden, inter, f8);
+    if (!workspace || workspace_bytes < p.bytes)
+        return fail(DSA_ERR_INVALID_ARG, "dsa_experts: workspace %zu B < %zu B needed", workspace_bytes, p.bytes);
+    const int sms = sm_count();
+    if (sms <= 0) return fail(DSA_ERR_CUDA, "dsa_experts: no CUDA device");
+    cudaStream_t st = (cudaStream_t)stream;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int32_t* counts = reinterpret_cast<int32_t*>(ws + p.counts);
+    int32_t* starts = reinterpret_cast<int32_t*>(ws + p.starts);
+    int32_t* pair_of = reinterpret_cast<int32_t*>(ws + p.pair_of);
+    const int threads = pairs >= 1024 ? 1024 : (pairs + 31) / 32 * 32;
+    cudaError_t e = launch_pdl(dispatch_kernel, dim3((unsigned)n_experts), dim3((unsigned)threads), 0, st, ids, pairs,
+                               n_experts, counts, starts, pair_of, status);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_experts dispatch launch");
+    GemmArgs a = {};
+    a.counts = counts;
+    a.starts = starts;
+    a.pair_of = pair_of;
+    a.n_experts = n_experts;
+    a.topk = topk;
+    a.pairs = pairs;
+    a.hidden = hidden;
+    a.inter = inter;
+    a.h = reinterpret_cast<uint16_t*>(ws + p.h);
+    a.h8 = ws + p.h;
+    a.h_scales = ws + p.h_scales;
+    a.part = reinterpret_cast<float*>(ws + p.part);
+    a.x_scales = x_scales;
+    a.status = status;
+    a.n_m = inter / 64;
+    a.nst = hidden / (f8 ? 128 : 64);
+    a.a_scales = w13_scales;
+    rc = f8 ? gemm_dispatch<true, true>(a, w13, x, rows, sms, st) : gemm_dispatch<false, true>(a, w13, x, rows, sms, st);
+    if (rc) return rc;
+    a.n_m = hidden / 128;
+    a.nst = inter / (f8 ? 128 : 64);
+    a.a_scales = w2_scales;
+    rc = f8 ? gemm_dispatch<true, false>(a, w2, a.h8, pairs, sms, st)
+            : gemm_dispatch<false, false>(a, w2, a.h, pairs, sms, st);
+    if (rc) return rc;
+    const long long n = (long long)rows * (hidden / 4);
+    long long blocks = (n + kSumThreads - 1) / kSumThreads;
+    if (blocks > (long long)sms * 32) blocks = (long long)sms * 32;
+    e = launch_pdl(combine_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, (const float*)a.part, ids, weights,
+                   rows, topk, n_experts, hidden, y);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "dsa_experts combine launch");
+    return DSA_OK;
+}

@@ -168,4 +168,25 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity,
     }
 }
 
+// Bounded wait that polls (the pipeline's hand-offs are short; a suspended wait wakes
+// up late enough to starve the ring). Gives up after about 2^31 cycles (~1 s), or at
+// once when another role already gave up; either way it returns false and the first
+// to give up flags DSA_STATUS_TIMEOUT.
+__device__ __forceinline__ bool poll_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          int32_t* status) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 1023u) == 0u) {
+            if (*abort_flag) return false;
+            if (clock64() - t0 > (1ll << 31)) {
+                *abort_flag = 1;
+                flag_status(status, DSA_STATUS_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
 }  // namespace dsa

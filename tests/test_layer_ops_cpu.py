@@ -132,3 +132,50 @@ def test_binding_checks_shapes():
         api.dsa_dequantize_latent(codes, torch.zeros(4, 2), x[:3])
     with pytest.raises(ValueError, match="logits"):
         api.dsa_router_logits(x, torch.zeros(64, 256, dtype=torch.bfloat16), torch.zeros(4, 63))
+
+
+def test_experts_refusals(lib):
+    import ctypes
+
+    need = ctypes.c_size_t(0)
+    assert lib.dsa_experts_workspace(8, 2, 4, 256, 128, 0, ctypes.byref(need)) == DSA_OK
+    bf16_bytes = need.value
+    assert bf16_bytes >= 16 * (256 * 4 + 128 * 2)
+    assert lib.dsa_experts_workspace(8, 2, 4, 256, 128, 1, ctypes.byref(need)) == DSA_OK
+    assert lib.dsa_experts_workspace(8, 2, 4, 256, 128, 0, None) == DSA_ERR_INVALID_ARG
+
+    def call(x=FAKE, xs=None, rows=8, hidden=256, ids=FAR, w=FAR, topk=2, w13=FAR, s13=None, w2=FAR,
+             s2=None, n=4, inter=128, y=FAR, ws=FAR, nbytes=1 << 30):
+        return lib.dsa_experts(x, xs, rows, hidden, ids, w, topk, w13, s13, w2, s2, n, inter, y, None,
+                               ws, nbytes, None)
+
+    assert call(rows=0) == DSA_OK
+    for bad in (dict(rows=-1), dict(topk=0), dict(n=0), dict(hidden=0), dict(inter=0), dict(x=None),
+                dict(ids=None), dict(w=None), dict(w13=None), dict(w2=None), dict(y=None),
+                dict(ws=None), dict(nbytes=bf16_bytes - 1), dict(x=FAKE + 8), dict(y=FAR + 2),
+                dict(ids=FAR + 2), dict(xs=FAR), dict(s13=FAR, s2=FAR), dict(xs=FAR, s13=FAR, s2=FAR + 1)):
+        assert call(**bad) == DSA_ERR_INVALID_ARG, bad
+        assert "dsa_experts" in _err(lib), bad
+    for bad in (dict(hidden=192), dict(inter=64), dict(inter=200), dict(n=1089),
+                dict(rows=1 << 20, topk=64), dict(n=1088, inter=1 << 20)):
+        assert call(**bad) == DSA_ERR_UNSUPPORTED, bad
+
+
+def test_experts_binding_checks():
+    bf16, u8 = torch.bfloat16, torch.uint8
+    x, y = torch.zeros(4, 256, dtype=bf16), torch.zeros(4, 256, dtype=bf16)
+    ids, w = torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    w13, w2 = torch.zeros(3, 256, 256, dtype=bf16), torch.zeros(3, 256, 128, dtype=bf16)
+    with pytest.raises(ValueError, match="w13"):
+        api.dsa_experts(x, ids, w, w13[:, :128], w2, y)
+    with pytest.raises(ValueError, match="weights"):
+        api.dsa_experts(x, ids, w[:, :1], w13, w2, y)
+    with pytest.raises(ValueError, match="y must"):
+        api.dsa_experts(x, ids, w, w13, w2, y[:2])
+    with pytest.raises(ValueError, match="FP8 takes"):
+        api.dsa_experts(x, ids, w, w13, w2, y, x_scales=torch.zeros(4, 2))
+    with pytest.raises(ValueError, match="scales must"):
+        api.dsa_experts(x, ids, w, w13, w2, y, x_scales=torch.zeros(4, 2),
+                        w13_scales=torch.zeros(3, 256, 2), w2_scales=torch.zeros(3, 256, 2))
+    with pytest.raises(ValueError, match="CUDA"):
+        api.dsa_experts(x, ids, w, w13, w2, y)

@@ -32,14 +32,22 @@ namespace {
 
 constexpr uint32_t kABytes = 128 * 128;  // 128 weight rows x 128 bytes of K
 constexpr int kStgLd = 80;               // floats per pair in the activation's staging
+constexpr int kSfStages = 8;             // K stages whose scales are loaded together
 
-template <bool F8, int N>
+template <bool F8, bool UP, int N>
 struct EL {  // shared and tensor memory of one block
     static constexpr uint32_t STAGE = kABytes + N * 128;
     static constexpr int S = (int)((200u * 1024u) / STAGE);  // ring stages
     static constexpr uint32_t RING = S * STAGE;
     static constexpr uint32_t STG = RING;  // activation staging, 32 pairs x 64 channels
-    static constexpr uint32_t BARS = STG + 32 * kStgLd * 4;
+    // FP8: two chunks of kSfStages stages' scales. A byte per weight row, and per pair a byte
+    // (first product) or a word (second); the pitches keep the transposing stores apart.
+    static constexpr uint32_t SFP = 128 + (UP ? N : 0) + 4;  // bytes
+    static constexpr uint32_t SFW_P = N + 4;                 // words
+    static constexpr uint32_t SF = STG + (UP ? 32 * kStgLd * 4 : 0);
+    static constexpr uint32_t SFBUF = !F8 ? 0 : kSfStages * (SFP + (UP ? 0 : 4 * SFW_P));
+    static constexpr uint32_t BARS = SF + 2 * SFBUF;
+    static_assert(SFBUF % 8 == 0, "alignment");
     static constexpr int NBARS = 3 * S + 5;  // full, empty, scales; 2 + 2 accumulators; drain
     static constexpr uint32_t MISC = BARS + 8 * NBARS;
     static constexpr uint32_t TAB = MISC + 16;  // int[2][n_experts + 1]
@@ -50,6 +58,11 @@ struct EL {  // shared and tensor memory of one block
     static_assert(COLS <= 512, "tensor memory");
     static_assert(STAGE % 1024 == 0, "stage alignment");
 };
+
+// The first product gathers rows of x itself for small tiles. A gathering copy takes about 60
+// cycles for its four rows: 16 of them (64 pairs) would take longer than the weights of their
+// stage do to arrive, so larger tiles read a copy of x in the pairs' order.
+constexpr bool gathers(int n) { return n < 64; }
 
 struct GemmArgs {
     const int32_t* counts;   // [E] pairs of each expert
@@ -132,9 +145,10 @@ __device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, ui
 template <bool F8, bool UP, int N>
 __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs a) {
-    using L = EL<F8, N>;
+    using L = EL<F8, UP, N>;
     constexpr int S = L::S;
-    constexpr int kBox = N < 32 ? N : 32;  // rows of h per copy
+    constexpr bool kGather = UP && gathers(N);
+    constexpr int kBox = N < 32 ? N : 32;  // rows per copy
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
@@ -209,18 +223,16 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
         if constexpr (!UP) pdl_wait();
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const Item it = item_of<N>(a, tab, start, w);
-            int row[N / 4 <= 32 ? 4 : 8];
-            if constexpr (UP) {
+            int row[4];
+            if constexpr (kGather) {
 #pragma unroll
-                for (int q = 0; q < (N / 4 <= 32 ? 1 : 2); ++q)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int p = (lane + 32 * q) * 4 + j;
-                        row[4 * q + j] = a.pair_of[it.pos + (p < it.n ? p : 0)] / a.topk;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int p = lane * 4 + j;
+                    row[j] = a.pair_of[it.pos + (p < it.n ? p : 0)] / a.topk;
+                }
             }
             const int quads = (it.n + 3) >> 2, boxes = (it.n + kBox - 1) / kBox;
-            const uint32_t bytes = kABytes + (UP ? quads * 512 : boxes * kBox * 128);
+            const uint32_t bytes = kABytes + (kGather ? quads * 512 : boxes * kBox * 128);
             for (int st = 0; st < a.nst; ++st, ++i) {
                 const int s = i % S;
                 int go = 1;
@@ -235,17 +247,17 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
                 }
                 const uint32_t dst = smem_u32(smem + s * L::STAGE);
                 const int k = st * (F8 ? 128 : 64);
-                if constexpr (UP) {
-                    if (lane == 0) tma_load_5d(dst, &tmA, k, 0, 0, it.m * 4, it.e, full + s);
-#pragma unroll
-                    for (int q = 0; q < (N / 4 <= 32 ? 1 : 2); ++q)
-                        if (lane + 32 * q < quads)
-                            tma_gather4(dst + kABytes + (lane + 32 * q) * 512, &tmB, k, row[4 * q], row[4 * q + 1],
-                                        row[4 * q + 2], row[4 * q + 3], full + s);
-                } else {
-                    if (lane == 0) tma_load_2d(dst, &tmA, k, it.e * a.hidden + it.m * 128, full + s);
-                    if (lane < boxes)
-                        tma_load_2d(dst + kABytes + lane * kBox * 128, &tmB, k, it.pos + lane * kBox, full + s);
+                if (lane == 0) {
+                    if constexpr (UP)
+                        tma_load_5d(dst, &tmA, k, 0, 0, it.m * 4, it.e, full + s);
+                    else
+                        tma_load_2d(dst, &tmA, k, it.e * a.hidden + it.m * 128, full + s);
+                }
+                if constexpr (kGather) {
+                    if (lane < quads)
+                        tma_gather4(dst + kABytes + lane * 512, &tmB, k, row[0], row[1], row[2], row[3], full + s);
+                } else if (lane < boxes) {
+                    tma_load_2d(dst + kABytes + lane * kBox * 128, &tmB, k, it.pos + lane * kBox, full + s);
                 }
             }
         }
@@ -401,65 +413,92 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
         }
     } else if (F8 && warp >= 8) {
         // ---------------- scales ----------------
-        // Each warp writes all scales of a stage to its own lane quarter (the block-scaled
-        // MMA reads a copy in each): word j of lane l is row 32 j + l. Four stages' scales
-        // are requested ahead.
+        // The rows' scales along K are contiguous: eight threads take eight stages of one
+        // row, a chunk ahead of its use, and store them transposed in shared memory. Each
+        // warp then writes all scales of a stage to its own lane quarter (the block-scaled
+        // MMA reads a copy in each): word j of lane l is row 32 j + l.
         const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * N;
-        constexpr int NB = N <= 32 ? 1 : N / 32;
-        int i = 0;
+        const int t = threadIdx.x - 256, sub = t >> 3, sst = t & 7;
+        constexpr int NB = N / 16;
+        int i = 0, chunk = 0;
         bool ok = true;
         if constexpr (!UP) pdl_wait();
         for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
             const Item it = item_of<N>(a, tab, start, w);
-            const float* pa[4];
-            const float* pb[NB];
             const long long ks = a.nst;  // scales per row: one per stage
+            // row sub + 16 i of the tile
+            const float* pa = a.a_scales + (UP ? (long long)it.e * 2 * a.inter + it.m * 64 + sub
+                                               : (long long)it.e * a.hidden + it.m * 128 + sub) * ks + sst;
+            const long long da = UP ? (long long)a.inter * ks : 16 * ks;
+            uint32_t pb[NB];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const long long r = UP ? (long long)it.e * 2 * a.inter + (lane >> 4) * a.inter + it.m * 64 + 16 * j + (lane & 15)
-                                       : (long long)it.e * a.hidden + it.m * 128 + 32 * j + lane;
-                pa[j] = a.a_scales + r * ks;
+            for (int k = 0; k < NB; ++k) {
+                const int p = it.pos + (sub + 16 * k < it.n ? sub + 16 * k : 0);
+                pb[k] = (uint32_t)(UP ? a.pair_of[p] / a.topk : p);
             }
+            const float* bsrc = UP ? a.x_scales : reinterpret_cast<const float*>(a.h_scales);
+            uint32_t va[8], vb[NB];
+            auto load = [&](int st0) {
+                const bool in = st0 + sst < a.nst;
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int p = it.pos + (32 * j + lane < it.n ? 32 * j + lane : 0);
-                pb[j] = UP ? a.x_scales + (a.pair_of[p] / a.topk) * ks
-                           : reinterpret_cast<const float*>(a.h_scales) + p * ks;  // four exponents a word
-            }
-            for (int st0 = 0; st0 < a.nst && ok; st0 += 4) {
-                uint32_t va[4][4], vb[4][L::SFB];
+                for (int k = 0; k < 8; ++k) {
+                    const float* src = UP ? pa + (k & 1) * da + (k >> 1) * 16 * ks : pa + k * da;
+                    va[k] = in ? __float_as_uint(__ldg(src + st0)) : 0u;
+                }
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (st0 + q < a.nst) {
+                for (int k = 0; k < NB; ++k) vb[k] = in ? __float_as_uint(bsrc[pb[k] * ks + st0 + sst]) : 0u;
+            };
+            load(0);
+            for (int st0 = 0; st0 < a.nst && ok; st0 += kSfStages, ++chunk) {
+                uint8_t* buf = smem + L::SF + (chunk & 1) * L::SFBUF;
+                uint32_t* words = reinterpret_cast<uint32_t*>(buf + kSfStages * L::SFP);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            va[q][j] = ((__float_as_uint(__ldg(pa[j] + st0 + q)) >> 23) & 255u) * 0x01010101u;
+                for (int k = 0; k < 8; ++k) buf[sst * L::SFP + sub + 16 * k] = (uint8_t)(va[k] >> 23);
 #pragma unroll
-                        for (int j = 0; j < L::SFB; ++j) {
-                            const uint32_t b = j < NB ? __float_as_uint(pb[j < NB ? j : 0][st0 + q]) : 0u;
-                            vb[q][j] = UP ? ((b >> 23) & 255u) * 0x01010101u : b;
-                        }
+                for (int k = 0; k < NB; ++k) {
+                    if constexpr (UP)
+                        buf[sst * L::SFP + 128 + sub + 16 * k] = (uint8_t)(vb[k] >> 23);
+                    else
+                        words[sst * L::SFW_P + sub + 16 * k] = vb[k];
+                }
+                // The chunk is in place; and every warp is done with the one before it, so
+                // the next turn may overwrite that.
+                asm volatile("bar.sync 2, 128;\n" ::: "memory");
+                if (st0 + kSfStages < a.nst) load(st0 + kSfStages);
+                const int ns = min(kSfStages, a.nst - st0);
+                for (int q = 0; q < ns; ++q, ++i) {
+                    uint32_t fa[4], fb[L::SFB];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) fa[j] = buf[q * L::SFP + 32 * j + lane] * 0x01010101u;
+#pragma unroll
+                    for (int j = 0; j < L::SFB; ++j) {
+                        const int r = 32 * j + lane;
+                        fb[j] = 0u;
+                        if (r < N)
+                            fb[j] = UP ? buf[q * L::SFP + 128 + r] * 0x01010101u : words[q * L::SFW_P + r];
                     }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (st0 + q >= a.nst || !ok) break;
                     const int s = i % S;
                     int go = 1;
                     if (lane == 0)
                         go = poll_wait(empty + s, (uint32_t)(((i / S) & 1) ^ 1), abort_flag, a.status);
                     go = __shfl_sync(0xffffffffu, go, 0);
-                    if (!go) {
-                        ok = false;
-                        break;
-                    }
+                    if (!go) ok = false;  // (the other warps keep the barrier above: they are told below)
+                    if (!ok) break;
                     tc_fence_after();
-                    tc_st_cols<4>(quarter + s * L::SFW, va[q]);
-                    tc_st_cols<L::SFB>(quarter + s * L::SFW + 4, vb[q]);
+                    tc_st_cols<4>(quarter + s * L::SFW, fa);
+                    tc_st_cols<L::SFB>(quarter + s * L::SFW + 4, fb);
                     tc_wait_st();
                     tc_fence_before();
                     if (lane == 0) mbar_arrive(sfull + s);
-                    ++i;
                 }
+                int all;  // the four warps share the barrier: they leave together
+                asm volatile(
+                    "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\n"
+                    "barrier.cta.red.and.pred q, 2, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+                    : "=r"(all)
+                    : "r"((int)ok)
+                    : "memory");
+                ok = all != 0;
             }
         }
     }
@@ -521,6 +560,27 @@ __global__ void __launch_bounds__(1024) dispatch_kernel(const int32_t* __restric
     }
 }
 
+// The rows of x in the pairs' order, `vecs` 16-byte pieces each; a warp takes a row.
+__global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ counts,
+                                                      const int32_t* __restrict__ starts, int n_experts,
+                                                      const int32_t* __restrict__ pair_of, int topk, int vecs,
+                                                      uint4* __restrict__ out) {
+    pdl_wait();
+    const int pos = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (pos >= starts[n_experts - 1] + counts[n_experts - 1]) return;
+    const uint4* src = x + (long long)(pair_of[pos] / topk) * vecs;
+    uint4* dst = out + (long long)pos * vecs;
+    for (int v0 = lane; v0 < vecs; v0 += 128) {
+        uint4 q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (v0 + 32 * j < vecs) q[j] = __ldg(src + v0 + 32 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (v0 + 32 * j < vecs) dst[v0 + 32 * j] = q[j];
+    }
+}
+
 // y[r] = sum over the row's experts, in their order in ids, of weight times partial.
 constexpr int kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads) combine_kernel(const float* __restrict__ part,
@@ -551,8 +611,15 @@ __global__ void __launch_bounds__(kSumThreads) combine_kernel(const float* __res
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Pairs per tile: what an expert gets on average. Fewer leave more of the ring to the weights
+// in flight; an expert with more pairs takes several tiles.
+int tile_of(long long pairs, int n_experts, bool f8) {
+    const long long mean = (pairs + n_experts - 1) / n_experts;
+    return mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : f8 ? 192 : 256;
+}
+
 struct Plan {
-    size_t counts, starts, pair_of, h, h_scales, part, bytes;
+    size_t counts, starts, pair_of, x, h, h_scales, part, bytes;
 };
 Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     Plan p;
@@ -563,6 +630,8 @@ Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     at += al256((size_t)n_experts * 4);
     p.pair_of = at;
     at += al256((size_t)pairs * 4);
+    p.x = at;
+    at += gathers(tile_of(pairs, n_experts, f8)) ? 0 : al256((size_t)pairs * hidden * (f8 ? 1 : 2));
     p.h = at;
     at += al256((size_t)pairs * inter * (f8 ? 1 : 2));
     p.h_scales = at;
@@ -589,7 +658,7 @@ int check_experts(const char* name, int rows, int topk, int n_experts, int hidde
 
 template <bool F8, bool UP, int N>
 int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_rows, int sms, cudaStream_t st) {
-    using L = EL<F8, N>;
+    using L = EL<F8, UP, N>;
     static_assert(L::TAB + 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1) + 1024 <= 227 * 1024, "shared memory");
     const int dyn = (int)(L::TAB + 8 * (a.n_experts + 1) + 1024);
     int rc = set_max_smem((const void*)experts_kernel<F8, UP, N>, 227 * 1024);
@@ -604,7 +673,8 @@ int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_row
         const uint32_t box[5] = {bk, 16, 2, 4, 1};
         rc = make_tmap(&tmA, dt, weights, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc) return rc;
-        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, 1, CU_TENSOR_MAP_SWIZZLE_128B);
+        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, gathers(N) ? 1 : 32,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
         rc = make_tmap_2d(&tmA, dt, weights, I, E * H, I * es, bk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc) return rc;
@@ -620,14 +690,13 @@ int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_row
 
 template <bool F8, bool UP>
 int gemm_dispatch(const GemmArgs& a, const void* weights, const void* b, int b_rows, int sms, cudaStream_t st) {
-    // Pairs per tile: what an expert gets on average. Fewer leave more of the ring to the
-    // weights in flight; an expert with more pairs takes several tiles.
-    const long long mean = (a.pairs + a.n_experts - 1) / a.n_experts;
-    if (mean <= 8) return gemm_launch<F8, UP, 16>(a, weights, b, b_rows, sms, st);
-    if (mean <= 24) return gemm_launch<F8, UP, 32>(a, weights, b, b_rows, sms, st);
-    if (mean <= 48) return gemm_launch<F8, UP, 64>(a, weights, b, b_rows, sms, st);
-    if (mean <= 96) return gemm_launch<F8, UP, 128>(a, weights, b, b_rows, sms, st);
-    return gemm_launch<F8, UP, F8 ? 192 : 256>(a, weights, b, b_rows, sms, st);
+    switch (tile_of(a.pairs, a.n_experts, F8)) {
+        case 16: return gemm_launch<F8, UP, 16>(a, weights, b, b_rows, sms, st);
+        case 32: return gemm_launch<F8, UP, 32>(a, weights, b, b_rows, sms, st);
+        case 64: return gemm_launch<F8, UP, 64>(a, weights, b, b_rows, sms, st);
+        case 128: return gemm_launch<F8, UP, 128>(a, weights, b, b_rows, sms, st);
+        default: return gemm_launch<F8, UP, F8 ? 192 : 256>(a, weights, b, b_rows, sms, st);
+    }
 }
 
 }  // namespace
@@ -694,7 +763,18 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     a.n_m = inter / 64;
     a.nst = hidden / (f8 ? 128 : 64);
     a.a_scales = w13_scales;
-    rc = f8 ? gemm_dispatch<true, true>(a, w13, x, rows, sms, st) : gemm_dispatch<false, true>(a, w13, x, rows, sms, st);
+    int x_rows = rows;
+    if (!gathers(tile_of(pairs, n_experts, f8))) {
+        e = launch_pdl(permute_kernel, dim3((unsigned)((pairs + 7) / 8)), dim3(256), 0, st, (const uint4*)x,
+                       (const int32_t*)counts, (const int32_t*)starts, n_experts, (const int32_t*)pair_of, topk,
+                       hidden / (f8 ? 16 : 8), (uint4*)(ws + p.x));
+        if (e == cudaSuccess) e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e, "dsa_experts permute launch");
+        x = ws + p.x;
+        x_rows = pairs;
+    }
+    rc = f8 ? gemm_dispatch<true, true>(a, w13, x, x_rows, sms, st)
+            : gemm_dispatch<false, true>(a, w13, x, x_rows, sms, st);
     if (rc) return rc;
     a.n_m = hidden / 128;
     a.nst = inter / (f8 ? 128 : 64);

@@ -21,9 +21,15 @@
 // contiguous in the pairs' order.
 //
 // Roles: warp 0 copies, warp 1 issues the MMAs, warps 4-7 take the accumulators (two, so
-// that the tensor cores run on meanwhile), with FP8 warps 8-11 put the scales into tensor
-// memory: one byte (the exponent) per row and 32 K values, for the block-scaled MMA. Waits
+// that the tensor cores run on meanwhile), with FP8 warps 8-11 lay out the scales: one byte (the
+// exponent) per row and 32 K values for the block-scaled MMA, which warp 1 copies to tensor
+// memory in order with its MMAs. (Stored there by the warps themselves, with tcgen05.st, the
+// scales of a stage took as long as its MMAs: a prefill's products were twice as slow.) Waits
 // are bounded; one that gives up sets DSA_STATUS_TIMEOUT and every role leaves its loop.
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "fp8.cuh"
 #include "tc.cuh"
 
@@ -32,28 +38,34 @@ namespace {
 
 constexpr uint32_t kABytes = 128 * 128;  // 128 weight rows x 128 bytes of K
 constexpr int kStgLd = 80;               // floats per pair in the activation's staging
-constexpr int kSfStages = 8;             // K stages whose scales are loaded together
+constexpr int kSfStages = 8;             // K stages whose scales travel together: a chunk
+constexpr uint32_t kSfBlock = 512;       // scale words of 128 rows, [32][4]: word [l][j] is row 32 j + l
+
+// A pair of blocks shares its MMAs where a tile is that large: each holds its own 128 weight
+// rows and half of the pairs' rows, and gets its weight rows' products with all pairs. Shared
+// memory then carries per multiply two thirds of what it does for one block's 128 x 256 tile,
+// which is what bounds that one.
+constexpr bool paired(int n) { return n > 128; }
 
 template <bool F8, bool UP, int N>
 struct EL {  // shared and tensor memory of one block
-    static constexpr uint32_t STAGE = kABytes + N * 128;
+    static constexpr int BR = paired(N) ? (N / 2 + 31) / 32 * 32 : N;  // rows of x or h of a stage
+    static constexpr uint32_t STAGE = kABytes + BR * 128;
     static constexpr int S = (int)((200u * 1024u) / STAGE);  // ring stages
     static constexpr uint32_t RING = S * STAGE;
     static constexpr uint32_t STG = RING;  // activation staging, 32 pairs x 64 channels
-    // FP8: two chunks of kSfStages stages' scales. A byte per weight row, and per pair a byte
-    // (first product) or a word (second); the pitches keep the transposing stores apart.
-    static constexpr uint32_t SFP = 128 + (UP ? N : 0) + 4;  // bytes
-    static constexpr uint32_t SFW_P = N + 4;                 // words
-    static constexpr uint32_t SF = STG + (UP ? 32 * kStgLd * 4 : 0);
-    static constexpr uint32_t SFBUF = !F8 ? 0 : kSfStages * (SFP + (UP ? 0 : 4 * SFW_P));
+    // FP8: two chunks of scales. A word holds four bytes along K: those of four stages where a
+    // scale spans one (weights, x), those of one stage for h.
+    static constexpr int SFN = (N + 127) / 128;       // blocks of N pairs
+    static constexpr int SFC = SFN * (UP ? 1 : 4);    // of four stages
+    static constexpr uint32_t SF = (STG + (UP ? 32 * kStgLd * 4 : 0) + 127) & ~127u;
+    static constexpr uint32_t SF_B = kSfStages / 4 * kSfBlock;  // the pairs' part of a chunk
+    static constexpr uint32_t SFBUF = !F8 ? 0 : SF_B + (UP ? kSfStages / 4 : kSfStages) * SFN * kSfBlock;
     static constexpr uint32_t BARS = SF + 2 * SFBUF;
-    static_assert(SFBUF % 8 == 0, "alignment");
-    static constexpr int NBARS = 3 * S + 5;  // full, empty, scales; 2 + 2 accumulators; drain
+    static constexpr int NBARS = 2 * S + 9;  // full, empty; 2 + 2 scales, accumulators; drain
     static constexpr uint32_t MISC = BARS + 8 * NBARS;
     static constexpr uint32_t TAB = MISC + 16;  // int[2][n_experts + 1]
-    static constexpr int SFB = N <= 32 ? 1 : N <= 64 ? 2 : N <= 128 ? 4 : 8;  // columns of N scales
-    static constexpr int SFW = F8 ? 4 + (SFB < 4 ? 4 : SFB) : 0;              // of a stage's scales
-    static constexpr int COLS = 2 * N + S * SFW;
+    static constexpr int COLS = 2 * N + (F8 ? 4 + 4 * SFC : 0);
     static constexpr uint32_t TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(COLS <= 512, "tensor memory");
     static_assert(STAGE % 1024 == 0, "stage alignment");
@@ -110,35 +122,65 @@ __device__ __forceinline__ Item item_of(const GemmArgs& a, const int* tab, const
 
 __device__ __forceinline__ void bar_sync_epilogue() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
 
-template <int W>
-__device__ __forceinline__ void tc_st_cols(uint32_t t, const uint32_t* v) {
-    if constexpr (W == 1)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(t), "r"(v[0]) : "memory");
-    else if constexpr (W == 2)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};\n" ::"r"(t), "r"(v[0]), "r"(v[1]) : "memory");
-    else if constexpr (W == 4)
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(t), "r"(v[0]), "r"(v[1]),
-                     "r"(v[2]), "r"(v[3])
-                     : "memory");
+// One block of scales (no swizzle, 8-row groups of 16-byte rows 128 bytes apart) from shared
+// memory to four columns of tensor memory, a copy in each lane quarter. In order with the
+// MMAs that the same thread issues before and after it. (Here and below: by one elected lane
+// of a converged warp, see warp_mma.)
+__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+template <bool PAIR>
+__device__ __forceinline__ void warp_cp_sf(uint32_t taddr, uint32_t saddr) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(taddr), "l"(sf_desc(saddr)) : "memory");
     else
-        asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(t), "r"(v[0]),
-                     "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                     : "memory");
+        asm volatile(
+            "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
+            "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(taddr), "l"(sf_desc(saddr)) : "memory");
 }
 
 // Instruction descriptor, kind::mxf8f6f4: E4M3 x E4M3 -> f32, both K-major, UE8M0 scales,
-// byte `id` of each scale word.
-__device__ __forceinline__ uint32_t idesc_mxf8(int N, int id) {
-    return ((uint32_t)id << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | (1u << 27) | ((uint32_t)id << 29);
+// bytes ida and idb of each row's scale word.
+__device__ __forceinline__ uint32_t idesc_mxf8(int M, int N, int ida, int idb) {
+    return ((uint32_t)idb << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
+           ((uint32_t)ida << 29);
 }
-__device__ __forceinline__ void tc_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
-                                          uint32_t sb, uint32_t accumulate) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(
-            d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
-        : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void warp_mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
+                                            uint32_t sb, uint32_t accumulate) {
+    if constexpr (PAIR)
+        asm volatile(
+            "{\n.reg .pred p, e;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %6, 0;\n"
+            "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::
+                "r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p, e;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %6, 0;\n"
+            "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::
+                "r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+            : "memory");
+}
+// A converged warp waits for a phase, for about a second at most; false after a timeout (here or
+// in another role).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 1;; ++i) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 255u) == 0u) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+            if (__any_sync(0xffffffffu, global_ns() - t0 > 1000000000ull)) {
+                *abort_flag = 1;
+                if ((threadIdx.x & 31) == 0) flag_status(status, DSA_STATUS_TIMEOUT);
+                return false;
+            }
+        }
+    }
 }
 
 // UP: the first product (rows of x gathered, activation); else the second.
@@ -147,14 +189,16 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs a) {
     using L = EL<F8, UP, N>;
     constexpr int S = L::S;
-    constexpr bool kGather = UP && gathers(N);
+    constexpr bool kGather = UP && gathers(N), kPair = paired(N);
     constexpr int kBox = N < 32 ? N : 32;  // rows per copy
+    constexpr int kRound = kPair ? 32 : 16;  // pairs of an MMA: multiples of it
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::BARS);
     uint64_t* empty = full + S;
-    uint64_t* sfull = empty + S;
-    uint64_t* acc_full = sfull + S;
+    uint64_t* sf_full = empty + S;
+    uint64_t* sf_empty = sf_full + 2;
+    uint64_t* acc_full = sf_empty + 2;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::MISC);
@@ -163,21 +207,32 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
     int* start = tab + a.n_experts + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // The leader (the even block of a pair, or the only one) issues the MMAs; full, scales and
+    // accumulator-empty barriers are its own, the others each block's.
+    const uint32_t rank = kPair ? cluster_rank() : 0;
+    const int w0 = kPair ? blockIdx.x >> 1 : blockIdx.x, wstep = kPair ? gridDim.x >> 1 : gridDim.x;
+
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
-            mbar_init(sfull + s, 4);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(sf_full + i, kPair ? 8 : 4);
+            mbar_init(sf_empty + i, 1);
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4);
+            mbar_init(acc_empty + i, kPair ? 8 : 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 1) tc_alloc(tmem_slot, L::TMEM);
+    if (warp == 1) {
+        if constexpr (kPair)
+            tc_alloc2(tmem_slot, L::TMEM);
+        else
+            tc_alloc(tmem_slot, L::TMEM);
+    }
     // The tables of the dispatch. The first product waits for it; the second starts early
     // (its predecessor lets it once it has itself seen the dispatch finished) and waits
     // below, before it touches h.
@@ -212,16 +267,38 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_barrier();  // the peer's barriers exist
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    auto arrive_leader = [&](uint64_t* bar) {
+        if constexpr (kPair)
+            mbar_arrive_cluster(cluster_addr(bar, 0));
+        else
+            mbar_arrive(bar);
+    };
     const int items = tab[a.n_experts] * a.n_m;
 
     if (warp == 0) {
         // ---------------- copies ----------------
         int i = 0;  // stages issued
         bool ok = true;
-        if constexpr (!UP) pdl_wait();
-        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+        auto load_a = [&](const Item& it, int st, int s) {  // (one lane)
+            const uint32_t dst = smem_u32(smem + s * L::STAGE);
+            const int k = st * (F8 ? 128 : 64), mt = kPair ? 2 * it.m + (int)rank : it.m;
+            if constexpr (kPair) {
+                const uint32_t bar = cluster_addr(full + s, 0);
+                if constexpr (UP)
+                    tma_load_5d_pair(dst, &tmA, k, 0, 0, mt * 4, it.e, bar);
+                else
+                    tma_load_2d_pair(dst, &tmA, k, it.e * a.hidden + mt * 128, bar);
+            } else {
+                if constexpr (UP)
+                    tma_load_5d(dst, &tmA, k, 0, 0, mt * 4, it.e, full + s);
+                else
+                    tma_load_2d(dst, &tmA, k, it.e * a.hidden + mt * 128, full + s);
+            }
+        };
+        for (int w = w0; w < items && ok; w += wstep) {
             const Item it = item_of<N>(a, tab, start, w);
             int row[4];
             if constexpr (kGather) {
@@ -231,76 +308,124 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
                     row[j] = a.pair_of[it.pos + (p < it.n ? p : 0)] / a.topk;
                 }
             }
-            const int quads = (it.n + 3) >> 2, boxes = (it.n + kBox - 1) / kBox;
-            const uint32_t bytes = kABytes + (kGather ? quads * 512 : boxes * kBox * 128);
-            for (int st = 0; st < a.nst; ++st, ++i) {
+            const int half = (it.n + 31) / 32 * 16;  // of a pair of blocks: columns from each
+            const int quads = (it.n + 3) >> 2, boxes = ((kPair ? half : it.n) + kBox - 1) / kBox;
+            const int pos = it.pos + (kPair ? (int)rank * half : 0);
+            const uint32_t bytes = (kABytes + (kGather ? quads * 512 : boxes * kBox * 128)) * (kPair ? 2 : 1);
+            auto load_b = [&](int st, int s) {  // (all lanes)
+                const uint32_t dst = smem_u32(smem + s * L::STAGE) + kABytes;
+                const int k = st * (F8 ? 128 : 64);
+                if constexpr (kGather) {
+                    if (lane < quads)
+                        tma_gather4(dst + lane * 512, &tmB, k, row[0], row[1], row[2], row[3], full + s);
+                } else if (lane < boxes) {
+                    if constexpr (kPair)
+                        tma_load_2d_pair(dst + lane * kBox * 128, &tmB, k, pos + lane * kBox, cluster_addr(full + s, 0));
+                    else
+                        tma_load_2d(dst + lane * kBox * 128, &tmB, k, pos + lane * kBox, full + s);
+                }
+            };
+            int st = 0;
+            if constexpr (!UP) {
+                if (w == w0) {
+                    // the first ring's weights do not wait for h
+                    const int pre = a.nst < S ? a.nst : S;
+                    if (lane == 0)
+                        for (int s = 0; s < pre; ++s) {
+                            if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+                            load_a(it, s, s);
+                        }
+                    pdl_wait();
+                    __syncwarp();
+                    for (; st < pre; ++st, ++i) load_b(st, st);
+                }
+            }
+            for (; st < a.nst; ++st, ++i) {
                 const int s = i % S;
                 int go = 1;
                 if (lane == 0) {
-                    go = poll_wait(empty + s, (uint32_t)(((i / S) & 1) ^ 1), abort_flag, a.status);
-                    if (go) mbar_arrive_expect_tx(full + s, bytes);
+                    go = wait_or_abort(empty + s, (uint32_t)(((i / S) & 1) ^ 1), abort_flag, a.status);
+                    if (go) {
+                        if (rank == 0) mbar_arrive_expect_tx(full + s, bytes);
+                        load_a(it, st, s);
+                    }
                 }
                 go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) {
                     ok = false;
                     break;
                 }
-                const uint32_t dst = smem_u32(smem + s * L::STAGE);
-                const int k = st * (F8 ? 128 : 64);
-                if (lane == 0) {
-                    if constexpr (UP)
-                        tma_load_5d(dst, &tmA, k, 0, 0, it.m * 4, it.e, full + s);
-                    else
-                        tma_load_2d(dst, &tmA, k, it.e * a.hidden + it.m * 128, full + s);
-                }
-                if constexpr (kGather) {
-                    if (lane < quads)
-                        tma_gather4(dst + kABytes + lane * 512, &tmB, k, row[0], row[1], row[2], row[3], full + s);
-                } else if (lane < boxes) {
-                    tma_load_2d(dst + kABytes + lane * kBox * 128, &tmB, k, it.pos + lane * kBox, full + s);
-                }
+                load_b(st, s);
             }
         }
+        if constexpr (!UP)
+            if (w0 >= items) pdl_wait();
         // the copies issued have landed before the block may leave its memory
-        if (lane == 0)
+        // (a pair's: the leader sees both blocks' copies, and neither leaves before the other)
+        if (lane == 0 && rank == 0)
             for (int j = i > S ? i - S : 0; j < i; ++j)
                 if (!mbar_wait(full + (j % S), (uint32_t)((j / S) & 1))) break;
         __syncwarp();
     } else if (warp == 1) {
-        // ---------------- MMA issue ----------------
-        if (lane == 0) {
-            int i = 0, t = 0;
+        // ---------------- MMA issue (the whole warp) ----------------
+        if (rank == 0) {
+            int i = 0, t = 0, chunk = 0;
             bool ok = true;
-            for (int w = blockIdx.x; w < items && ok; w += gridDim.x, ++t) {
+            auto commit = [&](uint64_t* bar) {
+                if constexpr (kPair)
+                    warp_commit2(bar);
+                else
+                    warp_commit(bar);
+            };
+            constexpr int M = kPair ? 256 : 128;
+            const uint32_t sf = tmem + 2 * N;
+            for (int w = w0; w < items && ok; w += wstep, ++t) {
                 const Item it = item_of<N>(a, tab, start, w);
-                const int n = (it.n + 15) & ~15;
+                const int n = (it.n + kRound - 1) / kRound * kRound;
                 const uint32_t d = tmem + (t & 1) * N;
-                if (!poll_wait(acc_empty + (t & 1), (uint32_t)(((t >> 1) & 1) ^ 1), abort_flag, a.status)) break;
-                for (int st = 0; st < a.nst; ++st, ++i) {
+                ok = warp_wait(acc_empty + (t & 1), (uint32_t)(((t >> 1) & 1) ^ 1), abort_flag, a.status);
+                for (int st = 0; st < a.nst && ok; ++st, ++i) {
                     const int s = i % S;
-                    const uint32_t par = (uint32_t)((i / S) & 1);
-                    ok = poll_wait(full + s, par, abort_flag, a.status);
-                    if constexpr (F8) ok = ok && poll_wait(sfull + s, par, abort_flag, a.status);
+                    if (F8 && (st & (kSfStages - 1)) == 0) {
+                        ok = warp_wait(sf_full + (chunk & 1), (uint32_t)((chunk >> 1) & 1), abort_flag, a.status);
+                        if (!ok) break;
+                    }
+                    ok = warp_wait(full + s, (uint32_t)((i / S) & 1), abort_flag, a.status);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + s * L::STAGE), sb = sa + kABytes;
+                    if (F8 && (st & 3) == 0) {  // the next four stages' scales
+                        const int g = (st >> 2) & (kSfStages / 4 - 1);
+                        const uint32_t src = smem_u32(smem + L::SF + (chunk & 1) * L::SFBUF);
+                        warp_cp_sf<kPair>(sf, src + g * kSfBlock);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
+                        for (int b = 0; b < L::SFC; ++b)
+                            warp_cp_sf<kPair>(sf + 4 + 4 * b, src + L::SF_B + (g * L::SFC + b) * kSfBlock);
+                    }
+                    const uint32_t sa = smem_u32(smem + s * L::STAGE), sb = sa + kABytes;
+                    const uint64_t da = sw128_desc(sa), db = sw128_desc(sb);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {  // 32 bytes of K each
+                        const uint32_t more = (st | kk) != 0;
                         if constexpr (F8) {
-                            const uint32_t sf = tmem + 2 * N + s * L::SFW;
-                            tc_mma_mx(d, sw128_desc(sa + 32 * kk), sw128_desc(sb + 32 * kk), idesc_mxf8(n, kk), sf,
-                                      sf + 4, (st | kk) != 0);
+                            // the byte of the scale words: the stage's, for h the K step's
+                            warp_mma_mx<kPair>(d, da + 2 * kk, db + 2 * kk, idesc_mxf8(M, n, st & 3, UP ? st & 3 : kk), sf,
+                                               sf + 4 + (UP ? 0 : (st & 3) * 4 * L::SFN), more);
+                        } else if constexpr (kPair) {
+                            warp_mma2(d, da + 2 * kk, db + 2 * kk, idesc_bf16(M, n), more);
                         } else {
-                            tc_mma(d, sw128_desc(sa + 32 * kk), sw128_desc(sb + 32 * kk), idesc_bf16(128, n),
-                                   (st | kk) != 0);
+                            warp_mma(d, da + 2 * kk, db + 2 * kk, idesc_bf16(M, n), more);
                         }
                     }
-                    tc_commit(empty + s);
+                    commit(empty + s);
+                    if (F8 && ((st & (kSfStages - 1)) == kSfStages - 1 || st + 1 == a.nst)) {
+                        commit(sf_empty + (chunk & 1));
+                        ++chunk;
+                    }
                 }
-                if (ok) tc_commit(acc_full + (t & 1));
+                if (ok) commit(acc_full + (t & 1));
             }
-            tc_commit(drain);  // every MMA issued: all of them, or those before an abort
-            if (!mbar_wait(drain, 0)) flag_status(a.status, DSA_STATUS_TIMEOUT);
+            commit(drain);  // every MMA issued: all of them, or those before an abort
+            if (lane == 0 && !mbar_wait(drain, 0)) flag_status(a.status, DSA_STATUS_TIMEOUT);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 8) {
@@ -308,10 +433,11 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
         const int ew = warp - 4, et = threadIdx.x - 128;
         float* stg = reinterpret_cast<float*>(smem + L::STG);
         int t = 0;
-        for (int w = blockIdx.x; w < items; w += gridDim.x, ++t) {
+        for (int w = w0; w < items; w += wstep, ++t) {
             const Item it = item_of<N>(a, tab, start, w);
+            const int mt = kPair ? 2 * it.m + (int)rank : it.m;
             int got = 1;
-            if (lane == 0) got = poll_wait(acc_full + (t & 1), (uint32_t)((t >> 1) & 1), abort_flag, a.status);
+            if (lane == 0) got = wait_or_abort(acc_full + (t & 1), (uint32_t)((t >> 1) & 1), abort_flag, a.status);
             got = __shfl_sync(0xffffffffu, got, 0);
             if constexpr (UP) {  // the four warps share barriers below: they leave together
                 int all;
@@ -326,7 +452,7 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
             if (!got) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * ew) << 16) + (t & 1) * N;
-            const int n16 = (it.n + 15) & ~15;
+            const int n16 = (it.n + kRound - 1) / kRound * kRound;
             for (int c0 = 0; c0 < it.n; c0 += 32) {
                 uint32_t v[32];
                 if (N >= 32 && n16 - c0 > 16) {
@@ -347,7 +473,7 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
                 }
                 if (c0 + 32 >= it.n) {  // the last columns are in registers
                     tc_fence_before();
-                    if (lane == 0) mbar_arrive(acc_empty + (t & 1));
+                    if (lane == 0) arrive_leader(acc_empty + (t & 1));
                 }
                 if constexpr (UP) {
                     bar_sync_epilogue();  // the staging is free
@@ -373,7 +499,7 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
                         f[4 * j + 3] = q.w;
                     }
                     const bool live = c0 + p < it.n;
-                    const long long at = (long long)(it.pos + c0 + p) * a.inter + it.m * 64 + seg * 16;
+                    const long long at = (long long)(it.pos + c0 + p) * a.inter + mt * 64 + seg * 16;
                     if constexpr (F8) {
                         float m = 0.f;
 #pragma unroll
@@ -402,33 +528,34 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
                     }
                 } else {
                     const int mine = a.pair_of[it.pos + (c0 + lane < it.n ? c0 + lane : 0)];
-                    float* to = a.part + it.m * 128 + 32 * ew + lane;
+                    float* to = a.part + mt * 128 + 32 * ew + lane;
+                    const bool inside = !kPair || mt * 128 < a.hidden;  // an odd number of row tiles: one too many
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
                         const int pair = __shfl_sync(0xffffffffu, mine, c);
-                        if (c0 + c < it.n) to[(long long)pair * a.hidden] = __uint_as_float(v[c]);
+                        if (c0 + c < it.n && inside) to[(long long)pair * a.hidden] = __uint_as_float(v[c]);
                     }
                 }
             }
         }
     } else if (F8 && warp >= 8) {
         // ---------------- scales ----------------
-        // The rows' scales along K are contiguous: eight threads take eight stages of one
-        // row, a chunk ahead of its use, and store them transposed in shared memory. Each
-        // warp then writes all scales of a stage to its own lane quarter (the block-scaled
-        // MMA reads a copy in each): word j of lane l is row 32 j + l.
-        const uint32_t quarter = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + 2 * N;
+        // The rows' scales along K are contiguous: eight threads take a chunk's eight stages
+        // of one row, a chunk ahead of its use, and store the bytes where the MMA warp's
+        // copies to tensor memory read them.
         const int t = threadIdx.x - 256, sub = t >> 3, sst = t & 7;
         constexpr int NB = N / 16;
-        int i = 0, chunk = 0;
+        int chunk = 0;
         bool ok = true;
         if constexpr (!UP) pdl_wait();
-        for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+        for (int w = w0; w < items && ok; w += wstep) {
             const Item it = item_of<N>(a, tab, start, w);
+            int mt = kPair ? 2 * it.m + (int)rank : it.m;
+            if (!UP && mt * 128 >= a.hidden) mt = 0;  // the tile too many: any scales
             const long long ks = a.nst;  // scales per row: one per stage
             // row sub + 16 i of the tile
-            const float* pa = a.a_scales + (UP ? (long long)it.e * 2 * a.inter + it.m * 64 + sub
-                                               : (long long)it.e * a.hidden + it.m * 128 + sub) * ks + sst;
+            const float* pa = a.a_scales + (UP ? (long long)it.e * 2 * a.inter + mt * 64 + sub
+                                               : (long long)it.e * a.hidden + mt * 128 + sub) * ks + sst;
             const long long da = UP ? (long long)a.inter * ks : 16 * ks;
             uint32_t pb[NB];
 #pragma unroll
@@ -449,63 +576,43 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
                 for (int k = 0; k < NB; ++k) vb[k] = in ? __float_as_uint(bsrc[pb[k] * ks + st0 + sst]) : 0u;
             };
             load(0);
-            for (int st0 = 0; st0 < a.nst && ok; st0 += kSfStages, ++chunk) {
+            for (int st0 = 0; st0 < a.nst; st0 += kSfStages, ++chunk) {
+                int go = 1;
+                if (lane == 0)
+                    go = wait_or_abort(sf_empty + (chunk & 1), (uint32_t)(((chunk >> 1) & 1) ^ 1), abort_flag, a.status);
+                go = __shfl_sync(0xffffffffu, go, 0);
+                if (!go) {
+                    ok = false;
+                    break;
+                }
                 uint8_t* buf = smem + L::SF + (chunk & 1) * L::SFBUF;
-                uint32_t* words = reinterpret_cast<uint32_t*>(buf + kSfStages * L::SFP);
+                // row sub + 16 k: word [sub + 16 (k % 2)][k / 2 % 4] of block k / 8
+                uint8_t* to = buf + (sst >> 2) * kSfBlock + sub * 16 + (sst & 3);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) buf[sst * L::SFP + sub + 16 * k] = (uint8_t)(va[k] >> 23);
+                for (int k = 0; k < 8; ++k) to[(k & 1) * 256 + (k >> 1) * 4] = (uint8_t)(va[k] >> 23);
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
+                    const uint32_t at = (k >> 3) * kSfBlock + (k & 1) * 256 + ((k >> 1) & 3) * 4;
                     if constexpr (UP)
-                        buf[sst * L::SFP + 128 + sub + 16 * k] = (uint8_t)(vb[k] >> 23);
+                        buf[L::SF_B + (sst >> 2) * L::SFN * kSfBlock + sub * 16 + (sst & 3) + at] = (uint8_t)(vb[k] >> 23);
                     else
-                        words[sst * L::SFW_P + sub + 16 * k] = vb[k];
+                        *reinterpret_cast<uint32_t*>(buf + L::SF_B + sst * L::SFN * kSfBlock + sub * 16 + at) = vb[k];
                 }
-                // The chunk is in place; and every warp is done with the one before it, so
-                // the next turn may overwrite that.
-                asm volatile("bar.sync 2, 128;\n" ::: "memory");
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_leader(sf_full + (chunk & 1));
                 if (st0 + kSfStages < a.nst) load(st0 + kSfStages);
-                const int ns = min(kSfStages, a.nst - st0);
-                for (int q = 0; q < ns; ++q, ++i) {
-                    uint32_t fa[4], fb[L::SFB];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) fa[j] = buf[q * L::SFP + 32 * j + lane] * 0x01010101u;
-#pragma unroll
-                    for (int j = 0; j < L::SFB; ++j) {
-                        const int r = 32 * j + lane;
-                        fb[j] = 0u;
-                        if (r < N)
-                            fb[j] = UP ? buf[q * L::SFP + 128 + r] * 0x01010101u : words[q * L::SFW_P + r];
-                    }
-                    const int s = i % S;
-                    int go = 1;
-                    if (lane == 0)
-                        go = poll_wait(empty + s, (uint32_t)(((i / S) & 1) ^ 1), abort_flag, a.status);
-                    go = __shfl_sync(0xffffffffu, go, 0);
-                    if (!go) ok = false;  // (the other warps keep the barrier above: they are told below)
-                    if (!ok) break;
-                    tc_fence_after();
-                    tc_st_cols<4>(quarter + s * L::SFW, fa);
-                    tc_st_cols<L::SFB>(quarter + s * L::SFW + 4, fb);
-                    tc_wait_st();
-                    tc_fence_before();
-                    if (lane == 0) mbar_arrive(sfull + s);
-                }
-                int all;  // the four warps share the barrier: they leave together
-                asm volatile(
-                    "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\n"
-                    "barrier.cta.red.and.pred q, 2, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
-                    : "=r"(all)
-                    : "r"((int)ok)
-                    : "memory");
-                ok = all != 0;
             }
         }
     }
     __syncthreads();
+    if constexpr (kPair) cluster_barrier();  // neither leaves while the other may reach it
     if (warp == 1) {
         tc_fence_after();
-        tc_dealloc(tmem, L::TMEM);
+        if constexpr (kPair)
+            tc_dealloc2(tmem, L::TMEM);
+        else
+            tc_dealloc(tmem, L::TMEM);
     }
 }
 
@@ -615,7 +722,7 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 // in flight; an expert with more pairs takes several tiles.
 int tile_of(long long pairs, int n_experts, bool f8) {
     const long long mean = (pairs + n_experts - 1) / n_experts;
-    return mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : f8 ? 192 : 256;
+    return mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : f8 ? 224 : 256;
 }
 
 struct Plan {
@@ -656,6 +763,26 @@ int check_experts(const char* name, int rows, int topk, int n_experts, int hidde
     return DSA_OK;
 }
 
+// Clusters of the launch that fit the device at once, asked once per kernel and device.
+cudaError_t max_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int* n) {
+    static std::mutex mu;
+    static std::map<std::pair<int, const void*>, int> known;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(mu);
+    auto it = known.find({dev, kernel});
+    if (it == known.end()) {
+        int c = 0;
+        e = cudaOccupancyMaxActiveClusters(&c, kernel, &cfg);
+        if (e != cudaSuccess) return e;
+        if (c < 1) return cudaErrorLaunchOutOfResources;
+        it = known.emplace(std::make_pair(dev, kernel), c).first;
+    }
+    *n = it->second;
+    return cudaSuccess;
+}
+
 template <bool F8, bool UP, int N>
 int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_rows, int sms, cudaStream_t st) {
     using L = EL<F8, UP, N>;
@@ -681,8 +808,30 @@ int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_row
         rc = make_tmap_2d(&tmB, dt, b, I, (uint64_t)b_rows, I * es, bk, N < 32 ? N : 32, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (rc) return rc;
-    cudaError_t e = launch_pdl(experts_kernel<F8, UP, N>, dim3((unsigned)sms), dim3(F8 ? 384 : 256), (size_t)dyn, st,
-                               tmA, tmB, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(F8 ? 384 : 256);
+    cfg.dynamicSmemBytes = (size_t)dyn;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = paired(N) ? 2 : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (paired(N)) {
+        cfg.gridDim.x &= ~1u;
+        // One pair of blocks per pair of SMs; fewer where not all SMs come in pairs (a pair that
+        // waited for others to leave would take its share of the items after theirs).
+        int clusters = 0;
+        cudaError_t q = max_clusters((const void*)experts_kernel<F8, UP, N>, cfg, &clusters);
+        if (q != cudaSuccess) return cuda_fail(q, "dsa_experts occupancy");
+        if (2 * clusters < sms) cfg.gridDim.x = (unsigned)(2 * clusters);
+    }
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, experts_kernel<F8, UP, N>, tmA, tmB, a);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_experts launch");
     return DSA_OK;
@@ -695,7 +844,7 @@ int gemm_dispatch(const GemmArgs& a, const void* weights, const void* b, int b_r
         case 32: return gemm_launch<F8, UP, 32>(a, weights, b, b_rows, sms, st);
         case 64: return gemm_launch<F8, UP, 64>(a, weights, b, b_rows, sms, st);
         case 128: return gemm_launch<F8, UP, 128>(a, weights, b, b_rows, sms, st);
-        default: return gemm_launch<F8, UP, F8 ? 192 : 256>(a, weights, b, b_rows, sms, st);
+        default: return gemm_launch<F8, UP, F8 ? 224 : 256>(a, weights, b, b_rows, sms, st);
     }
 }
 
@@ -760,7 +909,8 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     a.part = reinterpret_cast<float*>(ws + p.part);
     a.x_scales = x_scales;
     a.status = status;
-    a.n_m = inter / 64;
+    const bool two = paired(tile_of(pairs, n_experts, f8));
+    a.n_m = inter / (two ? 128 : 64);
     a.nst = hidden / (f8 ? 128 : 64);
     a.a_scales = w13_scales;
     int x_rows = rows;
@@ -776,7 +926,7 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     rc = f8 ? gemm_dispatch<true, true>(a, w13, x, x_rows, sms, st)
             : gemm_dispatch<false, true>(a, w13, x, x_rows, sms, st);
     if (rc) return rc;
-    a.n_m = hidden / 128;
+    a.n_m = two ? (hidden + 255) / 256 : hidden / 128;
     a.nst = inter / (f8 ? 128 : 64);
     a.a_scales = w2_scales;
     rc = f8 ? gemm_dispatch<true, false>(a, w2, a.h8, pairs, sms, st)

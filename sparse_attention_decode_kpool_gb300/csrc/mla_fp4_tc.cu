@@ -151,25 +151,6 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
                  "r"(v.z), "r"(v.w)
                  : "memory");
 }
-// MMA and commit by one elected lane of a converged warp (always the same one). The whole
-// warp runs the issue loop, so descriptors and loop counters stay in uniform registers,
-// where tcgen05.mma takes them; with one lane in the loop each was moved there again and
-// an issue took about 100 cycles instead of 60.
-__device__ __forceinline__ void warp_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t accumulate) {
-    asm volatile(
-        "{\n.reg .pred p, e;\nelect.sync _|e, 0xffffffff;\nsetp.ne.b32 p, %4, 0;\n"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-__device__ __forceinline__ void warp_commit(uint64_t* bar) {
-    asm volatile(
-        "{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\n"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-            smem_u32(bar))
-        : "memory");
-}
 // A warp waits for a phase, for about a second at most; after a timeout (here or in another
 // role) it returns at once. The whole warp waits and stays converged: with one lane
 // waiting for the others the warp came out in two parts, and each decoded by itself.

@@ -20,15 +20,17 @@
 // lanes, 16 apart. The rows of x are gathered by TMA (four rows a copy), those of h are
 // contiguous in the pairs' order.
 //
-// Roles: warp 0 copies, warp 1 issues the MMAs, warps 4-7 take the accumulators (two, so
-// that the tensor cores run on meanwhile), with FP8 warps 8-11 lay out the scales: one byte (the
+// Roles: warp 0 copies, warp 1 issues the MMAs, warps 4-11 take the accumulators (two, so
+// that the tensor cores run on meanwhile), with FP8 warps 12-15 lay out the scales: one byte (the
 // exponent) per row and 32 K values for the block-scaled MMA, which warp 1 copies to tensor
-// memory in order with its MMAs. (Stored there by the warps themselves, with tcgen05.st, the
-// scales of a stage took as long as its MMAs: a prefill's products were twice as slow.) Waits
-// are bounded; one that gives up sets DSA_STATUS_TIMEOUT and every role leaves its loop.
+// memory in order with its MMAs. (Such a copy takes the tensor pipe about 170 cycles; stored
+// by the warps instead, with tcgen05.st, the scales came so late behind the MMAs in flight
+// that the first product of 4,096 rows took 294 us instead of 243.) Waits are bounded; one that gives up sets DSA_STATUS_TIMEOUT and every role leaves its loop.
 #include <map>
 #include <mutex>
 #include <utility>
+
+#include <cuda_fp16.h>
 
 #include "fp8.cuh"
 #include "tc.cuh"
@@ -37,9 +39,15 @@ namespace dsa {
 namespace {
 
 constexpr uint32_t kABytes = 128 * 128;  // 128 weight rows x 128 bytes of K
-constexpr int kStgLd = 80;               // floats per pair in the activation's staging
+// The epilogue's staging in shared memory: 16 pairs x 64 channels of h, or x 128 of y, f32, each
+// 32 channels four floats further on: the eight threads of a pair read 16 bytes each from
+// different banks (and two pairs 16 banks apart are written at once).
+constexpr int kChunk = 16;
+constexpr int kStgUp = 80, kStgDown = 144;  // floats per pair
 constexpr int kSfStages = 8;             // K stages whose scales travel together: a chunk
 constexpr uint32_t kSfBlock = 512;       // scale words of 128 rows, [32][4]: word [l][j] is row 32 j + l
+constexpr int kEpiWarps = 8;             // warps 4-11 take the accumulators, in two groups
+constexpr int kSfWarp = 4 + kEpiWarps;   // FP8: warps 12-15 lay out the scales
 
 // A pair of blocks shares its MMAs where a tile is that large: each holds its own 128 weight
 // rows and half of the pairs' rows, and gets its weight rows' products with all pairs. Shared
@@ -49,26 +57,33 @@ constexpr bool paired(int n) { return n > 128; }
 
 template <bool F8, bool UP, int N>
 struct EL {  // shared and tensor memory of one block
-    static constexpr int BR = paired(N) ? (N / 2 + 31) / 32 * 32 : N;  // rows of x or h of a stage
+    static constexpr int BR = paired(N) ? N / 2 : N;        // rows of x or h of a stage
+    static constexpr int BOX = BR % 32 == 0 ? 32 : 16;      // of a copy
     static constexpr uint32_t STAGE = kABytes + BR * 128;
-    static constexpr int S = (int)((200u * 1024u) / STAGE);  // ring stages
-    static constexpr uint32_t RING = S * STAGE;
-    static constexpr uint32_t STG = RING;  // activation staging, 32 pairs x 64 channels
+    // Staging of the epilogue's groups of warps (a small tile is one group's).
+    static constexpr uint32_t STG_BYTES = 4 * kChunk * (UP ? kStgUp : kStgDown);
+    static constexpr int STG_BUFS = UP || F8 ? 2 : 1;  // of a group
+    static constexpr int STG_GROUPS = N > kChunk ? 2 : 1;
     // FP8: two chunks of scales. A word holds four bytes along K: those of four stages where a
     // scale spans one (weights, x), those of one stage for h.
-    static constexpr int SFN = (N + 127) / 128;       // blocks of N pairs
-    static constexpr int SFC = SFN * (UP ? 1 : 4);    // of four stages
-    static constexpr uint32_t SF = (STG + (UP ? 32 * kStgLd * 4 : 0) + 127) & ~127u;
-    static constexpr uint32_t SF_B = kSfStages / 4 * kSfBlock;  // the pairs' part of a chunk
-    static constexpr uint32_t SFBUF = !F8 ? 0 : SF_B + (UP ? kSfStages / 4 : kSfStages) * SFN * kSfBlock;
+    static constexpr int SFN = (N + 127) / 128;                 // blocks of N pairs
+    static constexpr int SFC = SFN * (UP ? 1 : 4);              // of four stages
+    static constexpr uint32_t SF_B = kSfStages / 4 * kSfBlock;  // where the pairs' part of a chunk starts
+    static constexpr uint32_t SFBUF = !F8 ? 0 : SF_B + kSfStages / 4 * SFC * kSfBlock;
+    static constexpr int COLS = 2 * N + (F8 ? 4 + 4 * SFC : 0);
+    static constexpr uint32_t TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+    static_assert(COLS <= 512, "tensor memory");
+    // The rest is the ring's. (512: barriers; 1024: the ring's alignment.)
+    static constexpr uint32_t TAB_MAX = 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1);
+    static constexpr uint32_t OTHER = STG_GROUPS * STG_BUFS * STG_BYTES + 2 * SFBUF + TAB_MAX + 512 + 1024;
+    static constexpr int S = (int)((227 * 1024 - OTHER) / STAGE);  // ring stages
+    static constexpr uint32_t STG = S * STAGE;
+    static constexpr uint32_t SF = STG + STG_GROUPS * STG_BUFS * STG_BYTES;
     static constexpr uint32_t BARS = SF + 2 * SFBUF;
     static constexpr int NBARS = 2 * S + 9;  // full, empty; 2 + 2 scales, accumulators; drain
     static constexpr uint32_t MISC = BARS + 8 * NBARS;
     static constexpr uint32_t TAB = MISC + 16;  // int[2][n_experts + 1]
-    static constexpr int COLS = 2 * N + (F8 ? 4 + 4 * SFC : 0);
-    static constexpr uint32_t TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-    static_assert(COLS <= 512, "tensor memory");
-    static_assert(STAGE % 1024 == 0, "stage alignment");
+    static_assert(8 * NBARS + 16 <= 512 && SF % 128 == 0 && BARS % 8 == 0 && STAGE % 1024 == 0, "layout");
 };
 
 // The first product gathers rows of x itself for small tiles. A gathering copy takes about 60
@@ -89,7 +104,8 @@ struct GemmArgs {
     uint8_t* h8;         // E4M3 [pairs, inter]
     uint8_t* h_scales;   // [pairs, inter / 32]
     // second product
-    float* part;  // [pairs (row, j), hidden]
+    uint16_t* part;     // f16 [pairs (row, j), hidden], under
+    uint8_t* part_exp;  // [pairs, hidden / 32] powers of two (biased)
     // FP8 scales
     const float* a_scales;  // weights, [E * rows, K / 128]
     const float* x_scales;  // [rows, hidden / 128]
@@ -113,14 +129,48 @@ __device__ __forceinline__ Item item_of(const GemmArgs& a, const int* tab, const
         else
             hi = mid;
     }
+    // The expert's pairs in equal tiles (a small rest would take a third of a full tile's time).
+    constexpr int kRound = paired(N) ? 32 : 16;
+    const int cnt = start[lo + 1] - start[lo], tiles = tab[lo + 1] - tab[lo];
+    const int size = ((cnt + tiles - 1) / tiles + kRound - 1) / kRound * kRound;
     it.e = lo;
-    const int off = (tile - tab[lo]) * N;
-    it.pos = start[lo] + off;
-    it.n = min(N, start[lo + 1] - it.pos);
+    it.pos = start[lo] + (tile - tab[lo]) * size;
+    it.n = min(size, start[lo + 1] - it.pos);
     return it;
 }
 
-__device__ __forceinline__ void bar_sync_epilogue() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+// g / (1 + exp(-g)) with the division and the exponential of the special-function unit, off by a
+// few 2^-22 of the result: h is rounded to 2^-9 at best.
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
+
+__device__ __forceinline__ void tc_ld16(uint32_t (&v)[16], uint32_t taddr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+// Waits for this thread's tensor-memory loads, as tc_wait_ld.
+__device__ __forceinline__ void tc_wait_ld16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
+
+// Barrier `id` of 128 threads (a warpgroup's); whether every one of them comes with ok.
+__device__ __forceinline__ bool group_barrier(int id, bool ok) {
+    int all;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\n"
+        "barrier.cta.red.and.pred q, %2, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+        : "=r"(all)
+        : "r"((int)ok), "r"(id)
+        : "memory");
+    return all != 0;
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;\n" ::"r"(id) : "memory"); }
 
 // One block of scales (no swizzle, 8-row groups of 16-byte rows 128 bytes apart) from shared
 // memory to four columns of tensor memory, a copy in each lane quarter. In order with the
@@ -185,12 +235,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // UP: the first product (rows of x gathered, activation); else the second.
 template <bool F8, bool UP, int N>
-__global__ void __launch_bounds__(F8 ? 384 : 256, 1)
+__global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     experts_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, GemmArgs a) {
     using L = EL<F8, UP, N>;
     constexpr int S = L::S;
     constexpr bool kGather = UP && gathers(N), kPair = paired(N);
-    constexpr int kBox = N < 32 ? N : 32;  // rows per copy
+    constexpr int kBox = L::BOX;
     constexpr int kRound = kPair ? 32 : 16;  // pairs of an MMA: multiples of it
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -221,7 +271,7 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
             mbar_init(sf_full + i, kPair ? 8 : 4);
             mbar_init(sf_empty + i, 1);
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, kPair ? 8 : 4);
+            mbar_init(acc_empty + i, (kPair ? 2 : 1) * kEpiWarps);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -428,122 +478,123 @@ __global__ void __launch_bounds__(F8 ? 384 : 256, 1)
             if (lane == 0 && !mbar_wait(drain, 0)) flag_status(a.status, DSA_STATUS_TIMEOUT);
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= 4 && warp < kSfWarp) {
         // ---------------- accumulators ----------------
-        const int ew = warp - 4, et = threadIdx.x - 128;
-        float* stg = reinterpret_cast<float*>(smem + L::STG);
-        int t = 0;
+        // Two groups of four warps take a chunk of 16 columns (pairs) in turn: out of tensor
+        // memory a chunk ahead, transposed through shared memory, a pair's channels to eight
+        // threads.
+        const int ew = warp & 3, eg = (warp - 4) >> 2, et = threadIdx.x & 127;
+        float* stg0 = reinterpret_cast<float*>(smem + L::STG + eg * L::STG_BUFS * L::STG_BYTES);
+        const int p = et >> 3, seg = et & 7;  // pair of the chunk; 8 or 16 channels
+        int t = 0, turn = 0;
         for (int w = w0; w < items; w += wstep, ++t) {
             const Item it = item_of<N>(a, tab, start, w);
             const int mt = kPair ? 2 * it.m + (int)rank : it.m;
             int got = 1;
             if (lane == 0) got = wait_or_abort(acc_full + (t & 1), (uint32_t)((t >> 1) & 1), abort_flag, a.status);
             got = __shfl_sync(0xffffffffu, got, 0);
-            if constexpr (UP) {  // the four warps share barriers below: they leave together
-                int all;
-                asm volatile(
-                    "{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\n"
-                    "barrier.cta.red.and.pred q, 1, 128, p;\nselp.s32 %0, 1, 0, q;\n}\n"
-                    : "=r"(all)
-                    : "r"(got)
-                    : "memory");
-                got = all;
-            }
+            got = group_barrier(1 + eg, got);  // the group shares barriers below: it leaves together
             if (!got) break;
             tc_fence_after();
             const uint32_t acc = tmem + ((uint32_t)(32 * ew) << 16) + (t & 1) * N;
-            const int n16 = (it.n + kRound - 1) / kRound * kRound;
-            for (int c0 = 0; c0 < it.n; c0 += 32) {
-                uint32_t v[32];
-                if (N >= 32 && n16 - c0 > 16) {
-                    tc_ld32(v, acc + c0);
-                    tc_wait_ld(v);
-                } else {
-                    uint32_t (&u)[32] = v;
-                    asm volatile(
-                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                        "%12,%13,%14,%15}, [%16];\n"
-                        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
-                          "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
-                          "=r"(u[14]), "=r"(u[15])
-                        : "r"(acc + c0));
-#pragma unroll
-                    for (int j = 16; j < 32; ++j) v[j] = 0u;
-                    tc_wait_ld(v);
-                }
-                if (c0 + 32 >= it.n) {  // the last columns are in registers
-                    tc_fence_before();
-                    if (lane == 0) arrive_leader(acc_empty + (t & 1));
-                }
+            uint32_t v[16], nv[16];
+            if (kChunk * eg < it.n) {
+                tc_ld16(v, acc + kChunk * eg);
+                tc_wait_ld16(v);
+            }
+            for (int c0 = kChunk * eg; c0 < it.n; c0 += 2 * kChunk, ++turn) {
+                const bool more = c0 + 2 * kChunk < it.n;
+                if (more) tc_ld16(nv, acc + c0 + 2 * kChunk);
+                float* stg = stg0 + (L::STG_BUFS == 2 ? (turn & 1) * (L::STG_BYTES / 4) : 0);
+                if (L::STG_BUFS == 1) group_sync(1 + eg);  // the staging is free
                 if constexpr (UP) {
-                    bar_sync_epilogue();  // the staging is free
                     const bool hi = lane >= 16;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
+                    for (int c = 0; c < kChunk; c += 2) {
                         // lanes below 16 hold gates and take column c, the others hold ups and take c + 1
                         const float mine = __uint_as_float(hi ? v[c + 1] : v[c]);
-                        const float other =
-                            __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? v[c] : v[c + 1]), 16);
+                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? v[c] : v[c + 1]), 16);
                         const float g = hi ? other : mine, u = hi ? mine : other;
-                        stg[(c + (hi ? 1 : 0)) * kStgLd + 16 * ew + (lane & 15)] = g / (1.f + __expf(-g)) * u;
+                        stg[(c + (hi ? 1 : 0)) * kStgUp + 16 * ew + 4 * (ew >> 1) + (lane & 15)] = silu(g) * u;
                     }
-                    bar_sync_epilogue();
-                    const int p = et >> 2, seg = et & 3;  // pair, 16 channels
-                    float f[16];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 q = *reinterpret_cast<const float4*>(stg + p * kStgLd + seg * 16 + 4 * j);
-                        f[4 * j] = q.x;
-                        f[4 * j + 1] = q.y;
-                        f[4 * j + 2] = q.z;
-                        f[4 * j + 3] = q.w;
-                    }
+                    group_sync(1 + eg);
+                    float f[8];
+                    const float* from = stg + p * kStgUp + seg * 8 + 4 * (seg >> 2);
+                    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(from);
+                    *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(from + 4);
                     const bool live = c0 + p < it.n;
-                    const long long at = (long long)(it.pos + c0 + p) * a.inter + mt * 64 + seg * 16;
+                    const long long at = (long long)(it.pos + c0 + p) * a.inter + mt * 64 + seg * 8;
                     if constexpr (F8) {
                         float m = 0.f;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(f[j]));
+                        for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(f[j]));
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
                         const int e = fp8_scale_exp(m);
                         const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-                        uint32_t o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[j] = e4m3x2(f[4 * j] * inv, f[4 * j + 1] * inv) |
-                                   (e4m3x2(f[4 * j + 2] * inv, f[4 * j + 3] * inv) << 16);
                         if (live) {
-                            *reinterpret_cast<uint4*>(a.h8 + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                            if (!(seg & 1)) a.h_scales[at >> 5] = (uint8_t)(e + 127);
+                            *reinterpret_cast<uint2*>(a.h8 + at) =
+                                make_uint2(e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16),
+                                           e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16));
+                            if (!(seg & 3)) a.h_scales[at >> 5] = (uint8_t)(e + 127);
                         }
                     } else if (live) {
-                        uint4 o[2];
-                        o[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                          pack_bf16x2(f[6], f[7]));
-                        o[1] = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]),
-                                          pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
-                        uint4* dst = reinterpret_cast<uint4*>(a.h + at);
-                        dst[0] = o[0];
-                        dst[1] = o[1];
+                        *reinterpret_cast<uint4*>(a.h + at) =
+                            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                       pack_bf16x2(f[6], f[7]));
                     }
                 } else {
-                    const int mine = a.pair_of[it.pos + (c0 + lane < it.n ? c0 + lane : 0)];
-                    float* to = a.part + mt * 128 + 32 * ew + lane;
-                    const bool inside = !kPair || mt * 128 < a.hidden;  // an odd number of row tiles: one too many
+                    // A product is kept to 11 bits, as f16 under one power of two for 32 channels of a
+                    // pair: 2^-12 of it at most, an eighth of what y's own rounding costs, and half
+                    // the bytes of f32.
+                    const bool live = c0 + p < it.n && (!kPair || mt * 128 < a.hidden);  // (odd row tiles: one too many)
+                    const int pair = a.pair_of[it.pos + (live ? c0 + p : 0)];
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int pair = __shfl_sync(0xffffffffu, mine, c);
-                        if (c0 + c < it.n && inside) to[(long long)pair * a.hidden] = __uint_as_float(v[c]);
+                    for (int c = 0; c < kChunk; ++c) stg[c * kStgDown + 36 * ew + lane] = __uint_as_float(v[c]);
+                    group_sync(1 + eg);
+                    float f[16];
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<float4*>(f + 4 * j) =
+                            *reinterpret_cast<const float4*>(stg + p * kStgDown + seg * 16 + 4 * (seg >> 1) + 4 * j);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {  // the largest finite one
+                        const uint32_t mag = __float_as_uint(f[j]) & 0x7fffffffu;
+                        top = max(top, mag < 0x7f800000u ? mag : 0u);
+                    }
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    const int e = max((int)(top >> 23) - 14, 1);  // 2^(e - 127): values below 2^15
+                    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const __half2 h2 = __floats2half2_rn(f[2 * j] * inv, f[2 * j + 1] * inv);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&h2);
+                    }
+                    if (live) {
+                        uint4* dst = reinterpret_cast<uint4*>(a.part + (long long)pair * a.hidden + mt * 128 + seg * 16);
+                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                        if (!(seg & 1))
+                            a.part_exp[(long long)pair * (a.hidden >> 5) + mt * 4 + (seg >> 1)] = (uint8_t)e;
                     }
                 }
+                if (more) {
+                    tc_wait_ld16(nv);
+#pragma unroll
+                    for (int c = 0; c < kChunk; ++c) v[c] = nv[c];
+                }
             }
+            tc_fence_before();  // this warp's columns are in registers
+            if (lane == 0) arrive_leader(acc_empty + (t & 1));
         }
-    } else if (F8 && warp >= 8) {
+    } else if (F8 && warp >= kSfWarp) {
         // ---------------- scales ----------------
         // The rows' scales along K are contiguous: eight threads take a chunk's eight stages
         // of one row, a chunk ahead of its use, and store the bytes where the MMA warp's
         // copies to tensor memory read them.
-        const int t = threadIdx.x - 256, sub = t >> 3, sst = t & 7;
+        const int t = threadIdx.x - 32 * kSfWarp, sub = t >> 3, sst = t & 7;
         constexpr int NB = N / 16;
         int chunk = 0;
         bool ok = true;
@@ -688,31 +739,50 @@ __global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ 
     }
 }
 
-// y[r] = sum over the row's experts, in their order in ids, of weight times partial.
+// y[r] = sum over the row's experts, in their order in ids, of weight times product; eight
+// channels a thread.
 constexpr int kSumThreads = 256;
-__global__ void __launch_bounds__(kSumThreads) combine_kernel(const float* __restrict__ part,
+__global__ void __launch_bounds__(kSumThreads) combine_kernel(const uint16_t* __restrict__ part,
+                                                              const uint8_t* __restrict__ part_exp,
                                                               const int32_t* __restrict__ ids,
                                                               const float* __restrict__ weights, int rows,
                                                               int topk, int n_experts, int hidden,
                                                               uint16_t* __restrict__ y) {
     pdl_wait();
-    const int per_row = hidden / 4;
+    const int per_row = hidden / 8;
     const long long n = (long long)rows * per_row;
     for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kSumThreads) {
         const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row);
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < topk; ++j) {
-            const long long p = (long long)r * topk + j;
-            const int id = __ldg(ids + p);
-            if (id < 0 || id >= n_experts) continue;
-            const float w = __ldg(weights + p);
-            const float4 v = __ldg(reinterpret_cast<const float4*>(part + p * hidden) + c);
-            s.x = fmaf(w, v.x, s.x);
-            s.y = fmaf(w, v.y, s.y);
-            s.z = fmaf(w, v.z, s.z);
-            s.w = fmaf(w, v.w, s.w);
+        float s[8] = {};
+        for (int j0 = 0; j0 < topk; j0 += 4) {  // four products are requested before the first is used
+            uint4 q[4];
+            float k[4], w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const long long p = (long long)r * topk + j0 + j;
+                const int id = j0 + j < topk ? __ldg(ids + p) : -1;
+                w[j] = 0.f;
+                k[j] = 0.f;
+                q[j] = make_uint4(0, 0, 0, 0);
+                if (id >= 0 && id < n_experts) {
+                    q[j] = ldg16_stream(part + p * hidden + c * 8);
+                    k[j] = __uint_as_float((uint32_t)__ldg(part_exp + p * (hidden >> 5) + (c >> 2)) << 23);
+                    w[j] = __ldg(weights + p);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[m]));
+                    s[2 * m] = fmaf(w[j], f.x * k[j], s[2 * m]);  // (the power of two is exact)
+                    s[2 * m + 1] = fmaf(w[j], f.y * k[j], s[2 * m + 1]);
+                }
+            }
         }
-        reinterpret_cast<uint2*>(y)[i] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+        reinterpret_cast<uint4*>(y)[i] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
+                                                    pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
     }
 }
 
@@ -726,7 +796,7 @@ int tile_of(long long pairs, int n_experts, bool f8) {
 }
 
 struct Plan {
-    size_t counts, starts, pair_of, x, h, h_scales, part, bytes;
+    size_t counts, starts, pair_of, x, h, h_scales, part, part_exp, bytes;
 };
 Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     Plan p;
@@ -744,7 +814,9 @@ Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     p.h_scales = at;
     at += f8 ? al256((size_t)pairs * (inter / 32)) : 0;
     p.part = at;
-    at += al256((size_t)pairs * hidden * 4);
+    at += al256((size_t)pairs * hidden * 2);
+    p.part_exp = at;
+    at += al256((size_t)pairs * (hidden / 32));
     p.bytes = at;
     return p;
 }
@@ -786,7 +858,7 @@ cudaError_t max_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int*
 template <bool F8, bool UP, int N>
 int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_rows, int sms, cudaStream_t st) {
     using L = EL<F8, UP, N>;
-    static_assert(L::TAB + 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1) + 1024 <= 227 * 1024, "shared memory");
+    static_assert(L::TAB + L::TAB_MAX + 1024 <= 227 * 1024, "shared memory");
     const int dyn = (int)(L::TAB + 8 * (a.n_experts + 1) + 1024);
     int rc = set_max_smem((const void*)experts_kernel<F8, UP, N>, 227 * 1024);
     if (rc) return rc;
@@ -800,17 +872,17 @@ int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_row
         const uint32_t box[5] = {bk, 16, 2, 4, 1};
         rc = make_tmap(&tmA, dt, weights, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc) return rc;
-        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, gathers(N) ? 1 : 32,
+        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, gathers(N) ? 1 : L::BOX,
                           CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
         rc = make_tmap_2d(&tmA, dt, weights, I, E * H, I * es, bk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc) return rc;
-        rc = make_tmap_2d(&tmB, dt, b, I, (uint64_t)b_rows, I * es, bk, N < 32 ? N : 32, CU_TENSOR_MAP_SWIZZLE_128B);
+        rc = make_tmap_2d(&tmB, dt, b, I, (uint64_t)b_rows, I * es, bk, L::BOX, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (rc) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
-    cfg.blockDim = dim3(F8 ? 384 : 256);
+    cfg.blockDim = dim3(F8 ? 512 : 384);
     cfg.dynamicSmemBytes = (size_t)dyn;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -906,7 +978,8 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     a.h = reinterpret_cast<uint16_t*>(ws + p.h);
     a.h8 = ws + p.h;
     a.h_scales = ws + p.h_scales;
-    a.part = reinterpret_cast<float*>(ws + p.part);
+    a.part = reinterpret_cast<uint16_t*>(ws + p.part);
+    a.part_exp = ws + p.part_exp;
     a.x_scales = x_scales;
     a.status = status;
     const bool two = paired(tile_of(pairs, n_experts, f8));
@@ -932,11 +1005,11 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     rc = f8 ? gemm_dispatch<true, false>(a, w2, a.h8, pairs, sms, st)
             : gemm_dispatch<false, false>(a, w2, a.h, pairs, sms, st);
     if (rc) return rc;
-    const long long n = (long long)rows * (hidden / 4);
+    const long long n = (long long)rows * (hidden / 8);
     long long blocks = (n + kSumThreads - 1) / kSumThreads;
     if (blocks > (long long)sms * 32) blocks = (long long)sms * 32;
-    e = launch_pdl(combine_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, (const float*)a.part, ids, weights,
-                   rows, topk, n_experts, hidden, y);
+    e = launch_pdl(combine_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, (const uint16_t*)a.part,
+                   (const uint8_t*)a.part_exp, ids, weights, rows, topk, n_experts, hidden, y);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_experts combine launch");
     return DSA_OK;

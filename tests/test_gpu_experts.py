@@ -74,8 +74,10 @@ class Problem:
     def check(self):
         """|y - exact| within what the arithmetic allows, element by element: bf16's rounding of
         y (2^-8 of it); f32 sums (2 K 2^-24 of the sum of magnitudes: twice a rounding sum's
-        bound, for an accumulator that truncates); and what a hidden value that lies that near
-        to a rounding border may become."""
+        bound, for an accumulator that truncates); what a hidden value that lies that near
+        to a rounding border may become; and each expert's product's rounding to 11 bits under a
+        power of two for 32 channels (2^-11 of it, or of 2^-28 of the largest of the 32: f16's
+        smallest step is 2^-24 where the largest lies in [2^14, 2^15))."""
         want = torch.zeros(self.rows, self.hidden, dtype=torch.float64, device="cuda")
         tol = torch.zeros_like(want)
         u = 2.0 ** -24
@@ -95,8 +97,11 @@ class Problem:
             off = torch.maximum((_hidden(h + s * dh, self.fp8) - held).abs(), (_hidden(h - s * dh, self.fp8) - held).abs())
             w2 = self.w2_64[e].T
             wt = self.weights[row, j].double()[:, None]
-            want.index_add_(0, row, wt * (held @ w2))
-            tol.index_add_(0, row, wt.abs() * (off @ w2.abs() + 2 * self.inter * u * (held.abs() @ w2.abs())))
+            p = held @ w2
+            want.index_add_(0, row, wt * p)
+            least = p.abs().reshape(len(row), -1, 32).amax(2).repeat_interleave(32, 1) * 2.0 ** -28
+            tol.index_add_(0, row, wt.abs() * (off @ w2.abs() + 2 * self.inter * u * (held.abs() @ w2.abs())
+                                               + 2.0 ** -11 * torch.maximum(p.abs(), least)))
         tol = tol * (1 + 2 * self.k * u) + 2.0 ** -8 * (want.abs() + tol) + self.k * u * want.abs() + 1e-38
         err = (self.y.double() - want).abs()
         assert bool((err <= tol).all()), (float((err / tol).max()), int((err > tol).sum()), err.numel())

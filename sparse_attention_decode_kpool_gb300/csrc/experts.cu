@@ -15,10 +15,10 @@
 // tensor-core cycles and no padding, and the weights stream as in the projection. A work
 // item is 128 weight rows times up to kN pairs of one expert over all of K; items go to
 // the blocks round robin, the weight rows of one expert and pair tile next to each other
-// in time. The gate and up rows of the first product are interleaved 16 by 16 in the tile
-// (a five-dimensional TMA box), so both halves of a hidden channel lie in one warp's
-// lanes, 16 apart. The rows of x are gathered by TMA (four rows a copy), those of h are
-// contiguous in the pairs' order.
+// in time. A tile of the first product is 64 gate rows and the 64 up rows of the same
+// channels (one three-dimensional TMA box). The rows of x are gathered by TMA (four rows a
+// copy) for small tiles; else they, as those of h, are contiguous in the pairs' order and one
+// copy (in four, a prefill's products took 6 to 8 % longer).
 //
 // Roles: warp 0 copies, warp 1 issues the MMAs, warps 4-11 take the accumulators (two, so
 // that the tensor cores run on meanwhile), with FP8 warps 12-15 lay out the scales: one byte (the
@@ -39,15 +39,15 @@ namespace dsa {
 namespace {
 
 constexpr uint32_t kABytes = 128 * 128;  // 128 weight rows x 128 bytes of K
-// The epilogue's staging in shared memory: 16 pairs x 64 channels of h, or x 128 of y, f32, each
-// 32 channels four floats further on: the eight threads of a pair read 16 bytes each from
-// different banks (and two pairs 16 banks apart are written at once).
-constexpr int kChunk = 16;
-constexpr int kStgUp = 80, kStgDown = 144;  // floats per pair
 constexpr int kSfStages = 8;             // K stages whose scales travel together: a chunk
 constexpr uint32_t kSfBlock = 512;       // scale words of 128 rows, [32][4]: word [l][j] is row 32 j + l
 constexpr int kEpiWarps = 8;             // warps 4-11 take the accumulators, in two groups
 constexpr int kSfWarp = 4 + kEpiWarps;   // FP8: warps 12-15 lay out the scales
+// The epilogue's staging in shared memory: 16 pairs x 128 weight rows, f32, each 32 rows four
+// floats further on: the eight threads of a pair read 16 bytes each from different banks.
+constexpr int kChunk = 16;
+constexpr int kStgLd = 144;  // floats per pair
+constexpr uint32_t kStgBytes = 4 * kChunk * kStgLd;
 
 // A pair of blocks shares its MMAs where a tile is that large: each holds its own 128 weight
 // rows and half of the pairs' rows, and gets its weight rows' products with all pairs. Shared
@@ -57,12 +57,11 @@ constexpr bool paired(int n) { return n > 128; }
 
 template <bool F8, bool UP, int N>
 struct EL {  // shared and tensor memory of one block
-    static constexpr int BR = paired(N) ? N / 2 : N;        // rows of x or h of a stage
-    static constexpr int BOX = BR % 32 == 0 ? 32 : 16;      // of a copy
+    static constexpr int BR = paired(N) ? (N / 2 + 31) / 32 * 32 : N;  // rows of x or h of a stage
     static constexpr uint32_t STAGE = kABytes + BR * 128;
-    // Staging of the epilogue's groups of warps (a small tile is one group's).
-    static constexpr uint32_t STG_BYTES = 4 * kChunk * (UP ? kStgUp : kStgDown);
-    static constexpr int STG_BUFS = UP || F8 ? 2 : 1;  // of a group
+    // Staging of the epilogue's groups of warps (a small tile is one group's), twice in the second
+    // product, whose K is shorter.
+    static constexpr int STG_BUFS = UP ? 1 : 2;
     static constexpr int STG_GROUPS = N > kChunk ? 2 : 1;
     // FP8: two chunks of scales. A word holds four bytes along K: those of four stages where a
     // scale spans one (weights, x), those of one stage for h.
@@ -75,10 +74,10 @@ struct EL {  // shared and tensor memory of one block
     static_assert(COLS <= 512, "tensor memory");
     // The rest is the ring's. (512: barriers; 1024: the ring's alignment.)
     static constexpr uint32_t TAB_MAX = 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1);
-    static constexpr uint32_t OTHER = STG_GROUPS * STG_BUFS * STG_BYTES + 2 * SFBUF + TAB_MAX + 512 + 1024;
+    static constexpr uint32_t OTHER = STG_GROUPS * STG_BUFS * kStgBytes + 2 * SFBUF + TAB_MAX + 512 + 1024;
     static constexpr int S = (int)((227 * 1024 - OTHER) / STAGE);  // ring stages
     static constexpr uint32_t STG = S * STAGE;
-    static constexpr uint32_t SF = STG + STG_GROUPS * STG_BUFS * STG_BYTES;
+    static constexpr uint32_t SF = STG + STG_GROUPS * STG_BUFS * kStgBytes;
     static constexpr uint32_t BARS = SF + 2 * SFBUF;
     static constexpr int NBARS = 2 * S + 9;  // full, empty; 2 + 2 scales, accumulators; drain
     static constexpr uint32_t MISC = BARS + 8 * NBARS;
@@ -240,7 +239,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     using L = EL<F8, UP, N>;
     constexpr int S = L::S;
     constexpr bool kGather = UP && gathers(N), kPair = paired(N);
-    constexpr int kBox = L::BOX;
     constexpr int kRound = kPair ? 32 : 16;  // pairs of an MMA: multiples of it
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -338,12 +336,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             if constexpr (kPair) {
                 const uint32_t bar = cluster_addr(full + s, 0);
                 if constexpr (UP)
-                    tma_load_5d_pair(dst, &tmA, k, 0, 0, mt * 4, it.e, bar);
+                    tma_load_3d_pair(dst, &tmA, k, mt * 64, 2 * it.e, bar);
                 else
                     tma_load_2d_pair(dst, &tmA, k, it.e * a.hidden + mt * 128, bar);
             } else {
                 if constexpr (UP)
-                    tma_load_5d(dst, &tmA, k, 0, 0, mt * 4, it.e, full + s);
+                    tma_load_3d(dst, &tmA, k, mt * 64, 2 * it.e, full + s);
                 else
                     tma_load_2d(dst, &tmA, k, it.e * a.hidden + mt * 128, full + s);
             }
@@ -359,20 +357,20 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                 }
             }
             const int half = (it.n + 31) / 32 * 16;  // of a pair of blocks: columns from each
-            const int quads = (it.n + 3) >> 2, boxes = ((kPair ? half : it.n) + kBox - 1) / kBox;
+            const int quads = (it.n + 3) >> 2;
             const int pos = it.pos + (kPair ? (int)rank * half : 0);
-            const uint32_t bytes = (kABytes + (kGather ? quads * 512 : boxes * kBox * 128)) * (kPair ? 2 : 1);
+            const uint32_t bytes = (kABytes + (kGather ? quads * 512 : L::BR * 128)) * (kPair ? 2 : 1);
             auto load_b = [&](int st, int s) {  // (all lanes)
                 const uint32_t dst = smem_u32(smem + s * L::STAGE) + kABytes;
                 const int k = st * (F8 ? 128 : 64);
                 if constexpr (kGather) {
                     if (lane < quads)
                         tma_gather4(dst + lane * 512, &tmB, k, row[0], row[1], row[2], row[3], full + s);
-                } else if (lane < boxes) {
+                } else if (lane == 0) {
                     if constexpr (kPair)
-                        tma_load_2d_pair(dst + lane * kBox * 128, &tmB, k, pos + lane * kBox, cluster_addr(full + s, 0));
+                        tma_load_2d_pair(dst, &tmB, k, pos, cluster_addr(full + s, 0));
                     else
-                        tma_load_2d(dst + lane * kBox * 128, &tmB, k, pos + lane * kBox, full + s);
+                        tma_load_2d(dst, &tmB, k, pos, full + s);
                 }
             };
             int st = 0;
@@ -484,12 +482,14 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         // memory a chunk ahead, transposed through shared memory, a pair's channels to eight
         // threads.
         const int ew = warp & 3, eg = (warp - 4) >> 2, et = threadIdx.x & 127;
-        float* stg0 = reinterpret_cast<float*>(smem + L::STG + eg * L::STG_BUFS * L::STG_BYTES);
+        float* stg0 = reinterpret_cast<float*>(smem + L::STG + eg * L::STG_BUFS * kStgBytes);
         const int p = et >> 3, seg = et & 7;  // pair of the chunk; 8 or 16 channels
         int t = 0, turn = 0;
         for (int w = w0; w < items; w += wstep, ++t) {
             const Item it = item_of<N>(a, tab, start, w);
             const int mt = kPair ? 2 * it.m + (int)rank : it.m;
+            auto pair_at = [&](int c0) { return a.pair_of[it.pos + (c0 + p < it.n ? c0 + p : 0)]; };
+            int pair = UP ? 0 : pair_at(kChunk * eg);
             int got = 1;
             if (lane == 0) got = wait_or_abort(acc_full + (t & 1), (uint32_t)((t >> 1) & 1), abort_flag, a.status);
             got = __shfl_sync(0xffffffffu, got, 0);
@@ -504,24 +504,26 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             }
             for (int c0 = kChunk * eg; c0 < it.n; c0 += 2 * kChunk, ++turn) {
                 const bool more = c0 + 2 * kChunk < it.n;
-                if (more) tc_ld16(nv, acc + c0 + 2 * kChunk);
-                float* stg = stg0 + (L::STG_BUFS == 2 ? (turn & 1) * (L::STG_BYTES / 4) : 0);
+                int next = 0;
+                if (more) {
+                    tc_ld16(nv, acc + c0 + 2 * kChunk);
+                    if (!UP) next = pair_at(c0 + 2 * kChunk);
+                }
+                float* stg = stg0 + (L::STG_BUFS == 2 ? (turn & 1) * (kStgBytes / 4) : 0);
                 if (L::STG_BUFS == 1) group_sync(1 + eg);  // the staging is free
-                if constexpr (UP) {
-                    const bool hi = lane >= 16;
 #pragma unroll
-                    for (int c = 0; c < kChunk; c += 2) {
-                        // lanes below 16 hold gates and take column c, the others hold ups and take c + 1
-                        const float mine = __uint_as_float(hi ? v[c + 1] : v[c]);
-                        const float other = __shfl_xor_sync(0xffffffffu, __uint_as_float(hi ? v[c] : v[c + 1]), 16);
-                        const float g = hi ? other : mine, u = hi ? mine : other;
-                        stg[(c + (hi ? 1 : 0)) * kStgUp + 16 * ew + 4 * (ew >> 1) + (lane & 15)] = silu(g) * u;
+                for (int c = 0; c < kChunk; ++c) stg[c * kStgLd + 36 * ew + lane] = __uint_as_float(v[c]);
+                group_sync(1 + eg);
+                if constexpr (UP) {
+                    float f[8], u[8];
+                    const float* from = stg + p * kStgLd + seg * 8 + 4 * (seg >> 2);
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        *reinterpret_cast<float4*>(f + j) = *reinterpret_cast<const float4*>(from + j);
+                        *reinterpret_cast<float4*>(u + j) = *reinterpret_cast<const float4*>(from + 72 + j);  // 64 rows on
                     }
-                    group_sync(1 + eg);
-                    float f[8];
-                    const float* from = stg + p * kStgUp + seg * 8 + 4 * (seg >> 2);
-                    *reinterpret_cast<float4*>(f) = *reinterpret_cast<const float4*>(from);
-                    *reinterpret_cast<float4*>(f + 4) = *reinterpret_cast<const float4*>(from + 4);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = silu(f[j]) * u[j];
                     const bool live = c0 + p < it.n;
                     const long long at = (long long)(it.pos + c0 + p) * a.inter + mt * 64 + seg * 8;
                     if constexpr (F8) {
@@ -548,16 +550,12 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                     // pair: 2^-12 of it at most, an eighth of what y's own rounding costs, and half
                     // the bytes of f32.
                     const bool live = c0 + p < it.n && (!kPair || mt * 128 < a.hidden);  // (odd row tiles: one too many)
-                    const int pair = a.pair_of[it.pos + (live ? c0 + p : 0)];
-#pragma unroll
-                    for (int c = 0; c < kChunk; ++c) stg[c * kStgDown + 36 * ew + lane] = __uint_as_float(v[c]);
-                    group_sync(1 + eg);
                     float f[16];
                     uint32_t top = 0;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         *reinterpret_cast<float4*>(f + 4 * j) =
-                            *reinterpret_cast<const float4*>(stg + p * kStgDown + seg * 16 + 4 * (seg >> 1) + 4 * j);
+                            *reinterpret_cast<const float4*>(stg + p * kStgLd + seg * 16 + 4 * (seg >> 1) + 4 * j);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {  // the largest finite one
                         const uint32_t mag = __float_as_uint(f[j]) & 0x7fffffffu;
@@ -584,6 +582,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                     tc_wait_ld16(nv);
 #pragma unroll
                     for (int c = 0; c < kChunk; ++c) v[c] = nv[c];
+                    pair = next;
                 }
             }
             tc_fence_before();  // this warp's columns are in registers
@@ -620,7 +619,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                 const bool in = st0 + sst < a.nst;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const float* src = UP ? pa + (k & 1) * da + (k >> 1) * 16 * ks : pa + k * da;
+                    const float* src = UP ? pa + (k >> 2) * da + (k & 3) * 16 * ks : pa + k * da;
                     va[k] = in ? __float_as_uint(__ldg(src + st0)) : 0u;
                 }
 #pragma unroll
@@ -867,17 +866,17 @@ int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_row
     const uint32_t bk = F8 ? 128 : 64;
     CUtensorMap tmA, tmB;
     if (UP) {
-        const uint64_t dims[5] = {H, 16, 2, I / 16, E};
-        const uint64_t strides[4] = {H * es, I * H * es, 16 * H * es, 2 * I * H * es};
-        const uint32_t box[5] = {bk, 16, 2, 4, 1};
-        rc = make_tmap(&tmA, dt, weights, 5, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        const uint64_t dims[3] = {H, I, 2 * E};
+        const uint64_t strides[2] = {H * es, I * H * es};
+        const uint32_t box[3] = {bk, 64, 2};
+        rc = make_tmap(&tmA, dt, weights, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc) return rc;
-        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, gathers(N) ? 1 : L::BOX,
+        rc = make_tmap_2d(&tmB, dt, b, H, (uint64_t)b_rows, H * es, bk, gathers(N) ? 1 : L::BR,
                           CU_TENSOR_MAP_SWIZZLE_128B);
     } else {
         rc = make_tmap_2d(&tmA, dt, weights, I, E * H, I * es, bk, 128, CU_TENSOR_MAP_SWIZZLE_128B);
         if (rc) return rc;
-        rc = make_tmap_2d(&tmB, dt, b, I, (uint64_t)b_rows, I * es, bk, L::BOX, CU_TENSOR_MAP_SWIZZLE_128B);
+        rc = make_tmap_2d(&tmB, dt, b, I, (uint64_t)b_rows, I * es, bk, L::BR, CU_TENSOR_MAP_SWIZZLE_128B);
     }
     if (rc) return rc;
     cudaLaunchConfig_t cfg = {};

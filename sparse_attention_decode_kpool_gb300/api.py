@@ -879,21 +879,22 @@ def dsa_rmsnorm(x, weight, eps: float, out=None, residual=None, residual_out=Non
                 scales=None, stream=None) -> None:
     """RMS norm of x + residual (x alone without one) into ``out`` (bf16) and/or the FP8 rows
     ``codes``, ``scales``; the sum itself into ``residual_out`` (which may be ``residual``)."""
-    shape, width = x.shape, x.size(-1)
-    for name, t in (("out", out), ("residual", residual), ("residual_out", residual_out),
-                    ("codes", codes)):
-        if t is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {tuple(shape)} as x")
-    if weight.numel() != width:
-        raise ValueError(f"weight must be [{width}]")
-    if codes is not None and scales is not None:
-        _fp8_rows(codes, scales)
+    shape = x.shape
+    width = shape[-1]
+    if (weight.numel() != width or (out is not None and out.shape != shape)
+            or (residual is not None and residual.shape != shape)
+            or (residual_out is not None and residual_out.shape != shape)):
+        raise ValueError(f"weight must be [{width}]; out, residual and residual_out must be "
+                         f"{tuple(shape)} as x")
+    if codes is not None and scales is not None and (codes.shape != shape
+                                                     or _fp8_rows(codes, scales) != width):
+        raise ValueError(f"codes must be {tuple(shape)} as x")
     dev = _device_of(x, "x")
     bf16 = torch.bfloat16
     _run(dev, stream, _lib.load().dsa_rmsnorm,
          _dev_ptr(x, bf16, dev, "x"), _dev_ptr(residual, bf16, dev, "residual"),
          _dev_ptr(weight, bf16, dev, "weight"), x.numel() // width if width else 0, width,
-         float(eps), _dev_ptr(residual_out, bf16, dev, "residual_out"),
+         eps, _dev_ptr(residual_out, bf16, dev, "residual_out"),
          _dev_ptr(out, bf16, dev, "out"), _dev_ptr(codes, torch.uint8, dev, "codes"),
          _dev_ptr(scales, torch.float32, dev, "scales"))
 

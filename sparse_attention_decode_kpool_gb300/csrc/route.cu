@@ -8,15 +8,14 @@
 //
 // One warp per row; expert e is lane e % 32's piece e / 32. Rows are few or short (a
 // thousand bytes), so latency and instructions bound it, not memory: the best expert of
-// a round is two warp reductions (the largest key, then the lowest id that has it), and
-// only the lane that held it looks for its next best.
+// a round is one warp reduction and a vote over the lanes' best, each lane's pieces sorted.
 //
 // The choice is the one that 64-bit arithmetic makes. It is first made in f32; every c
-// computed so is within err of the exact one (err below), so where the smallest chosen
-// and the largest rejected value (of experts, or of groups) are further apart than the
-// errors of both, the f32 choice is final. Else, about one row in a thousand for
-// unrelated scores, the warp repeats the row in f64. (f64 throughout would take about 30
-// times the arithmetic on this part's few FP64 units.)
+// computed so is within err of the exact one, so where the smallest chosen and the largest
+// rejected value (of experts, or of groups) are further apart than the errors of both, the
+// f32 choice is final. Else, about one row in a thousand for unrelated scores, those that are
+// not are compared in f64, or where it is the groups that are in doubt the whole row repeated.
+// (f64 throughout would take some 30 times the arithmetic on this part's few FP64 units.)
 #include "common.cuh"
 
 namespace dsa {
@@ -32,6 +31,8 @@ struct RouteArgs {
     float* weights;
     long long ld;
     int rows, n, groups, gsize, topk_group, group_top, topk, shared;
+    int per_log;      // log2 of the lanes that scan a group: 32 / groups, rounded down
+    uint32_t gmagic;  // 2^32 / gsize, rounded up; 0 for 1
     int softmax, renorm;
     float scale;
 };
@@ -66,122 +67,58 @@ __device__ __forceinline__ T warp_sum_t(T v) {
     return v;
 }
 
-// One row in T's arithmetic. logit[] holds the lane's pieces (-inf past the last expert).
-// Gives the chosen pieces (bit i of `taken`), their scores s[] and whether the row holds a
-// NaN; returns false when T is float and the choice, or the renormalising sum, is not
-// certain. buf: the warp's staging area, 33 T per piece.
-template <typename T, int NPL>
-__device__ bool choose(const RouteArgs& a, const float (&logit)[NPL], int lane, T* buf, T (&s)[NPL],
-                       uint32_t& taken, bool& nan) {
+// e / a.gsize for e < 2^10.
+__device__ __forceinline__ int group_of(const RouteArgs& a, int e) {
+    return a.gmagic ? (int)__umulhi((uint32_t)e, a.gmagic) : e;
+}
+
+// The best two of each group's values, from the warp's staging area (value e at e + e / 32): 32 / groups lanes, rounded down to a power of two, scan one group. Lane g * per of
+// group g then has its score, the other lanes -inf. Returns the mask of the topk_group best
+// groups; *gap: by how much the worst of them leads the best other (inf if there is none).
+template <typename T>
+__device__ __forceinline__ uint32_t best_groups(const RouteArgs& a, const T* buf, int lane, T* gap) {
     const T NI = neg_inf<T>();
-    T c[NPL];
-    bool bad = false;
-    T top = NI;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        T z = (T)logit[i];
-        if (!(z == z) || (a.softmax && z > (T)3.4028235e38)) {
-            bad = true;
-            z = NI;
-        }
-        s[i] = z;
-        top = z > top ? z : top;
-    }
-    top = warp_max_t(top);
-    T sum = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const T z = s[i];
-        c[i] = z;  // the logit, until its score is known
-        if (a.softmax) {
-            s[i] = z > NI ? exp_t(z - top) : (T)0;
-            sum += s[i];
-        } else {
-            s[i] = z > NI ? (T)1 / ((T)1 + exp_t(-z)) : (T)0;
+    const int per = 1 << a.per_log, g = lane >> a.per_log, j0 = lane & (per - 1);
+    T b1 = NI, b2 = NI;
+    if (g < a.groups) {
+        const int first = g * a.gsize;
+        for (int e = first + j0; e < first + a.gsize; e += per) {
+            const T v = buf[e + (e >> 5)];
+            b2 = v > b1 ? b1 : (v > b2 ? v : b2);
+            b1 = v > b1 ? v : b1;
         }
     }
-    if (a.softmax) {
-        sum = warp_sum_t(sum);
-        const T inv = sum > 0 ? (T)1 / sum : (T)0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] *= inv;
+    for (int o = per >> 1; o > 0; o >>= 1) {
+        const T o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
+        const T lo = o1 > b1 ? b1 : o1;
+        b1 = o1 > b1 ? o1 : b1;
+        b2 = b2 > o2 ? b2 : o2;
+        b2 = lo > b2 ? lo : b2;
     }
-    T smax = 0, bmax = 0;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        T b = 0;
-        if (a.bias && e < a.n) b = (T)__ldg(a.bias + e);
-        if (!(b == b)) {
-            bad = true;
-            c[i] = NI;
-        }
-        const bool cand = e < a.n && c[i] > NI;
-        smax = cand && s[i] > smax ? s[i] : smax;
-        const T ab = b < 0 ? -b : b;
-        bmax = cand && ab > bmax && ab < (T)1e30 ? ab : bmax;
-        c[i] = cand ? s[i] + b : NI;
+    T score = b1;
+    if (a.group_top == 2 && b2 > NI) score += b2;
+    if (g >= a.groups || j0 != 0) score = NI;
+    uint32_t kept = 0;
+    T low = 0;
+    for (int k = 0; k < a.topk_group; ++k) {
+        const T m = warp_max_t(score);
+        if (!(m > NI)) break;
+        const int at = __ffs(__ballot_sync(kAll, score == m)) - 1;  // the lowest group of equal ones
+        kept |= 1u << (at >> a.per_log);
+        if (lane == at) score = NI;
+        low = m;
     }
-    nan = __any_sync(kAll, bad);
-    // |computed c - exact c|: the score's few roundings (2^-19 of the largest leaves room
-    // for the softmax's sum) and the bias's addition.
-    T err = 0;
-    if constexpr (sizeof(T) == 4)
-        err = 1.9073486e-6f * warp_max_t(smax) + 1.2e-7f * warp_max_t(bmax) + 1e-37f;
-    bool sure = true;
+    const T next = warp_max_t(score);
+    *gap = next > NI ? low - next : -NI;
+    return kept;
+}
 
-    if (a.groups > 1) {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) buf[33 * i + lane] = c[i];
-        __syncwarp();
-        // 32 / groups (rounded down to a power of two) lanes scan one group
-        int per = 32;
-        while (per * a.groups > 32) per >>= 1;
-        const int g = lane / per, j0 = lane % per;
-        T b1 = NI, b2 = NI;
-        if (g < a.groups) {
-            for (int j = j0; j < a.gsize; j += per) {
-                const int e = g * a.gsize + j;
-                const T v = buf[33 * (e >> 5) + (e & 31)];
-                b2 = v > b1 ? b1 : (v > b2 ? v : b2);
-                b1 = v > b1 ? v : b1;
-            }
-        }
-        for (int o = per >> 1; o > 0; o >>= 1) {
-            const T o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-            const T lo = o1 > b1 ? b1 : o1;
-            b1 = o1 > b1 ? o1 : b1;
-            b2 = b2 > o2 ? b2 : o2;
-            b2 = lo > b2 ? lo : b2;
-        }
-        T score = b1;
-        if (a.group_top == 2 && b2 > NI) score += b2;
-        const bool lead = g < a.groups && j0 == 0;
-        if (!lead) score = NI;
-        uint32_t kept = 0;
-        T low = 0;
-        for (int k = 0; k < a.topk_group; ++k) {
-            const T m = warp_max_t((kept >> g) & 1u ? NI : score);
-            if (!(m > NI)) break;
-            const int id = (int)__reduce_min_sync(
-                kAll, lead && !((kept >> g) & 1u) && score == m ? (uint32_t)g : 64u);
-            kept |= 1u << id;
-            low = m;
-        }
-        if constexpr (sizeof(T) == 4) {
-            const T next = warp_max_t((kept >> g) & 1u ? NI : score);
-            if (next > NI && !(low - next > 4 * err)) sure = false;
-        }
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.n && !((kept >> (e / a.gsize)) & 1u)) c[i] = NI;
-        }
-    }
-
-    // the topk best, one after the other
-    taken = 0;
+// The topk largest c, ties to the lowest expert; bit i of the result: the lane's piece i is
+// chosen. *gap: by how much the worst chosen leads the best other.
+template <typename T, int NPL>
+__device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c)[NPL], int lane, T* gap) {
+    const T NI = neg_inf<T>();
+    uint32_t taken = 0;
     T best = NI;
     int at = 0;
 #pragma unroll
@@ -194,9 +131,12 @@ __device__ bool choose(const RouteArgs& a, const float (&logit)[NPL], int lane, 
     for (int k = 0; k < a.topk; ++k) {
         const T m = warp_max_t(best);
         if (!(m > NI)) break;
-        const uint32_t id = __reduce_min_sync(kAll, best == m ? (uint32_t)(lane + 32 * at) : 0xffffffffu);
+        const uint32_t who = __ballot_sync(kAll, best == m);
+        bool mine = best == m;
+        if (who & (who - 1))  // several lanes: the lowest expert
+            mine = mine && __reduce_min_sync(who, (uint32_t)(lane + 32 * at)) == (uint32_t)(lane + 32 * at);
         low = m;
-        if ((id & 31u) == (uint32_t)lane) {
+        if (mine) {
             taken |= 1u << at;
             best = NI;
 #pragma unroll
@@ -207,72 +147,302 @@ __device__ bool choose(const RouteArgs& a, const float (&logit)[NPL], int lane, 
                 }
         }
     }
-    if constexpr (sizeof(T) == 4) {
-        const T next = warp_max_t(best);
-        if (next > NI && !(low - next > 2 * err)) sure = false;
-    }
-    return sure;
+    const T next = warp_max_t(best);
+    *gap = next > NI ? low - next : -NI;
+    return taken;
 }
 
+// The same in f32, for values that are certain: each lane sorts its pieces' keys (the value's
+// order, its last log2(NPL) bits replaced by the piece, the lower the larger; 0 for none) into
+// its column of `list`, and a round takes the largest head. *low: the worst chosen value,
+// *next: the best other (-inf if none), both cut down to a multiple of NPL ulps.
 template <int NPL>
-__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
-    __shared__ double stage[kRouteWarps][33 * NPL];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long r = (long long)blockIdx.x * kRouteWarps + warp;
-    pdl_wait();
-    if (r >= a.rows) return;
+__device__ __forceinline__ uint32_t best_keys(const RouteArgs& a, const float (&c)[NPL], int lane, uint32_t* list,
+                                              float* low, float* next) {
+    constexpr uint32_t kPiece = NPL - 1;
+    uint32_t k[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) k[i] = c[i] > neg_inf<float>() ? (key_of(c[i]) & ~kPiece) | (kPiece - i) : 0u;
+    // Batcher's odd-even merge sort, largest first
+#pragma unroll
+    for (int p = 1; p < NPL; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < NPL; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < NPL && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(k[i + j], k[i + j + q]);
+                        k[i + j + q] = min(k[i + j], k[i + j + q]);
+                        k[i + j] = hi;
+                    }
+#pragma unroll
+    for (int i = 1; i < NPL; ++i) list[32 * i + lane] = k[i];
+    __syncwarp();
+    uint32_t head = k[0], taken = 0, worst = 0;
+    int at = 0;
+    for (int round = 0; round < a.topk; ++round) {
+        const uint32_t m = __reduce_max_sync(kAll, head);
+        if (m == 0) break;
+        worst = m;
+        const uint32_t who = __ballot_sync(kAll, head == m);
+        const bool mine = lane == __ffs(who) - 1;  // (of equal keys any: the gap is 0 then, or both are chosen)
+        const uint32_t then = at + 1 < NPL ? list[32 * (at + 1) + lane] : 0u;
+        taken |= mine ? 1u << (kPiece - (head & kPiece)) : 0u;
+        at += mine;
+        head = mine ? then : head;
+    }
+    const uint32_t other = __reduce_max_sync(kAll, head);
+    *low = worst ? of_key(worst & ~kPiece) : neg_inf<float>();
+    *next = other ? of_key(other & ~kPiece) : neg_inf<float>();
+    return taken;
+}
+
+// The best `most` of the pieces in `doubt` by their c in f64 (of softmax scores, which all
+// have the same factor, without it: there is no bias then).
+__device__ __noinline__ uint32_t choose_f64(const RouteArgs& a, long long r, int lane, float top, uint32_t doubt,
+                                            int most) {
     const float* row = a.logits + r * a.ld;
-    float logit[NPL], s[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        logit[i] = e < a.n ? __ldg(row + e) : neg_inf<float>();
-    }
-    uint32_t taken;
-    bool nan;
-    bool sure = choose<float, NPL>(a, logit, lane, reinterpret_cast<float*>(stage[warp]), s, taken, nan);
-    float total = 0.f;
-    bool tiny = false;  // near f32's smallest: digits are lost that a ratio of scores needs
-#pragma unroll
-    for (int i = 0; i < NPL; ++i)
-        if ((taken >> i) & 1u) {
-            total += s[i];
-            tiny |= s[i] < 1e-30f;
+    uint32_t taken = 0;
+    for (int round = 0; round < most; ++round) {
+        double best = neg_inf<double>();
+        int at = 0;
+        for (uint32_t left = doubt & ~taken; left; left &= left - 1) {
+            const int i = __ffs(left) - 1, e = lane + 32 * i;
+            const double z = (double)__ldg(row + e);
+            double v = a.softmax ? exp(z - (double)top) : 1 / (1 + exp(-z));
+            if (a.bias) v += (double)__ldg(a.bias + e);
+            if (v > best) {
+                best = v;
+                at = i;
+            }
         }
-    total = warp_sum_t(total);
-    if (!sure || (a.renorm && __any_sync(kAll, tiny))) {
-        double sd[NPL], td = 0;
-        choose<double, NPL>(a, logit, lane, stage[warp], sd, taken, nan);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if ((taken >> i) & 1u) td += sd[i];
-        td = warp_sum_t(td);
-        const double inv = a.renorm ? (td > 0 ? 1.0 / td : 0.0) : 1.0;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = (float)(sd[i] * inv);
-        total = 1.f;
+        const double m = warp_max_t(best);
+        const uint32_t who = __ballot_sync(kAll, best == m && best > neg_inf<double>());
+        if (!who) break;
+        if ((who >> lane) & 1u)
+            if (__reduce_min_sync(who, (uint32_t)(lane + 32 * at)) == (uint32_t)(lane + 32 * at)) taken |= 1u << at;
+        __syncwarp();
     }
-    const float f = a.renorm ? (total > 0.f ? a.scale / total : 0.f) : a.scale;
+    return taken;
+}
+
+// The chosen experts' scores and the row's outputs, in ascending expert id; then padding and
+// shared experts. Lane k takes the k-th chosen one; T: what the scores are computed in. In f32
+// it gives up (false) where a ratio of scores needs digits that numbers near its smallest lack.
+template <typename T, int NPL>
+__device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, uint32_t taken, T top, T inv, bool nan,
+                                     int* chosen) {
     const int width = a.topk + a.shared;
     int32_t* ids = a.ids + r * width;
     float* weights = a.weights + r * width;
+    const float* row = a.logits + r * a.ld;
     int n = 0;
+    __syncwarp();  // the staging area is free
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const bool mine = (taken >> i) & 1u;
         const uint32_t who = __ballot_sync(kAll, mine);
-        if (mine) {
-            const int at = n + __popc(who & ((1u << lane) - 1u));
-            ids[at] = lane + 32 * i;
-            weights[at] = nan ? __uint_as_float(0x7fc00000u) : s[i] * f;
-        }
+        if (mine) chosen[n + __popc(who & ((1u << lane) - 1u))] = lane + 32 * i;
         n += __popc(who);
+    }
+    __syncwarp();
+    T s[(DSA_MAX_TOPK + 31) / 32], total = 0;
+    bool tiny = false;
+#pragma unroll
+    for (int q = 0; q < (DSA_MAX_TOPK + 31) / 32; ++q) {
+        s[q] = 0;
+        if (lane + 32 * q < n) {
+            const T z = (T)__ldg(row + chosen[lane + 32 * q]);
+            s[q] = a.softmax ? exp_t(z - top) * inv : (T)1 / ((T)1 + exp_t(-z));
+            tiny |= s[q] < (T)1e-30;
+        }
+        total += s[q];
+    }
+    if (sizeof(T) == 4 && a.renorm && __any_sync(kAll, tiny)) return false;
+    T f = (T)a.scale;
+    if (a.renorm) {
+        total = warp_sum_t(total);
+        f = total > 0 ? f / total : (T)0;
+    }
+#pragma unroll
+    for (int q = 0; q < (DSA_MAX_TOPK + 31) / 32; ++q) {
+        const int k = lane + 32 * q;
+        if (k < n) {
+            ids[k] = chosen[k];
+            weights[k] = nan ? __uint_as_float(0x7fc00000u) : (float)(s[q] * f);
+        }
     }
     for (int k = n + lane; k < width; k += 32) {
         const bool extra = k >= a.topk;
         ids[k] = extra ? a.n + (k - a.topk) : -1;
         weights[k] = extra ? 1.f : 0.f;
     }
+    return true;
+}
+
+// A row in f64 throughout. A function of its own, seldom called: its registers and
+// instructions stay out of the rows that f32 decides.
+template <int NPL>
+__device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, int lane, double* buf) {
+    const double NI = neg_inf<double>();
+    const float* row = a.logits + r * a.ld;
+    double s[NPL], c[NPL], top = NI;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        double z = e < a.n ? (double)__ldg(row + e) : NI;
+        if (!(z == z) || (a.softmax && z > 3.5e38)) {
+            bad = true;
+            z = NI;
+        }
+        c[i] = z;  // the logit, until its score is known
+        top = z > top ? z : top;
+    }
+    top = warp_max_t(top);
+    double sum = 0, inv = 1;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        s[i] = 0;
+        if (c[i] > NI) s[i] = a.softmax ? exp(c[i] - top) : 1 / (1 + exp(-c[i]));
+        sum += s[i];
+    }
+    if (a.softmax) {
+        sum = warp_sum_t(sum);
+        inv = sum > 0 ? 1 / sum : 0;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] *= inv;
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        const double b = a.bias && e < a.n ? (double)__ldg(a.bias + e) : 0;
+        if (!(b == b)) {
+            bad = true;
+            c[i] = NI;
+        }
+        c[i] = c[i] > NI ? s[i] + b : NI;
+    }
+    const bool nan = __any_sync(kAll, bad);
+    double gap;
+    if (a.groups > 1) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) buf[33 * i + lane] = c[i];
+        __syncwarp();
+        const uint32_t kept = best_groups(a, buf, lane, &gap);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.n && !((kept >> group_of(a, e)) & 1u)) c[i] = NI;
+        }
+    }
+    const uint32_t taken = best_experts(a, c, lane, &gap);
+    emit<double, NPL>(a, r, lane, taken, top, inv, nan, reinterpret_cast<int*>(buf));
+}
+
+template <int NPL>
+__global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
+    __shared__ __align__(8) unsigned char stage[kRouteWarps][33 * NPL * sizeof(double)];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long r = (long long)blockIdx.x * kRouteWarps + warp;
+    pdl_wait();
+    if (r >= a.rows) return;
+    const float NI = neg_inf<float>();
+    const float* row = a.logits + r * a.ld;
+    float z[NPL], s[NPL], c[NPL];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const int e = lane + 32 * i;
+        z[i] = e < a.n ? __ldg(row + e) : NI;
+    }
+    float top = NI;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        if (!(z[i] == z[i]) || (a.softmax && z[i] > 3.4028235e38f)) {
+            bad = true;
+            z[i] = NI;
+        }
+        top = fmaxf(top, z[i]);
+    }
+    // Scores by the special-function unit's exponential and division, for the choice: within
+    // 2^-21 of the largest of them, the softmax's common factor within 2^-18 of itself.
+    float inv = 1.f;
+    if (a.softmax) {
+        top = warp_max_t(top);
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            s[i] = z[i] > NI ? __expf(z[i] - top) : 0.f;
+            sum += s[i];
+        }
+        sum = warp_sum_t(sum);
+        inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] *= inv;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-z[i]));
+    }
+    float smax = 0.f, bmax = 0.f;
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        smax = fmaxf(smax, s[i]);
+        c[i] = z[i] > NI ? s[i] : NI;
+    }
+    if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            const float b = e < a.n ? __ldg(a.bias + e) : 0.f;
+            bad |= !(b == b);
+            const float sum = c[i] + b;
+            c[i] = c[i] > NI && b == b ? sum : NI;
+            const float m = fabsf(b);
+            bmax = m < 1e30f ? fmaxf(bmax, m) : bmax;  // (larger ones make no close call)
+        }
+        bmax = warp_max_t(bmax);
+    }
+    const bool nan = __any_sync(kAll, bad);
+    // |c as computed - c|: the score's error (but for the softmax's common factor, which moves no
+    // score past another) and the addition's
+    const float err = (a.softmax && a.bias ? 3.8146973e-6f : 4.7683716e-7f) * warp_max_t(smax) + 1.2e-7f * bmax + 1e-37f;
+    bool sure = true;
+    if (a.groups > 1) {
+        float* buf = reinterpret_cast<float*>(stage[warp]);
+        float gap;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) buf[33 * i + lane] = c[i];
+        __syncwarp();
+        const uint32_t kept = best_groups(a, buf, lane, &gap);
+        sure = gap > 4 * err;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = lane + 32 * i;
+            if (e < a.n && !((kept >> group_of(a, e)) & 1u)) c[i] = NI;
+        }
+        __syncwarp();
+    }
+    float low, next;
+    uint32_t taken = best_keys(a, c, lane, reinterpret_cast<uint32_t*>(stage[warp]), &low, &next);
+    // two errors, and what the keys cut off
+    const float margin = 2 * err + (fabsf(low) + fabsf(next)) * (NPL * 1.1920929e-7f);
+    if (sure && next > NI && !(low - next > margin)) {
+        sure = !(a.softmax && a.bias) && fabsf(low) < 1e30f;
+        if (sure) {  // only what lies that near to the border is in doubt
+            uint32_t doubt = 0;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i)
+                if ((taken >> i) & 1u ? c[i] <= next + margin : c[i] > NI && c[i] >= low - margin) doubt |= 1u << i;
+            const int most = (int)__reduce_add_sync(kAll, (uint32_t)__popc(taken & doubt));
+            taken = (taken & ~doubt) | choose_f64(a, r, lane, top, doubt, most);
+        }
+    }
+    if (!sure || !emit<float, NPL>(a, r, lane, taken, top, inv, nan, reinterpret_cast<int*>(stage[warp])))
+        route_row_f64<NPL>(a, r, lane, reinterpret_cast<double*>(stage[warp]));
 }
 
 }  // namespace
@@ -318,6 +488,9 @@ extern "C" int dsa_route(const float* logits, int rows, int n_experts, long long
     a.n = n_experts;
     a.groups = n_group;
     a.gsize = n_experts / n_group;
+    a.gmagic = a.gsize > 1 ? (uint32_t)(0xffffffffu / (uint32_t)a.gsize + 1) : 0u;
+    a.per_log = 5;
+    while ((n_group << a.per_log) > 32) --a.per_log;
     a.topk_group = topk_group;
     a.group_top = group_top;
     a.topk = topk;

@@ -221,7 +221,8 @@ ROUTE = [
     (33, 320, 10, "sigmoid", False, 32, 9, 1, True, 0),
     (21, 1000, 64, "sigmoid", True, 5, 5, 2, True, 0),
     (9, 1024, 1, "softmax", True, 32, 1, 2, False, 0),
-    (50, 66, 2, "sigmoid", True, 33 - 11, 1, 1, True, 0),
+    (50, 66, 2, "sigmoid", True, 22, 1, 1, True, 0),
+    (20, 16, 3, "sigmoid", True, 16, 5, 1, True, 0),
 ]
 
 # The scores, in roundings of 2^-24: an exponential 4 (two units in the last place), its argument

@@ -106,7 +106,7 @@ def test_binding_checks_shapes():
     w = torch.zeros(256, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="weight"):
         api.dsa_rmsnorm(x, w[:128], 1e-6, x)
-    with pytest.raises(ValueError, match="out must be"):
+    with pytest.raises(ValueError, match="out, residual"):
         api.dsa_rmsnorm(x, w, 1e-6, x[:2])
     with pytest.raises(ValueError, match="codes"):
         api.dsa_rmsnorm(x, w, 1e-6, x, codes=torch.zeros(4, 256, dtype=torch.uint8),
@@ -140,7 +140,7 @@ def test_experts_refusals(lib):
     need = ctypes.c_size_t(0)
     assert lib.dsa_experts_workspace(8, 2, 4, 256, 128, 0, ctypes.byref(need)) == DSA_OK
     bf16_bytes = need.value
-    assert bf16_bytes >= 16 * (256 * 4 + 128 * 2)
+    assert bf16_bytes >= 16 * (256 * 2 + 128 * 2)
     assert lib.dsa_experts_workspace(8, 2, 4, 256, 128, 1, ctypes.byref(need)) == DSA_OK
     assert lib.dsa_experts_workspace(8, 2, 4, 256, 128, 0, None) == DSA_ERR_INVALID_ARG
 

@@ -591,68 +591,72 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
     } else if (F8 && warp >= kSfWarp) {
         // ---------------- scales ----------------
         // The rows' scales along K are contiguous: eight threads take a chunk's eight stages
-        // of one row, a chunk ahead of its use, and store the bytes where the MMA warp's
-        // copies to tensor memory read them.
+        // of one row, a chunk ahead of its use (the next item's first behind this one's last),
+        // and store the bytes where the MMA warp's copies to tensor memory read them.
         const int t = threadIdx.x - 32 * kSfWarp, sub = t >> 3, sst = t & 7;
         constexpr int NB = N / 16;
-        int chunk = 0;
-        bool ok = true;
-        if constexpr (!UP) pdl_wait();
-        for (int w = w0; w < items && ok; w += wstep) {
+        const long long ks = a.nst;  // scales per row: one per stage
+        const long long da = UP ? (long long)a.inter * ks : 16 * ks;
+        const float* bsrc = UP ? a.x_scales : reinterpret_cast<const float*>(a.h_scales);
+        const float* pa = nullptr;
+        uint32_t pb[NB];
+        auto rows_of = [&](int w) {  // row sub + 16 k of the item's tiles
             const Item it = item_of<N>(a, tab, start, w);
             int mt = kPair ? 2 * it.m + (int)rank : it.m;
             if (!UP && mt * 128 >= a.hidden) mt = 0;  // the tile too many: any scales
-            const long long ks = a.nst;  // scales per row: one per stage
-            // row sub + 16 i of the tile
-            const float* pa = a.a_scales + (UP ? (long long)it.e * 2 * a.inter + mt * 64 + sub
-                                               : (long long)it.e * a.hidden + mt * 128 + sub) * ks + sst;
-            const long long da = UP ? (long long)a.inter * ks : 16 * ks;
-            uint32_t pb[NB];
+            pa = a.a_scales + (UP ? (long long)it.e * 2 * a.inter + mt * 64 + sub
+                                  : (long long)it.e * a.hidden + mt * 128 + sub) * ks + sst;
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const int p = it.pos + (sub + 16 * k < it.n ? sub + 16 * k : 0);
                 pb[k] = (uint32_t)(UP ? a.pair_of[p] / a.topk : p);
             }
-            const float* bsrc = UP ? a.x_scales : reinterpret_cast<const float*>(a.h_scales);
-            uint32_t va[8], vb[NB];
-            auto load = [&](int st0) {
-                const bool in = st0 + sst < a.nst;
+        };
+        uint32_t va[8], vb[NB];
+        auto load = [&](int st0) {
+            const bool in = st0 + sst < a.nst;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float* src = UP ? pa + (k >> 2) * da + (k & 3) * 16 * ks : pa + k * da;
-                    va[k] = in ? __float_as_uint(__ldg(src + st0)) : 0u;
-                }
-#pragma unroll
-                for (int k = 0; k < NB; ++k) vb[k] = in ? __float_as_uint(bsrc[pb[k] * ks + st0 + sst]) : 0u;
-            };
-            load(0);
-            for (int st0 = 0; st0 < a.nst; st0 += kSfStages, ++chunk) {
-                int go = 1;
-                if (lane == 0)
-                    go = wait_or_abort(sf_empty + (chunk & 1), (uint32_t)(((chunk >> 1) & 1) ^ 1), abort_flag, a.status);
-                go = __shfl_sync(0xffffffffu, go, 0);
-                if (!go) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* buf = smem + L::SF + (chunk & 1) * L::SFBUF;
-                // row sub + 16 k: word [sub + 16 (k % 2)][k / 2 % 4] of block k / 8
-                uint8_t* to = buf + (sst >> 2) * kSfBlock + sub * 16 + (sst & 3);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) to[(k & 1) * 256 + (k >> 1) * 4] = (uint8_t)(va[k] >> 23);
-#pragma unroll
-                for (int k = 0; k < NB; ++k) {
-                    const uint32_t at = (k >> 3) * kSfBlock + (k & 1) * 256 + ((k >> 1) & 3) * 4;
-                    if constexpr (UP)
-                        buf[L::SF_B + (sst >> 2) * L::SFN * kSfBlock + sub * 16 + (sst & 3) + at] = (uint8_t)(vb[k] >> 23);
-                    else
-                        *reinterpret_cast<uint32_t*>(buf + L::SF_B + sst * L::SFN * kSfBlock + sub * 16 + at) = vb[k];
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_leader(sf_full + (chunk & 1));
-                if (st0 + kSfStages < a.nst) load(st0 + kSfStages);
+            for (int k = 0; k < 8; ++k) {
+                const float* src = UP ? pa + (k >> 2) * da + (k & 3) * 16 * ks : pa + k * da;
+                va[k] = in ? __float_as_uint(__ldg(src + st0)) : 0u;
             }
+#pragma unroll
+            for (int k = 0; k < NB; ++k) vb[k] = in ? __float_as_uint(bsrc[pb[k] * ks + st0 + sst]) : 0u;
+        };
+        if constexpr (!UP) pdl_wait();
+        int w = w0, st0 = 0;
+        if (w < items) {
+            rows_of(w);
+            load(0);
+        }
+        for (int chunk = 0; w < items; ++chunk) {
+            int go = 1;
+            if (lane == 0)
+                go = wait_or_abort(sf_empty + (chunk & 1), (uint32_t)(((chunk >> 1) & 1) ^ 1), abort_flag, a.status);
+            if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            uint8_t* buf = smem + L::SF + (chunk & 1) * L::SFBUF;
+            // row sub + 16 k: word [sub + 16 (k % 2)][k / 2 % 4] of block k / 8
+            uint8_t* to = buf + (sst >> 2) * kSfBlock + sub * 16 + (sst & 3);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) to[(k & 1) * 256 + (k >> 1) * 4] = (uint8_t)(va[k] >> 23);
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const uint32_t at = (k >> 3) * kSfBlock + (k & 1) * 256 + ((k >> 1) & 3) * 4;
+                if constexpr (UP)
+                    buf[L::SF_B + (sst >> 2) * L::SFN * kSfBlock + sub * 16 + (sst & 3) + at] = (uint8_t)(vb[k] >> 23);
+                else
+                    *reinterpret_cast<uint32_t*>(buf + L::SF_B + sst * L::SFN * kSfBlock + sub * 16 + at) = vb[k];
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_leader(sf_full + (chunk & 1));
+            st0 += kSfStages;
+            if (st0 >= a.nst) {
+                st0 = 0;
+                w += wstep;
+                if (w < items) rows_of(w);
+            }
+            if (w < items) load(st0);
         }
     }
     __syncthreads();
@@ -673,6 +677,7 @@ __global__ void __launch_bounds__(1024) dispatch_kernel(const int32_t* __restric
                                                         int32_t* counts, int32_t* starts, int32_t* pair_of,
                                                         int32_t* status) {
     __shared__ int eq_w[32], lt_w[32];
+    pdl_trigger();  // the products' blocks set themselves up meanwhile
     pdl_wait();
     const int e = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int per = (int)(((long long)pairs + 32 * warps - 1) / (32 * warps)) * 32;
@@ -787,11 +792,15 @@ __global__ void __launch_bounds__(kSumThreads) combine_kernel(const uint16_t* __
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Pairs per tile: what an expert gets on average. Fewer leave more of the ring to the weights
-// in flight; an expert with more pairs takes several tiles.
+// Pairs per tile, by what an expert gets on average (its tiles are cut to its own count, so a
+// larger one costs shared memory for weights in flight rather than work). Measured with 64
+// experts of 4,096 x 1,024, bf16, some more popular than others: 12 pairs each 271 us at 16 a
+// tile, 257 at 32, 253 at 64; 20: 287 at 32, 258 at 64; 40: 278 at 64, 276 at 128, 281 at 256;
+// 56: 293, 283, 287; 104: 326 at 128, 311 at 256. FP8: 56: 183 at 64, 169 at 128, 179 at 224;
+// 104: 202 and 203; 130: 229 and 221.
 int tile_of(long long pairs, int n_experts, bool f8) {
     const long long mean = (pairs + n_experts - 1) / n_experts;
-    return mean <= 8 ? 16 : mean <= 24 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : f8 ? 224 : 256;
+    return mean <= 8 ? 16 : mean <= 14 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : f8 ? 224 : 256;
 }
 
 struct Plan {

@@ -26,7 +26,8 @@ class DsaDecodeLayer:
                  score_path: str = "auto", fuse_expand: bool = True, decode_from=None,
                  fuse_append: bool = True, latent_fp8: bool = False, frontend=None,
                  l2_prefetch_bytes: Optional[int] = None, latent_fp4: bool = False,
-                 fp4_exp: Optional[int] = None, manage_pages: bool = False):
+                 fp4_exp: Optional[int] = None, manage_pages: bool = False, experts=None,
+                 experts_fp8: bool = False):
         if manage_pages and not fuse_append:
             # of the three calls the store cannot see whether the pooled key's page is shared
             raise ValueError("managed pages are appended to by dsa_decode_append only "
@@ -182,6 +183,11 @@ class DsaDecodeLayer:
         self.fe = None
         if frontend is not None:
             self._init_frontend(frontend)
+        # The other half of the layer (dsa_rmsnorm, dsa_route, dsa_experts): the residual
+        # stream, its two norms, the router and the experts, in bf16 or FP8.
+        self.ex = None
+        if experts is not None:
+            self._init_experts(experts, bool(experts_fp8))
 
     # -- pages -------------------------------------------------------------
     def _init_pages(self) -> None:
@@ -299,11 +305,82 @@ class DsaDecodeLayer:
 
     def layer_step(self, stream=None) -> None:
         """The whole decode layer: front-end, the token's append (when the layer was
-        built with decode_from), then the step."""
+        built with decode_from), then the step; with experts the layer's input norm before
+        and its mlp() behind them."""
+        if self.ex is not None:
+            self.attn_input(stream)
         self.frontend(stream)
         if self.decode_from is not None:
             self.append(stream)
         self.step(stream)
+        if self.ex is not None:
+            self.mlp(stream)
+
+    # -- the other half of the layer ---------------------------------------
+    def _init_experts(self, ex, fp8: bool) -> None:
+        g, dev, R = self.geom, self.device, self.wl.rows
+        if self.y is None:
+            raise ValueError("the experts take the projected output (with_o_absorb=True)")
+        if tuple(ex.stream.shape) != (R, g.hidden):
+            raise ValueError(f"the experts' stream must be [{R}, {g.hidden}]")
+        up = lambda t: None if t is None else t.to(dev).contiguous()
+        n, H, I = int(ex.w2.shape[0]), g.hidden, ex.inter
+        self.ex, self.experts_fp8 = ex, fp8
+        # The residual stream (updated in place) and what the layer before adds to it, this
+        # layer's own output after a step: chained layers share the one and pass the other on.
+        self.resid = up(ex.stream)
+        self.mlp_out = torch.zeros((R, H), dtype=torch.bfloat16, device=dev)
+        self.attn_norm, self.mlp_norm = up(ex.attn_norm), up(ex.mlp_norm)
+        self.w_router, self.route_bias = up(ex.padded_router()), up(ex.bias)
+        self.w13, self.w2 = up(ex.w13), up(ex.w2)
+        self.mlp_x = torch.zeros((R, H), dtype=torch.bfloat16, device=dev)
+        self.mlp_codes = self.mlp_scales = self.w13_scales = self.w2_scales = None
+        if fp8:
+            def encode(w):
+                codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
+                scales = torch.empty(w.shape[:-1] + (w.shape[-1] // 128,), dtype=torch.float32,
+                                     device=dev)
+                api.dsa_quantize_latent(w, codes, scales)
+                return codes, scales
+            (self.w13, self.w13_scales), (self.w2, self.w2_scales) = encode(self.w13), encode(self.w2)
+            self.mlp_codes = torch.zeros((R, H), dtype=torch.uint8, device=dev)
+            self.mlp_scales = torch.zeros((R, H // 128), dtype=torch.float32, device=dev)
+        self.logits = torch.zeros((R, int(self.w_router.shape[0])), dtype=torch.float32, device=dev)
+        k = ex.topk + ex.shared
+        self.expert_ids = torch.zeros((R, k), dtype=torch.int32, device=dev)
+        self.expert_weights = torch.zeros((R, k), dtype=torch.float32, device=dev)
+        nl = api.dsa_router_logits_workspace(R, H, int(self.w_router.shape[0]))
+        ne = api.dsa_experts_workspace(R, k, n, H, I, fp8)
+        self.logits_workspace = torch.zeros(max(nl, 1), dtype=torch.uint8, device=dev)
+        self.experts_workspace = torch.zeros(max(ne, 1), dtype=torch.uint8, device=dev)
+
+    def attn_input(self, stream=None) -> None:
+        """resid += mlp_out (what the layer before added); x = its norm, the front-end's input."""
+        if self.fe is None:
+            raise ValueError("the layer was not built with a front-end")
+        api.dsa_rmsnorm(self.mlp_out, self.attn_norm, self.ex.eps, self.x, residual=self.resid,
+                        residual_out=self.resid, stream=stream)
+
+    def mlp(self, stream=None) -> None:
+        """resid += y; mlp_out = the experts' output for its norm."""
+        if self.ex is None:
+            raise ValueError("the layer was not built with experts")
+        self._mlp_from(self.resid, stream)
+
+    def _mlp_from(self, residual_out, stream=None) -> None:
+        ex = self.ex
+        api.dsa_rmsnorm(self.y, self.mlp_norm, ex.eps, self.mlp_x, residual=self.resid,
+                        residual_out=residual_out, codes=self.mlp_codes, scales=self.mlp_scales,
+                        stream=stream)
+        api.dsa_router_logits(self.mlp_x, self.w_router, self.logits, self.status,
+                              self.logits_workspace, stream=stream)
+        api.dsa_route(self.logits, ex.topk, self.expert_ids, self.expert_weights, ex.n_experts,
+                      ex.score, self.route_bias, ex.n_group, ex.topk_group, scale=ex.scale,
+                      shared=ex.shared, stream=stream)
+        api.dsa_experts(self.mlp_codes if self.experts_fp8 else self.mlp_x, self.expert_ids,
+                        self.expert_weights, self.w13, self.w2, self.mlp_out, self.mlp_scales,
+                        self.w13_scales, self.w2_scales, self.status, self.experts_workspace,
+                        stream=stream)
 
     def _carve(self, device, pinned: bool, names: bool = True) -> torch.Tensor:
         """One byte buffer holding the step inputs at 256-byte aligned offsets; on the
@@ -606,6 +683,10 @@ class DsaDecodeLayer:
         with torch.cuda.stream(s):
             self.frontend()
             self.step()
+            if self.ex is not None:  # (the stream and the layer's output as they were)
+                before = self.mlp_out.clone()
+                self._mlp_from(None)
+                self.mlp_out.copy_(before)
         torch.cuda.current_stream(self.device).wait_stream(s)
         torch.cuda.synchronize(self.device)
         gr = torch.cuda.CUDAGraph()
@@ -616,8 +697,17 @@ class DsaDecodeLayer:
 
     def launches_per_layer_step(self) -> int:
         """Library kernel launches one layer_step() makes: the front-end's two GEMMs
-        with their reductions and the norm kernel, the append, the step."""
+        with their reductions and the norm kernel, the append, the step, the experts' half."""
         n = 5 + self.launches_per_step()
+        if self.ex is not None:
+            # two norms, the logits, the route; the experts' dispatch, products and sums, and
+            # for more than 14 pairs an expert the copy of x in their order
+            R, nr = self.wl.rows, int(self.w_router.shape[0])
+            tc = (api.dsa_get_option(api._lib.DSA_OPT_PROJECT_KERNEL)
+                  != api._lib.DSA_PROJECT_KERNEL_MMA and nr % 128 == 0
+                  and self.geom.hidden % 512 == 0)
+            pairs, experts = self.expert_ids.numel(), int(self.w2.shape[0])
+            n += 3 + (R + 63) // 64 + (0 if tc else 1) + 4 + (1 if pairs > 14 * experts else 0)
         return n + (0 if self.decode_from is None else self._append_launches())
 
     def launches_per_append_step(self) -> int:

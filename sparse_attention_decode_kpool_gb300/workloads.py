@@ -42,6 +42,7 @@ _T_QIDX, _T_W, _T_QLAT, _T_CKV, _T_OABS, _T_LENS, _T_PERM = 7, 8, 9, 10, 11, 12,
 _T_KPOOL = 14
 _T_FX, _T_FQA, _T_FKVA, _T_FWK, _T_FGATE, _T_FWP, _T_FQN, _T_FKVN, _T_FQABS, _T_FWQB = (
     20, 21, 22, 23, 24, 25, 26, 27, 28, 29)
+_T_EAN, _T_EMN, _T_EWR, _T_EB, _T_EW13, _T_EW2, _T_ESTREAM = 40, 41, 42, 43, 44, 45, 46
 
 
 def _rng(seed: int, tensor: int, seq: int = 0, chunk: Optional[int] = None) -> np.random.Generator:
@@ -422,6 +423,57 @@ def make_frontend(g: "Geometry", rows: int, q_lora_rank: int = 1536, seed: int =
         wq_b=mat(_T_FWQB, hi * ihd, q_lora_rank, q_lora_rank ** -0.5),
         eps=eps,
     )
+
+
+@dataclasses.dataclass
+class Experts:
+    """The other half of a decoder layer: its two norms, the router and the experts (the
+    routed ones, then the shared ones that every row takes)."""
+
+    stream: torch.Tensor     # [R, hidden] bf16: the residual stream the layer is given
+    attn_norm: torch.Tensor  # [hidden] bf16, before the front-end
+    mlp_norm: torch.Tensor   # [hidden] bf16, before the router
+    router: torch.Tensor     # [n_experts, hidden] bf16
+    bias: Optional[torch.Tensor]  # [n_experts] f32, for balance
+    w13: torch.Tensor        # [n_experts + shared, 2 * inter, hidden] bf16
+    w2: torch.Tensor         # [n_experts + shared, hidden, inter] bf16
+    topk: int
+    n_group: int
+    topk_group: int
+    scale: float
+    shared: int
+    eps: float
+    score: str = "sigmoid"
+
+    @property
+    def n_experts(self) -> int:
+        return int(self.router.shape[0])
+
+    @property
+    def inter(self) -> int:
+        return int(self.w2.shape[2])
+
+    def padded_router(self) -> torch.Tensor:
+        """The router's rows, then zero rows up to a multiple of 64."""
+        pad = (-self.n_experts) % 64
+        zeros = torch.zeros((pad, self.router.shape[1]), dtype=torch.bfloat16)
+        return torch.cat([self.router, zeros], dim=0).contiguous()
+
+
+def make_experts(g: "Geometry", rows: int, n_experts: int, topk: int, inter: int, seed: int = 0,
+                 n_group: int = 1, topk_group: int = 1, shared: int = 1, scale: float = 2.5,
+                 eps: float = 1e-6) -> Experts:
+    hidden, n = g.hidden, n_experts + shared
+    mat = lambda t, *s, std: _normal_bf16(seed, t, 0, math.prod(s), 0.0, std).view(*s)
+    return Experts(
+        stream=mat(_T_ESTREAM, rows, hidden, std=1.0),
+        attn_norm=_normal_bf16(seed, _T_EAN, 0, hidden, 1.0, 0.1),
+        mlp_norm=_normal_bf16(seed, _T_EMN, 0, hidden, 1.0, 0.1),
+        router=mat(_T_EWR, n_experts, hidden, std=hidden ** -0.5),
+        bias=torch.from_numpy(_normal_f32(_rng(seed, _T_EB), (n_experts,), 0.0, 0.05)),
+        w13=mat(_T_EW13, n, 2 * inter, hidden, std=hidden ** -0.5),
+        w2=mat(_T_EW2, n, hidden, inter, std=inter ** -0.5),
+        topk=topk, n_group=n_group, topk_group=topk_group, scale=scale, shared=shared, eps=eps)
 
 
 # ---------------------------------------------------------------------------

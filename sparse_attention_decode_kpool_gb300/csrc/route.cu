@@ -13,9 +13,10 @@
 // The choice is the one that 64-bit arithmetic makes. It is first made in f32; every c
 // computed so is within err of the exact one, so where the smallest chosen and the largest
 // rejected value (of experts, or of groups) are further apart than the errors of both, the
-// f32 choice is final. Else, about one row in a thousand for unrelated scores, those that are
-// not are compared in f64, or where it is the groups that are in doubt the whole row repeated.
-// (f64 throughout would take some 30 times the arithmetic on this part's few FP64 units.)
+// f32 choice is final. Else, about one row in a thousand for unrelated scores, what is not is
+// compared in f64; a softmax with a bias, whose common factor matters, repeats the whole row.
+// (A whole row in f64 takes about 20 us on this part's few FP64 units, longer than 30,000 rows
+// in f32: it was the tail that a batch waited for.)
 #include "common.cuh"
 
 namespace dsa {
@@ -55,10 +56,30 @@ __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 __device__ __forceinline__ float warp_max_t(float v) { return of_key(__reduce_max_sync(kAll, key_of(v))); }
+// (By integers: this part's FP64 units are few, a comparison there takes as long as dozens here.)
 __device__ __forceinline__ double warp_max_t(double v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
-    return v;
+    unsigned long long b = (unsigned long long)__double_as_longlong(v + 0.0);
+    b ^= (b >> 63) ? ~0ull : 1ull << 63;
+    const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(b >> 32));
+    const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(b >> 32) == hi ? (uint32_t)b : 0u);
+    b = (unsigned long long)hi << 32 | lo;
+    b ^= (b >> 63) ? 1ull << 63 : ~0ull;
+    return __longlong_as_double((long long)b);
+}
+__device__ __forceinline__ float max_t(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float min_t(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double max_t(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double min_t(double a, double b) { return fmin(a, b); }
+// 2^x and 1 / x on the special-function unit, subnormals taken as zero.
+__device__ __forceinline__ float ex2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 template <typename T>
 __device__ __forceinline__ T warp_sum_t(T v) {
@@ -73,10 +94,11 @@ __device__ __forceinline__ int group_of(const RouteArgs& a, int e) {
 }
 
 // The best two of each group's values, from the warp's staging area (value e at e + e / 32): 32 / groups lanes, rounded down to a power of two, scan one group. Lane g * per of
-// group g then has its score, the other lanes -inf. Returns the mask of the topk_group best
-// groups; *gap: by how much the worst of them leads the best other (inf if there is none).
+// group g has its score in *own and the smallest value in it in *least, the other lanes -inf.
+// Returns the mask of the `most` best groups; *low: the worst of them, *next: the best other.
 template <typename T>
-__device__ __forceinline__ uint32_t best_groups(const RouteArgs& a, const T* buf, int lane, T* gap) {
+__device__ __forceinline__ uint32_t best_groups(const RouteArgs& a, const T* buf, int lane, int most, T* own, T* least,
+                                                T* low, T* next) {
     const T NI = neg_inf<T>();
     const int per = 1 << a.per_log, g = lane >> a.per_log, j0 = lane & (per - 1);
     T b1 = NI, b2 = NI;
@@ -84,39 +106,38 @@ __device__ __forceinline__ uint32_t best_groups(const RouteArgs& a, const T* buf
         const int first = g * a.gsize;
         for (int e = first + j0; e < first + a.gsize; e += per) {
             const T v = buf[e + (e >> 5)];
-            b2 = v > b1 ? b1 : (v > b2 ? v : b2);
-            b1 = v > b1 ? v : b1;
+            b2 = max_t(b2, min_t(b1, v));
+            b1 = max_t(b1, v);
         }
     }
     for (int o = per >> 1; o > 0; o >>= 1) {
         const T o1 = __shfl_xor_sync(kAll, b1, o), o2 = __shfl_xor_sync(kAll, b2, o);
-        const T lo = o1 > b1 ? b1 : o1;
-        b1 = o1 > b1 ? o1 : b1;
-        b2 = b2 > o2 ? b2 : o2;
-        b2 = lo > b2 ? lo : b2;
+        b2 = max_t(max_t(b2, o2), min_t(b1, o1));
+        b1 = max_t(b1, o1);
     }
     T score = b1;
     if (a.group_top == 2 && b2 > NI) score += b2;
     if (g >= a.groups || j0 != 0) score = NI;
+    *own = score;
+    *least = a.group_top == 2 && b2 > NI ? b2 : b1;
     uint32_t kept = 0;
-    T low = 0;
-    for (int k = 0; k < a.topk_group; ++k) {
+    *low = NI;
+    for (int k = 0; k < most; ++k) {
         const T m = warp_max_t(score);
         if (!(m > NI)) break;
         const int at = __ffs(__ballot_sync(kAll, score == m)) - 1;  // the lowest group of equal ones
         kept |= 1u << (at >> a.per_log);
         if (lane == at) score = NI;
-        low = m;
+        *low = m;
     }
-    const T next = warp_max_t(score);
-    *gap = next > NI ? low - next : -NI;
+    *next = warp_max_t(score);
     return kept;
 }
 
 // The topk largest c, ties to the lowest expert; bit i of the result: the lane's piece i is
-// chosen. *gap: by how much the worst chosen leads the best other.
+// chosen.
 template <typename T, int NPL>
-__device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c)[NPL], int lane, T* gap) {
+__device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c)[NPL], int lane) {
     const T NI = neg_inf<T>();
     uint32_t taken = 0;
     T best = NI;
@@ -127,7 +148,6 @@ __device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c
             best = c[i];
             at = i;
         }
-    T low = 0;
     for (int k = 0; k < a.topk; ++k) {
         const T m = warp_max_t(best);
         if (!(m > NI)) break;
@@ -135,7 +155,6 @@ __device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c
         bool mine = best == m;
         if (who & (who - 1))  // several lanes: the lowest expert
             mine = mine && __reduce_min_sync(who, (uint32_t)(lane + 32 * at)) == (uint32_t)(lane + 32 * at);
-        low = m;
         if (mine) {
             taken |= 1u << at;
             best = NI;
@@ -147,18 +166,17 @@ __device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c
                 }
         }
     }
-    const T next = warp_max_t(best);
-    *gap = next > NI ? low - next : -NI;
     return taken;
 }
 
 // The same in f32, for values that are certain: each lane sorts its pieces' keys (the value's
 // order, its last log2(NPL) bits replaced by the piece, the lower the larger; 0 for none) into
 // its column of `list`, and a round takes the largest head. *low: the worst chosen value,
-// *next: the best other (-inf if none), both cut down to a multiple of NPL ulps.
+// *next: the best other (-inf if none), both cut down to a multiple of NPL ulps. Lane j gets
+// the j-th chosen expert in *mine_id (of the first 32; no expert: unchanged), all *count.
 template <int NPL>
 __device__ __forceinline__ uint32_t best_keys(const RouteArgs& a, const float (&c)[NPL], int lane, uint32_t* list,
-                                              float* low, float* next) {
+                                              float* low, float* next, int* mine_id, int* count) {
     constexpr uint32_t kPiece = NPL - 1;
     uint32_t k[NPL];
 #pragma unroll
@@ -181,38 +199,46 @@ __device__ __forceinline__ uint32_t best_keys(const RouteArgs& a, const float (&
     for (int i = 1; i < NPL; ++i) list[32 * i + lane] = k[i];
     __syncwarp();
     uint32_t head = k[0], taken = 0, worst = 0;
-    int at = 0;
-    for (int round = 0; round < a.topk; ++round) {
+    int at = 0, round = 0;
+    for (; round < a.topk; ++round) {
         const uint32_t m = __reduce_max_sync(kAll, head);
         if (m == 0) break;
         worst = m;
         const uint32_t who = __ballot_sync(kAll, head == m);
-        const bool mine = lane == __ffs(who) - 1;  // (of equal keys any: the gap is 0 then, or both are chosen)
+        const int winner = __ffs(who) - 1;  // (of equal keys any: the gap is 0 then, or both are chosen)
+        const uint32_t piece = kPiece - (m & kPiece);
+        const bool mine = lane == winner;
         const uint32_t then = at + 1 < NPL ? list[32 * (at + 1) + lane] : 0u;
-        taken |= mine ? 1u << (kPiece - (head & kPiece)) : 0u;
+        taken |= mine ? 1u << piece : 0u;
+        *mine_id = lane == round ? winner + 32 * (int)piece : *mine_id;
         at += mine;
         head = mine ? then : head;
     }
+    *count = round;
     const uint32_t other = __reduce_max_sync(kAll, head);
     *low = worst ? of_key(worst & ~kPiece) : neg_inf<float>();
     *next = other ? of_key(other & ~kPiece) : neg_inf<float>();
     return taken;
 }
 
-// The best `most` of the pieces in `doubt` by their c in f64 (of softmax scores, which all
-// have the same factor, without it: there is no bias then).
+// c of expert e in f64 (a softmax score without the factor that all have: there is no bias then).
+__device__ __forceinline__ double value_f64(const RouteArgs& a, long long r, float top, int e) {
+    const double z = (double)__ldg(a.logits + r * a.ld + e);
+    double v = a.softmax ? exp(z - (double)top) : 1 / (1 + exp(-z));
+    if (a.bias) v += (double)__ldg(a.bias + e);
+    return v;
+}
+
+// The best `most` of the pieces in `doubt`.
 __device__ __noinline__ uint32_t choose_f64(const RouteArgs& a, long long r, int lane, float top, uint32_t doubt,
                                             int most) {
-    const float* row = a.logits + r * a.ld;
     uint32_t taken = 0;
     for (int round = 0; round < most; ++round) {
         double best = neg_inf<double>();
         int at = 0;
         for (uint32_t left = doubt & ~taken; left; left &= left - 1) {
-            const int i = __ffs(left) - 1, e = lane + 32 * i;
-            const double z = (double)__ldg(row + e);
-            double v = a.softmax ? exp(z - (double)top) : 1 / (1 + exp(-z));
-            if (a.bias) v += (double)__ldg(a.bias + e);
+            const int i = __ffs(left) - 1;
+            const double v = value_f64(a, r, top, lane + 32 * i);
             if (v > best) {
                 best = v;
                 at = i;
@@ -228,24 +254,44 @@ __device__ __noinline__ uint32_t choose_f64(const RouteArgs& a, long long r, int
     return taken;
 }
 
-// The chosen experts' scores and the row's outputs, in ascending expert id; then padding and
-// shared experts. Lane k takes the k-th chosen one; T: what the scores are computed in. In f32
+// The best `most` of the groups in doubt, of which the pieces `needed` hold all that may be in
+// their sums.
+__device__ __noinline__ uint32_t choose_groups_f64(const RouteArgs& a, long long r, int lane, float top, uint32_t needed,
+                                                   int pieces, int most, double* buf) {
+    __syncwarp();
+    for (int i = 0; i < pieces; ++i)
+        buf[33 * i + lane] = (needed >> i) & 1u ? value_f64(a, r, top, lane + 32 * i) : neg_inf<double>();
+    __syncwarp();
+    double own, least, low, next;
+    return best_groups(a, buf, lane, most, &own, &least, &low, &next);
+}
+
+// The chosen experts (count >= 0 of them, lane j's in mine_id; else by the bits of `taken`),
+// their scores and the row's outputs in ascending expert id; then padding and shared experts.
+// Lane k takes the k-th chosen one; T: what the scores are computed in. In f32
 // it gives up (false) where a ratio of scores needs digits that numbers near its smallest lack.
 template <typename T, int NPL>
-__device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, uint32_t taken, T top, T inv, bool nan,
-                                     int* chosen) {
+__device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, uint32_t taken, int count, int mine_id,
+                                     T top, T inv, bool nan, int* chosen) {
     const int width = a.topk + a.shared;
     int32_t* ids = a.ids + r * width;
     float* weights = a.weights + r * width;
     const float* row = a.logits + r * a.ld;
-    int n = 0;
+    int n = count;
     __syncwarp();  // the staging area is free
+    if (n >= 0) {  // at most 32, one a lane, in any order: each to the place of its rank
+        int rank = 0;
+        for (int j = 0; j < n; ++j) rank += __shfl_sync(kAll, mine_id, j) < mine_id;
+        if (lane < n) chosen[rank] = mine_id;
+    } else {
+        n = 0;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const bool mine = (taken >> i) & 1u;
-        const uint32_t who = __ballot_sync(kAll, mine);
-        if (mine) chosen[n + __popc(who & ((1u << lane) - 1u))] = lane + 32 * i;
-        n += __popc(who);
+        for (int i = 0; i < NPL; ++i) {
+            const bool mine = (taken >> i) & 1u;
+            const uint32_t who = __ballot_sync(kAll, mine);
+            if (mine) chosen[n + __popc(who & ((1u << lane) - 1u))] = lane + 32 * i;
+            n += __popc(who);
+        }
     }
     __syncwarp();
     T s[(DSA_MAX_TOPK + 31) / 32], total = 0;
@@ -326,123 +372,147 @@ __device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, int 
         c[i] = c[i] > NI ? s[i] + b : NI;
     }
     const bool nan = __any_sync(kAll, bad);
-    double gap;
     if (a.groups > 1) {
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < NPL; ++i) buf[33 * i + lane] = c[i];
         __syncwarp();
-        const uint32_t kept = best_groups(a, buf, lane, &gap);
+        double own, least, low, next;
+        const uint32_t kept = best_groups(a, buf, lane, a.topk_group, &own, &least, &low, &next);
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = lane + 32 * i;
             if (e < a.n && !((kept >> group_of(a, e)) & 1u)) c[i] = NI;
         }
     }
-    const uint32_t taken = best_experts(a, c, lane, &gap);
-    emit<double, NPL>(a, r, lane, taken, top, inv, nan, reinterpret_cast<int*>(buf));
+    const uint32_t taken = best_experts(a, c, lane);
+    emit<double, NPL>(a, r, lane, taken, -1, 0, top, inv, nan, reinterpret_cast<int*>(buf));
 }
 
-template <int NPL>
+template <int NPL, bool SOFTMAX>
 __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
     __shared__ __align__(8) unsigned char stage[kRouteWarps][33 * NPL * sizeof(double)];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long r = (long long)blockIdx.x * kRouteWarps + warp;
-    pdl_wait();
-    if (r >= a.rows) return;
     const float NI = neg_inf<float>();
-    const float* row = a.logits + r * a.ld;
-    float z[NPL], s[NPL], c[NPL];
-    bool bad = false;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 32 * i;
-        z[i] = e < a.n ? __ldg(row + e) : NI;
-    }
-    float top = NI;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        if (!(z[i] == z[i]) || (a.softmax && z[i] > 3.4028235e38f)) {
-            bad = true;
-            z[i] = NI;
-        }
-        top = fmaxf(top, z[i]);
-    }
-    // Scores by the special-function unit's exponential and division, for the choice: within
-    // 2^-21 of the largest of them, the softmax's common factor within 2^-18 of itself.
-    float inv = 1.f;
-    if (a.softmax) {
-        top = warp_max_t(top);
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            s[i] = z[i] > NI ? __expf(z[i] - top) : 0.f;
-            sum += s[i];
-        }
-        sum = warp_sum_t(sum);
-        inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] *= inv;
-    } else {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) s[i] = __fdividef(1.f, 1.f + __expf(-z[i]));
-    }
-    float smax = 0.f, bmax = 0.f;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        smax = fmaxf(smax, s[i]);
-        c[i] = z[i] > NI ? s[i] : NI;
-    }
-    if (a.bias) {
+    pdl_wait();
+    const long long r = (long long)blockIdx.x * kRouteWarps + warp;
+    if (r >= a.rows) return;
+    {
+        float z[NPL], c[NPL];
+        bool bad = false;
+        float top = NI, inv = 1.f, smax = 0.f, bmax = 0.f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             const int e = lane + 32 * i;
-            const float b = e < a.n ? __ldg(a.bias + e) : 0.f;
-            bad |= !(b == b);
-            const float sum = c[i] + b;
-            c[i] = c[i] > NI && b == b ? sum : NI;
-            const float m = fabsf(b);
-            bmax = m < 1e30f ? fmaxf(bmax, m) : bmax;  // (larger ones make no close call)
+            z[i] = e < a.n ? __ldg(a.logits + r * a.ld + e) : NI;
         }
-        bmax = warp_max_t(bmax);
-    }
-    const bool nan = __any_sync(kAll, bad);
-    // |c as computed - c|: the score's error (but for the softmax's common factor, which moves no
-    // score past another) and the addition's
-    const float err = (a.softmax && a.bias ? 3.8146973e-6f : 4.7683716e-7f) * warp_max_t(smax) + 1.2e-7f * bmax + 1e-37f;
-    bool sure = true;
-    if (a.groups > 1) {
-        float* buf = reinterpret_cast<float*>(stage[warp]);
-        float gap;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) buf[33 * i + lane] = c[i];
-        __syncwarp();
-        const uint32_t kept = best_groups(a, buf, lane, &gap);
-        sure = gap > 4 * err;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            const int e = lane + 32 * i;
-            if (e < a.n && !((kept >> group_of(a, e)) & 1u)) c[i] = NI;
+            const bool odd = SOFTMAX ? !(z[i] < __uint_as_float(0x7f800000u)) : !(z[i] == z[i]);
+            bad |= odd;
+            z[i] = odd ? NI : z[i];
+            if (SOFTMAX) top = fmaxf(top, z[i]);
+        }
+        // Scores by the special-function unit, for the choice: within 2^-21 of the largest of them,
+        // the softmax's common factor within 2^-18 of itself.
+        constexpr float kLog2e = 1.4426950408889634f;
+        if (SOFTMAX) {
+            top = warp_max_t(top);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                c[i] = z[i] > NI ? ex2_fast((z[i] - top) * kLog2e) : 0.f;
+                sum += c[i];
+            }
+            sum = warp_sum_t(sum);
+            inv = sum > 0.f ? 1.f / sum : 0.f;
+            smax = inv;  // the largest logit's
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const float s = SOFTMAX ? c[i] * inv : rcp_fast(1.f + ex2_fast(z[i] * -kLog2e));
+            if (!SOFTMAX) smax = fmaxf(smax, s);
+            c[i] = z[i] > NI ? s : NI;
+        }
+        if (!SOFTMAX) smax = warp_max_t(smax);
+        if (a.bias) {
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int e = lane + 32 * i;
+                const float b = e < a.n ? __ldg(a.bias + e) : 0.f;
+                bad |= !(b == b);
+                c[i] = c[i] > NI && b == b ? c[i] + b : NI;
+                const float m = fabsf(b);
+                bmax = m < 1e30f ? fmaxf(bmax, m) : bmax;  // (larger ones make no close call)
+            }
+            bmax = warp_max_t(bmax);
+        }
+        const bool nan = __any_sync(kAll, bad);
+        // |c as computed - c|: the score's error (but for the softmax's common factor, which moves
+        // no score past another) and the addition's
+        const float err = (SOFTMAX && a.bias ? 3.8146973e-6f : 4.7683716e-7f) * smax + 1.2e-7f * bmax + 1e-37f;
+        bool sure = true;
+        if (a.groups > 1) {
+            float* buf = reinterpret_cast<float*>(stage[warp]);
+            float own, least, low, next;
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) buf[33 * i + lane] = c[i];
+            __syncwarp();
+            uint32_t kept = best_groups(a, buf, lane, a.topk_group, &own, &least, &low, &next);
+            if (next > NI && !(low - next > 4 * err)) {
+                sure = !(SOFTMAX && a.bias) && fabsf(low) < 1e30f;
+                if (sure) {  // the groups near the border, by what may be in their sums
+                    const int g = lane >> a.per_log;
+                    const bool near = own > NI && ((kept >> g) & 1u ? own <= next + 4 * err : own >= low - 4 * err);
+                    const uint32_t doubt = __reduce_or_sync(kAll, near ? 1u << g : 0u);
+                    uint32_t needed = 0;
+#pragma unroll
+                    for (int i = 0; i < NPL; ++i) {
+                        const int e = lane + 32 * i, h = e < a.n ? group_of(a, e) : 0;
+                        const float from = __shfl_sync(kAll, least, h << a.per_log) - 2 * err;
+                        if (e < a.n && ((doubt >> h) & 1u) && c[i] > NI && c[i] >= from) needed |= 1u << i;
+                    }
+                    kept = (kept & ~doubt) | choose_groups_f64(a, r, lane, top, needed, NPL, __popc(kept & doubt),
+                                                               reinterpret_cast<double*>(stage[warp]));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) {
+                const int e = lane + 32 * i;
+                if (e < a.n && !((kept >> group_of(a, e)) & 1u)) c[i] = NI;
+            }
         }
         __syncwarp();
-    }
-    float low, next;
-    uint32_t taken = best_keys(a, c, lane, reinterpret_cast<uint32_t*>(stage[warp]), &low, &next);
-    // two errors, and what the keys cut off
-    const float margin = 2 * err + (fabsf(low) + fabsf(next)) * (NPL * 1.1920929e-7f);
-    if (sure && next > NI && !(low - next > margin)) {
-        sure = !(a.softmax && a.bias) && fabsf(low) < 1e30f;
-        if (sure) {  // only what lies that near to the border is in doubt
-            uint32_t doubt = 0;
+        float low, next;
+        int mine_id = 0, count = 0;
+        uint32_t taken = best_keys(a, c, lane, reinterpret_cast<uint32_t*>(stage[warp]), &low, &next, &mine_id, &count);
+        if (a.topk > 32) count = -1;
+        // two errors, and what the keys cut off
+        const float margin = 2 * err + (fabsf(low) + fabsf(next)) * (NPL * 1.1920929e-7f);
+        if (sure && next > NI && !(low - next > margin)) {
+            sure = !(SOFTMAX && a.bias) && fabsf(low) < 1e30f;
+            if (sure) {  // only what lies that near to the border is in doubt
+                uint32_t doubt = 0;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                if ((taken >> i) & 1u ? c[i] <= next + margin : c[i] > NI && c[i] >= low - margin) doubt |= 1u << i;
-            const int most = (int)__reduce_add_sync(kAll, (uint32_t)__popc(taken & doubt));
-            taken = (taken & ~doubt) | choose_f64(a, r, lane, top, doubt, most);
+                for (int i = 0; i < NPL; ++i)
+                    if ((taken >> i) & 1u ? c[i] <= next + margin : c[i] > NI && c[i] >= low - margin) doubt |= 1u << i;
+                const int most = (int)__reduce_add_sync(kAll, (uint32_t)__popc(taken & doubt));
+                taken = (taken & ~doubt) | choose_f64(a, r, lane, top, doubt, most);
+                count = -1;
+            }
         }
+        if (!sure || !emit<float, NPL>(a, r, lane, taken, count, mine_id, top, inv, nan, reinterpret_cast<int*>(stage[warp])))
+            route_row_f64<NPL>(a, r, lane, reinterpret_cast<double*>(stage[warp]));
     }
-    if (!sure || !emit<float, NPL>(a, r, lane, taken, top, inv, nan, reinterpret_cast<int*>(stage[warp])))
-        route_row_f64<NPL>(a, r, lane, reinterpret_cast<double*>(stage[warp]));
+}
+
+template <int NPL>
+cudaError_t route_launch(const RouteArgs& a, cudaStream_t st) {
+    // (A warp for several rows, their biases looked up once, was slower: a row in doubt holds up
+    // those behind it.)
+    const dim3 grid((unsigned)((a.rows + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+    return a.softmax ? launch_pdl(route_kernel<NPL, true>, grid, block, 0, st, a)
+                     : launch_pdl(route_kernel<NPL, false>, grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -498,19 +568,18 @@ extern "C" int dsa_route(const float* logits, int rows, int n_experts, long long
     a.softmax = score == DSA_ROUTE_SOFTMAX;
     a.renorm = renorm != 0;
     a.scale = scale;
-    const dim3 grid((unsigned)((rows + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (n_experts <= 64)
-        e = launch_pdl(route_kernel<2>, grid, block, 0, st, a);
+        e = route_launch<2>(a, st);
     else if (n_experts <= 128)
-        e = launch_pdl(route_kernel<4>, grid, block, 0, st, a);
+        e = route_launch<4>(a, st);
     else if (n_experts <= 256)
-        e = launch_pdl(route_kernel<8>, grid, block, 0, st, a);
+        e = route_launch<8>(a, st);
     else if (n_experts <= 512)
-        e = launch_pdl(route_kernel<16>, grid, block, 0, st, a);
+        e = route_launch<16>(a, st);
     else
-        e = launch_pdl(route_kernel<32>, grid, block, 0, st, a);
+        e = route_launch<32>(a, st);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_route launch");
     return DSA_OK;

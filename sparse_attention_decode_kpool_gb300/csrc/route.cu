@@ -8,12 +8,12 @@
 //
 // One warp per row; expert e is lane e % 32's piece e / 32. Rows are few or short (a
 // thousand bytes), so latency and instructions bound it, not memory: the best expert of
-// a round is one warp reduction and a vote over the lanes' best, each lane's pieces sorted.
+// a round is one warp reduction over the lanes' best, each lane's pieces sorted.
 //
 // The choice is the one that 64-bit arithmetic makes. It is first made in f32; every c
 // computed so is within err of the exact one, so where the smallest chosen and the largest
 // rejected value (of experts, or of groups) are further apart than the errors of both, the
-// f32 choice is final. Else, about one row in a thousand for unrelated scores, what is not is
+// f32 choice is final. Else, one to two rows in a hundred for unrelated scores, what is not is
 // compared in f64; a softmax with a bias, whose common factor matters, repeats the whole row.
 // (A whole row in f64 takes about 20 us on this part's few FP64 units, longer than 30,000 rows
 // in f32: it was the tail that a batch waited for.)
@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kRouteWarps = 4;
 constexpr uint32_t kAll = 0xffffffffu;
+constexpr int kSets = (DSA_MAX_TOPK + 31) / 32;  // registers for one chosen expert per lane
 
 struct RouteArgs {
     const float* logits;
@@ -169,18 +170,23 @@ __device__ __forceinline__ uint32_t best_experts(const RouteArgs& a, const T (&c
     return taken;
 }
 
-// The same in f32, for values that are certain: each lane sorts its pieces' keys (the value's
-// order, its last log2(NPL) bits replaced by the piece, the lower the larger; 0 for none) into
-// its column of `list`, and a round takes the largest head. *low: the worst chosen value,
-// *next: the best other (-inf if none), both cut down to a multiple of NPL ulps. Lane j gets
-// the j-th chosen expert in *mine_id (of the first 32; no expert: unchanged), all *count.
+// The same in f32, for values that are certain: each lane sorts its pieces' keys into its column
+// of `list`, and a round takes the largest head. A key is the value's order, its last bits
+// replaced by the expert's number (piece and lane), the lower the larger; 0 for none. So keys
+// differ, and one reduction a round says all. Lane j gets the key of the j-th best in
+// mine[j / 32]. *low: the worst chosen value, *next: the best other (-inf if none), both cut
+// down to a multiple of 32 NPL ulps. Returns how many there are.
 template <int NPL>
-__device__ __forceinline__ uint32_t best_keys(const RouteArgs& a, const float (&c)[NPL], int lane, uint32_t* list,
-                                              float* low, float* next, int* mine_id, int* count) {
-    constexpr uint32_t kPiece = NPL - 1;
+__device__ __forceinline__ int best_keys(const RouteArgs& a, const float (&c)[NPL], int lane, uint32_t* list, float* low,
+                                         float* next, uint32_t (&mine)[kSets]) {
+    constexpr uint32_t kCut = 32 * NPL - 1;
     uint32_t k[NPL];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) k[i] = c[i] > neg_inf<float>() ? (key_of(c[i]) & ~kPiece) | (kPiece - i) : 0u;
+    for (int i = 0; i < NPL; ++i) {
+        const uint32_t b = __float_as_uint(c[i]);  // (a -0 sorts below +0: their gap is 0, a doubt)
+        const uint32_t o = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+        k[i] = c[i] > neg_inf<float>() ? (o & ~kCut) | (kCut - (uint32_t)(lane + 32 * i)) : 0u;
+    }
     // Batcher's odd-even merge sort, largest first
 #pragma unroll
     for (int p = 1; p < NPL; p <<= 1)
@@ -196,29 +202,31 @@ __device__ __forceinline__ uint32_t best_keys(const RouteArgs& a, const float (&
                         k[i + j] = hi;
                     }
 #pragma unroll
-    for (int i = 1; i < NPL; ++i) list[32 * i + lane] = k[i];
-    __syncwarp();
-    uint32_t head = k[0], taken = 0, worst = 0;
-    int at = 0, round = 0;
-    for (; round < a.topk; ++round) {
-        const uint32_t m = __reduce_max_sync(kAll, head);
-        if (m == 0) break;
-        worst = m;
-        const uint32_t who = __ballot_sync(kAll, head == m);
-        const int winner = __ffs(who) - 1;  // (of equal keys any: the gap is 0 then, or both are chosen)
-        const uint32_t piece = kPiece - (m & kPiece);
-        const bool mine = lane == winner;
-        const uint32_t then = at + 1 < NPL ? list[32 * (at + 1) + lane] : 0u;
-        taken |= mine ? 1u << piece : 0u;
-        *mine_id = lane == round ? winner + 32 * (int)piece : *mine_id;
-        at += mine;
-        head = mine ? then : head;
+    for (int i = 1; i < NPL; ++i) list[32 * (i - 1) + lane] = k[i];
+    list[32 * (NPL - 1) + lane] = 0u;
+    const uint32_t* then = list + lane;
+    uint32_t head = k[0], worst = 0;
+    int count = 0;
+#pragma unroll
+    for (int q = 0; q < kSets; ++q) {
+        mine[q] = 0;
+        const int rounds = min(32, a.topk - 32 * q);
+        for (int j = 0; j < rounds; ++j) {
+            const uint32_t m = __reduce_max_sync(kAll, head);
+            if (m == 0) break;
+            worst = m;
+            ++count;
+            mine[q] = lane == j ? m : mine[q];
+            if (head == m) {
+                head = *then;
+                then += 32;
+            }
+        }
     }
-    *count = round;
     const uint32_t other = __reduce_max_sync(kAll, head);
-    *low = worst ? of_key(worst & ~kPiece) : neg_inf<float>();
-    *next = other ? of_key(other & ~kPiece) : neg_inf<float>();
-    return taken;
+    *low = worst ? of_key(worst & ~kCut) : neg_inf<float>();
+    *next = other ? of_key(other & ~kCut) : neg_inf<float>();
+    return count;
 }
 
 // c of expert e in f64 (a softmax score without the factor that all have: there is no bias then).
@@ -266,38 +274,46 @@ __device__ __noinline__ uint32_t choose_groups_f64(const RouteArgs& a, long long
     return best_groups(a, buf, lane, most, &own, &least, &low, &next);
 }
 
-// The chosen experts (count >= 0 of them, lane j's in mine_id; else by the bits of `taken`),
+// The chosen experts (count >= 0 of them, by their keys; else by the bits of `taken`),
 // their scores and the row's outputs in ascending expert id; then padding and shared experts.
 // Lane k takes the k-th chosen one; T: what the scores are computed in. In f32
 // it gives up (false) where a ratio of scores needs digits that numbers near its smallest lack.
 template <typename T, int NPL>
-__device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, uint32_t taken, int count, int mine_id,
-                                     T top, T inv, bool nan, int* chosen) {
+__device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, uint32_t taken, int count,
+                                     const uint32_t (&mine)[kSets], T top, T inv, bool nan, int* chosen) {
     const int width = a.topk + a.shared;
     int32_t* ids = a.ids + r * width;
     float* weights = a.weights + r * width;
     const float* row = a.logits + r * a.ld;
     int n = count;
     __syncwarp();  // the staging area is free
-    if (n >= 0) {  // at most 32, one a lane, in any order: each to the place of its rank
-        int rank = 0;
-        for (int j = 0; j < n; ++j) rank += __shfl_sync(kAll, mine_id, j) < mine_id;
-        if (lane < n) chosen[rank] = mine_id;
+    if (n >= 0) {  // each to the place of its rank: the larger the number in the key, the earlier
+#pragma unroll
+        for (int q = 0; q < kSets; ++q) {
+            if (32 * q >= n) break;
+            const uint32_t number = mine[q] & (32 * NPL - 1);
+            int rank = 0;
+#pragma unroll
+            for (int p = 0; p < kSets; ++p)
+                for (int j = 0; j < min(32, n - 32 * p); ++j)
+                    rank += (__shfl_sync(kAll, mine[p], j) & (32 * NPL - 1)) > number;
+            if (lane + 32 * q < n) chosen[rank] = 32 * NPL - 1 - number;
+        }
     } else {
         n = 0;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            const bool mine = (taken >> i) & 1u;
-            const uint32_t who = __ballot_sync(kAll, mine);
-            if (mine) chosen[n + __popc(who & ((1u << lane) - 1u))] = lane + 32 * i;
+            const bool here = (taken >> i) & 1u;
+            const uint32_t who = __ballot_sync(kAll, here);
+            if (here) chosen[n + __popc(who & ((1u << lane) - 1u))] = lane + 32 * i;
             n += __popc(who);
         }
     }
     __syncwarp();
-    T s[(DSA_MAX_TOPK + 31) / 32], total = 0;
+    T s[kSets], total = 0;
     bool tiny = false;
 #pragma unroll
-    for (int q = 0; q < (DSA_MAX_TOPK + 31) / 32; ++q) {
+    for (int q = 0; q < kSets; ++q) {
         s[q] = 0;
         if (lane + 32 * q < n) {
             const T z = (T)__ldg(row + chosen[lane + 32 * q]);
@@ -313,7 +329,7 @@ __device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, 
         f = total > 0 ? f / total : (T)0;
     }
 #pragma unroll
-    for (int q = 0; q < (DSA_MAX_TOPK + 31) / 32; ++q) {
+    for (int q = 0; q < kSets; ++q) {
         const int k = lane + 32 * q;
         if (k < n) {
             ids[k] = chosen[k];
@@ -386,7 +402,8 @@ __device__ __noinline__ void route_row_f64(const RouteArgs& a, long long r, int 
         }
     }
     const uint32_t taken = best_experts(a, c, lane);
-    emit<double, NPL>(a, r, lane, taken, -1, 0, top, inv, nan, reinterpret_cast<int*>(buf));
+    const uint32_t none[kSets] = {};
+    emit<double, NPL>(a, r, lane, taken, -1, none, top, inv, nan, reinterpret_cast<int*>(buf));
 }
 
 template <int NPL, bool SOFTMAX>
@@ -484,14 +501,19 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
         }
         __syncwarp();
         float low, next;
-        int mine_id = 0, count = 0;
-        uint32_t taken = best_keys(a, c, lane, reinterpret_cast<uint32_t*>(stage[warp]), &low, &next, &mine_id, &count);
-        if (a.topk > 32) count = -1;
+        uint32_t mine[kSets], taken = 0;
+        int count = best_keys(a, c, lane, reinterpret_cast<uint32_t*>(stage[warp]), &low, &next, mine);
         // two errors, and what the keys cut off
-        const float margin = 2 * err + (fabsf(low) + fabsf(next)) * (NPL * 1.1920929e-7f);
+        const float margin = 2 * err + (fabsf(low) + fabsf(next)) * (32 * NPL * 1.1920929e-7f);
         if (sure && next > NI && !(low - next > margin)) {
             sure = !(SOFTMAX && a.bias) && fabsf(low) < 1e30f;
             if (sure) {  // only what lies that near to the border is in doubt
+#pragma unroll
+                for (int q = 0; q < kSets; ++q)
+                    for (int j = 0; j < min(32, count - 32 * q); ++j) {
+                        const int e = 32 * NPL - 1 - (int)(__shfl_sync(kAll, mine[q], j) & (32 * NPL - 1));
+                        taken |= (e & 31) == lane ? 1u << (e >> 5) : 0u;
+                    }
                 uint32_t doubt = 0;
 #pragma unroll
                 for (int i = 0; i < NPL; ++i)
@@ -501,7 +523,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
                 count = -1;
             }
         }
-        if (!sure || !emit<float, NPL>(a, r, lane, taken, count, mine_id, top, inv, nan, reinterpret_cast<int*>(stage[warp])))
+        if (!sure || !emit<float, NPL>(a, r, lane, taken, count, mine, top, inv, nan, reinterpret_cast<int*>(stage[warp])))
             route_row_f64<NPL>(a, r, lane, reinterpret_cast<double*>(stage[warp]));
     }
 }

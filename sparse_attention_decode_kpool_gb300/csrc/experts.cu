@@ -103,7 +103,7 @@ struct GemmArgs {
     uint8_t* h8;         // E4M3 [pairs, inter]
     uint8_t* h_scales;   // [pairs, inter / 32]
     // second product
-    uint16_t* part;     // f16 [pairs (row, j), hidden], under
+    uint16_t* part;     // f16 [pairs in their order, hidden], under
     uint8_t* part_exp;  // [pairs, hidden / 32] powers of two (biased)
     // FP8 scales
     const float* a_scales;  // weights, [E * rows, K / 128]
@@ -480,7 +480,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         // ---------------- accumulators ----------------
         // Two groups of four warps take a chunk of 16 columns (pairs) in turn: out of tensor
         // memory a chunk ahead, transposed through shared memory, a pair's channels to eight
-        // threads.
+        // threads. (The second product's straight from the registers, two bytes a lane, took
+        // half as long again: the stores are too many.)
         const int ew = warp & 3, eg = (warp - 4) >> 2, et = threadIdx.x & 127;
         float* stg0 = reinterpret_cast<float*>(smem + L::STG + eg * L::STG_BUFS * kStgBytes);
         const int p = et >> 3, seg = et & 7;  // pair of the chunk; 8 or 16 channels
@@ -488,8 +489,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         for (int w = w0; w < items; w += wstep, ++t) {
             const Item it = item_of<N>(a, tab, start, w);
             const int mt = kPair ? 2 * it.m + (int)rank : it.m;
-            auto pair_at = [&](int c0) { return a.pair_of[it.pos + (c0 + p < it.n ? c0 + p : 0)]; };
-            int pair = UP ? 0 : pair_at(kChunk * eg);
             int got = 1;
             if (lane == 0) got = wait_or_abort(acc_full + (t & 1), (uint32_t)((t >> 1) & 1), abort_flag, a.status);
             got = __shfl_sync(0xffffffffu, got, 0);
@@ -504,16 +503,13 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             }
             for (int c0 = kChunk * eg; c0 < it.n; c0 += 2 * kChunk, ++turn) {
                 const bool more = c0 + 2 * kChunk < it.n;
-                int next = 0;
-                if (more) {
-                    tc_ld16(nv, acc + c0 + 2 * kChunk);
-                    if (!UP) next = pair_at(c0 + 2 * kChunk);
-                }
+                if (more) tc_ld16(nv, acc + c0 + 2 * kChunk);
                 float* stg = stg0 + (L::STG_BUFS == 2 ? (turn & 1) * (kStgBytes / 4) : 0);
                 if (L::STG_BUFS == 1) group_sync(1 + eg);  // the staging is free
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c) stg[c * kStgLd + 36 * ew + lane] = __uint_as_float(v[c]);
                 group_sync(1 + eg);
+                const bool live = c0 + p < it.n;
                 if constexpr (UP) {
                     float f[8], u[8];
                     const float* from = stg + p * kStgLd + seg * 8 + 4 * (seg >> 2);
@@ -524,7 +520,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] = silu(f[j]) * u[j];
-                    const bool live = c0 + p < it.n;
                     const long long at = (long long)(it.pos + c0 + p) * a.inter + mt * 64 + seg * 8;
                     if constexpr (F8) {
                         float m = 0.f;
@@ -549,7 +544,6 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                     // A product is kept to 11 bits, as f16 under one power of two for 32 channels of a
                     // pair: 2^-12 of it at most, an eighth of what y's own rounding costs, and half
                     // the bytes of f32.
-                    const bool live = c0 + p < it.n && (!kPair || mt * 128 < a.hidden);  // (odd row tiles: one too many)
                     float f[16];
                     uint32_t top = 0;
 #pragma unroll
@@ -570,19 +564,18 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                         const __half2 h2 = __floats2half2_rn(f[2 * j] * inv, f[2 * j + 1] * inv);
                         o[j] = *reinterpret_cast<const uint32_t*>(&h2);
                     }
-                    if (live) {
-                        uint4* dst = reinterpret_cast<uint4*>(a.part + (long long)pair * a.hidden + mt * 128 + seg * 16);
+                    if (live && (!kPair || mt * 128 < a.hidden)) {  // (of an odd number of row tiles one too many)
+                        const long long row = it.pos + c0 + p;
+                        uint4* dst = reinterpret_cast<uint4*>(a.part + row * a.hidden + mt * 128 + seg * 16);
                         dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
                         dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                        if (!(seg & 1))
-                            a.part_exp[(long long)pair * (a.hidden >> 5) + mt * 4 + (seg >> 1)] = (uint8_t)e;
+                        if (!(seg & 1)) a.part_exp[row * (a.hidden >> 5) + mt * 4 + (seg >> 1)] = (uint8_t)e;
                     }
                 }
                 if (more) {
                     tc_wait_ld16(nv);
 #pragma unroll
                     for (int c = 0; c < kChunk; ++c) v[c] = nv[c];
-                    pair = next;
                 }
             }
             tc_fence_before();  // this warp's columns are in registers
@@ -671,11 +664,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 }
 
 // One block per expert: its pairs in ascending order behind those of the experts before it.
-// Each warp looks at one contiguous part of the ids twice: how many are its expert's (and,
+// place_of: where a pair is in that order. Each warp looks at one contiguous part of the ids twice: how many are its expert's (and,
 // over the block, how many belong to lower ones), then which.
 __global__ void __launch_bounds__(1024) dispatch_kernel(const int32_t* __restrict__ ids, int pairs, int n_experts,
                                                         int32_t* counts, int32_t* starts, int32_t* pair_of,
-                                                        int32_t* status) {
+                                                        int32_t* place_of, int32_t* status) {
     __shared__ int eq_w[32], lt_w[32];
     pdl_trigger();  // the products' blocks set themselves up meanwhile
     pdl_wait();
@@ -685,6 +678,7 @@ __global__ void __launch_bounds__(1024) dispatch_kernel(const int32_t* __restric
     const int lo = (int)(p0 < pairs ? p0 : pairs), hi = (int)(p0 + per < pairs ? p0 + per : pairs);
     int eq = 0, lt = 0;
     bool bad = false;
+#pragma unroll 8
     for (int p = lo + lane; p < hi; p += 32) {
         const int id = __ldg(ids + p);
         eq += id == e;
@@ -714,10 +708,15 @@ __global__ void __launch_bounds__(1024) dispatch_kernel(const int32_t* __restric
     }
     int at = base + before;
     if (eq == 0) return;
+#pragma unroll 4
     for (int p = lo; p < hi; p += 32) {
         const bool mine = p + lane < hi && __ldg(ids + p + lane) == e;
         const uint32_t who = __ballot_sync(0xffffffffu, mine);
-        if (mine) pair_of[at + __popc(who & ((1u << lane) - 1u))] = p + lane;
+        if (mine) {
+            const int place = at + __popc(who & ((1u << lane) - 1u));
+            pair_of[place] = p + lane;
+            place_of[p + lane] = place;
+        }
         at += __popc(who);
     }
 }
@@ -749,6 +748,7 @@ constexpr int kSumThreads = 256;
 __global__ void __launch_bounds__(kSumThreads) combine_kernel(const uint16_t* __restrict__ part,
                                                               const uint8_t* __restrict__ part_exp,
                                                               const int32_t* __restrict__ ids,
+                                                              const int32_t* __restrict__ place_of,
                                                               const float* __restrict__ weights, int rows,
                                                               int topk, int n_experts, int hidden,
                                                               uint16_t* __restrict__ y) {
@@ -769,8 +769,9 @@ __global__ void __launch_bounds__(kSumThreads) combine_kernel(const uint16_t* __
                 k[j] = 0.f;
                 q[j] = make_uint4(0, 0, 0, 0);
                 if (id >= 0 && id < n_experts) {
-                    q[j] = ldg16_stream(part + p * hidden + c * 8);
-                    k[j] = __uint_as_float((uint32_t)__ldg(part_exp + p * (hidden >> 5) + (c >> 2)) << 23);
+                    const long long at = __ldg(place_of + p);
+                    q[j] = ldg16_stream(part + at * hidden + c * 8);
+                    k[j] = __uint_as_float((uint32_t)__ldg(part_exp + at * (hidden >> 5) + (c >> 2)) << 23);
                     w[j] = __ldg(weights + p);
                 }
             }
@@ -804,7 +805,7 @@ int tile_of(long long pairs, int n_experts, bool f8) {
 }
 
 struct Plan {
-    size_t counts, starts, pair_of, x, h, h_scales, part, part_exp, bytes;
+    size_t counts, starts, pair_of, place_of, x, h, h_scales, part, part_exp, bytes;
 };
 Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     Plan p;
@@ -814,6 +815,8 @@ Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     p.starts = at;
     at += al256((size_t)n_experts * 4);
     p.pair_of = at;
+    at += al256((size_t)pairs * 4);
+    p.place_of = at;
     at += al256((size_t)pairs * 4);
     p.x = at;
     at += gathers(tile_of(pairs, n_experts, f8)) ? 0 : al256((size_t)pairs * hidden * (f8 ? 1 : 2));
@@ -969,9 +972,10 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     int32_t* counts = reinterpret_cast<int32_t*>(ws + p.counts);
     int32_t* starts = reinterpret_cast<int32_t*>(ws + p.starts);
     int32_t* pair_of = reinterpret_cast<int32_t*>(ws + p.pair_of);
+    int32_t* place_of = reinterpret_cast<int32_t*>(ws + p.place_of);
     const int threads = pairs >= 1024 ? 1024 : (pairs + 31) / 32 * 32;
     cudaError_t e = launch_pdl(dispatch_kernel, dim3((unsigned)n_experts), dim3((unsigned)threads), 0, st, ids, pairs,
-                               n_experts, counts, starts, pair_of, status);
+                               n_experts, counts, starts, pair_of, place_of, status);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_experts dispatch launch");
     GemmArgs a = {};
@@ -1017,7 +1021,7 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     long long blocks = (n + kSumThreads - 1) / kSumThreads;
     if (blocks > (long long)sms * 32) blocks = (long long)sms * 32;
     e = launch_pdl(combine_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, (const uint16_t*)a.part,
-                   (const uint8_t*)a.part_exp, ids, weights, rows, topk, n_experts, hidden, y);
+                   (const uint8_t*)a.part_exp, ids, (const int32_t*)place_of, weights, rows, topk, n_experts, hidden, y);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_experts combine launch");
     return DSA_OK;

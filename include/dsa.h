@@ -816,7 +816,7 @@ int dsa_frontend(const dsa_bf16* x, int rows, int hidden, const dsa_bf16* w_x, i
  * bf16; codes [rows, width] u8 and scales [rows, width / 128] f32 (both or neither). out is
  * nullable with codes. residual_out and out may each be x or residual itself; any other
  * overlap is refused. The squares are summed in f32: rows whose sum passes 3.4e38 give 0.
- * Limits: codes need width % 128 == 0.
+ * Limits: rows < 2^31; width <= 2^24; codes need width % 128 == 0.
  */
 int dsa_rmsnorm(const dsa_bf16* x, const dsa_bf16* residual, const dsa_bf16* weight,
                 long long rows, int width, float eps, dsa_bf16* residual_out, dsa_bf16* out,
@@ -881,7 +881,8 @@ int dsa_route(const float* logits, int rows, int n_experts, long long ld, int sc
  * with x_scales [rows, hidden / 128], w13_scales [n_experts, 2 inter, hidden / 128],
  * w2_scales [n_experts, hidden, inter / 128] f32, as dsa_quantize_latent or dsa_rmsnorm make
  * them: the scales are powers of two, and only their exponents are read. ids, weights [rows,
- * topk]; y [rows, hidden] bf16. Limits: hidden and inter multiples of 128; n_experts <=
+ * topk]; y [rows, hidden] bf16 (may be x). Limits: hidden and inter multiples of 128, at most
+ * 65536; n_experts <=
  * DSA_MAX_EXPERTS + DSA_MAX_TOPK; rows * topk <= 2^24; 16-byte aligned tensors (4 for scales, ids and
  * weights) and workspace. The workspace's contents need not be kept between calls; calls
  * that overlap in time need one each. `status` also gets DSA_STATUS_TIMEOUT if a wait inside

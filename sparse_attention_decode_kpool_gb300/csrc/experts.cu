@@ -26,9 +26,7 @@
 // memory in order with its MMAs. (Such a copy takes the tensor pipe about 170 cycles; stored
 // by the warps instead, with tcgen05.st, the scales came so late behind the MMAs in flight
 // that the first product of 4,096 rows took 294 us instead of 243.) Waits are bounded; one that gives up sets DSA_STATUS_TIMEOUT and every role leaves its loop.
-#include <map>
-#include <mutex>
-#include <utility>
+#include <atomic>
 
 #include <cuda_fp16.h>
 
@@ -38,6 +36,7 @@
 namespace dsa {
 namespace {
 
+constexpr int kMaxDevices = 64;
 constexpr uint32_t kABytes = 128 * 128;  // 128 weight rows x 128 bytes of K
 constexpr int kSfStages = 8;             // K stages whose scales travel together: a chunk
 constexpr uint32_t kSfBlock = 512;       // scale words of 128 rows, [32][4]: word [l][j] is row 32 j + l
@@ -838,31 +837,29 @@ int check_experts(const char* name, int rows, int topk, int n_experts, int hidde
                     n_experts, hidden, inter);
     if (hidden % 128 != 0 || inter % 128 != 0)
         return fail(DSA_ERR_UNSUPPORTED, "%s: hidden %d and inter %d must be multiples of 128", name, hidden, inter);
-    if (n_experts > DSA_MAX_EXPERTS + DSA_MAX_TOPK || (long long)n_experts * 2 * inter > 0x7fffffffLL ||
-        (long long)n_experts * hidden > 0x7fffffffLL)
-        return fail(DSA_ERR_UNSUPPORTED, "%s: too many experts (%d)", name, n_experts);
+    if (hidden > 65536 || inter > 65536)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: hidden %d and inter %d must be at most 65536", name, hidden, inter);
+    if (n_experts > DSA_MAX_EXPERTS + DSA_MAX_TOPK)
+        return fail(DSA_ERR_UNSUPPORTED, "%s: at most %d experts (got %d)", name, DSA_MAX_EXPERTS + DSA_MAX_TOPK,
+                    n_experts);
     if ((long long)rows * topk > (1 << 24))
         return fail(DSA_ERR_UNSUPPORTED, "%s: rows * topk %lld > %d", name, (long long)rows * topk, 1 << 24);
     return DSA_OK;
 }
 
-// Clusters of the launch that fit the device at once, asked once per kernel and device.
-cudaError_t max_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, int* n) {
-    static std::mutex mu;
-    static std::map<std::pair<int, const void*>, int> known;
+// Clusters of the launch that fit the device at once, asked once per kernel (its `known`) and
+// device.
+cudaError_t max_clusters(const void* kernel, const cudaLaunchConfig_t& cfg, std::atomic<int>* known, int* n) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    auto it = known.find({dev, kernel});
-    if (it == known.end()) {
-        int c = 0;
-        e = cudaOccupancyMaxActiveClusters(&c, kernel, &cfg);
-        if (e != cudaSuccess) return e;
-        if (c < 1) return cudaErrorLaunchOutOfResources;
-        it = known.emplace(std::make_pair(dev, kernel), c).first;
-    }
-    *n = it->second;
+    const bool keep = dev >= 0 && dev < kMaxDevices;
+    *n = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*n > 0) return cudaSuccess;
+    e = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (*n < 1) return cudaErrorLaunchOutOfResources;
+    if (keep) known[dev].store(*n, std::memory_order_relaxed);
     return cudaSuccess;
 }
 
@@ -909,7 +906,8 @@ int gemm_launch(const GemmArgs& a, const void* weights, const void* b, int b_row
         // One pair of blocks per pair of SMs; fewer where not all SMs come in pairs (a pair that
         // waited for others to leave would take its share of the items after theirs).
         int clusters = 0;
-        cudaError_t q = max_clusters((const void*)experts_kernel<F8, UP, N>, cfg, &clusters);
+        static std::atomic<int> known[kMaxDevices];
+        cudaError_t q = max_clusters((const void*)experts_kernel<F8, UP, N>, cfg, known, &clusters);
         if (q != cudaSuccess) return cuda_fail(q, "dsa_experts occupancy");
         if (2 * clusters < sms) cfg.gridDim.x = (unsigned)(2 * clusters);
     }

@@ -218,7 +218,8 @@ extern "C" int dsa_rmsnorm(const dsa_bf16* x, const dsa_bf16* residual, const ds
     if (codes && width % 128 != 0)
         return fail(DSA_ERR_UNSUPPORTED, "dsa_rmsnorm: FP8 rows need a width of a multiple of 128, not %d",
                     width);
-    if (rows > 0x7fffffffLL) return fail(DSA_ERR_UNSUPPORTED, "dsa_rmsnorm: too many rows");
+    if (rows > 0x7fffffffLL || width > (1 << 24))
+        return fail(DSA_ERR_UNSUPPORTED, "dsa_rmsnorm: at most 2^31 - 1 rows of 2^24 channels");
     if (rows == 0) return DSA_OK;  // (tensors without elements have no address)
     if ((codes != nullptr) != (scales != nullptr))
         return fail(DSA_ERR_INVALID_ARG, "dsa_rmsnorm: codes and scales go together");

@@ -532,7 +532,7 @@ template <int NPL>
 cudaError_t route_launch(const RouteArgs& a, cudaStream_t st) {
     // (A warp for several rows, their biases looked up once, was slower: a row in doubt holds up
     // those behind it.)
-    const dim3 grid((unsigned)((a.rows + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
+    const dim3 grid((unsigned)(((long long)a.rows + kRouteWarps - 1) / kRouteWarps)), block(kRouteWarps * 32);
     return a.softmax ? launch_pdl(route_kernel<NPL, true>, grid, block, 0, st, a)
                      : launch_pdl(route_kernel<NPL, false>, grid, block, 0, st, a);
 }

@@ -161,6 +161,36 @@ def test_uneven_padding_and_bad_ids(rows, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("last", [1, 15, 16, 17, 33])
+def test_few_pairs_behind_many(last, fp8):
+    """Large tiles, and the last expert's pairs so few that half a tile's rows lie behind the end."""
+    p = Problem(last, 330, 3, 1, 256, 128, fp8)
+    p.ids[:, 0] = torch.arange(330, device="cuda") % 2
+    p.ids[100:100 + last, 0] = 2
+    p.run()
+    p.check()
+    assert int(p.status) == 0
+
+
+def test_odd_number_of_row_tiles():
+    """A pair of blocks' second tile of the down product lies behind the last expert's rows."""
+    for fp8 in (False, True):
+        p = Problem(31, 420, 2, 1, 384, 128, fp8)
+        p.run()
+        p.check()
+
+
+def test_output_over_the_input():
+    p = Problem(12, 45, 4, 2, 256, 128, False)
+    p.run()
+    want, x = p.y.clone(), p.x.clone()
+    api.dsa_experts(x, p.ids, p.weights, p.w13, p.w2, x, workspace=p.ws)
+    assert torch.equal(x, want)
+    p.run()
+    assert torch.equal(p.y, want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_same_expert_twice_counts_twice(fp8):
     p = Problem(3, 9, 4, 2, 128, 128, fp8)
     p.ids[:, 1] = p.ids[:, 0]

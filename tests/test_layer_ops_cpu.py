@@ -30,6 +30,7 @@ def test_rmsnorm_refusals(lib):
     assert call(rows=0) == DSA_OK
     assert call(rows=-1) == DSA_ERR_INVALID_ARG
     assert call(width=0) == DSA_ERR_INVALID_ARG
+    assert call(width=(1 << 24) + 128) == DSA_ERR_UNSUPPORTED
     assert call(rows=1 << 31) == DSA_ERR_UNSUPPORTED
     assert call(eps=-1e-6) == DSA_ERR_INVALID_ARG and "eps" in _err(lib)
     assert call(eps=float("nan")) == DSA_ERR_INVALID_ARG
@@ -157,7 +158,7 @@ def test_experts_refusals(lib):
         assert call(**bad) == DSA_ERR_INVALID_ARG, bad
         assert "dsa_experts" in _err(lib), bad
     for bad in (dict(hidden=192), dict(inter=64), dict(inter=200), dict(n=1089),
-                dict(rows=1 << 20, topk=64), dict(n=1088, inter=1 << 20)):
+                dict(rows=1 << 20, topk=64), dict(inter=65664), dict(hidden=65664)):
         assert call(**bad) == DSA_ERR_UNSUPPORTED, bad
 
 

@@ -6,7 +6,7 @@
 // h is rounded to bf16, or with FP8 weights to E4M3 under one 2^k per 32 channels: it is
 // the second product's tensor-core operand. All sums are f32.
 //
-// Four launches. (1) dispatch: one block per expert finds its (row, j) pairs in order and
+// Four launches (three for few pairs, see kOwnPairs). (1) dispatch: one block per expert finds its (row, j) pairs in order and
 // how many pairs lie before them. (2) gate and up products with the activation, (3) the
 // down products, both by the same persistent tensor-core kernel, (4) the weighted sums.
 //
@@ -54,6 +54,15 @@ constexpr uint32_t kStgBytes = 4 * kChunk * kStgLd;
 // which is what bounds that one.
 constexpr bool paired(int n) { return n > 128; }
 
+// The first product gathers rows of x itself for small tiles. A gathering copy takes about 60
+// cycles for its four rows: 16 of them (64 pairs) would take longer than the weights of their
+// stage do to arrive, so larger tiles read a copy of x in the pairs' order.
+constexpr bool gathers(int n) { return n < 64; }
+
+// Up to so many pairs every block of the products orders them for itself, without the dispatch
+// before it (2 to 3 us of a call that reads eight experts' weights in 33).
+constexpr int kOwnPairs = 256;
+
 template <bool F8, bool UP, int N>
 struct EL {  // shared and tensor memory of one block
     static constexpr int BR = paired(N) ? (N / 2 + 31) / 32 * 32 : N;  // rows of x or h of a stage
@@ -72,7 +81,8 @@ struct EL {  // shared and tensor memory of one block
     static constexpr uint32_t TMEM = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
     static_assert(COLS <= 512, "tensor memory");
     // The rest is the ring's. (512: barriers; 1024: the ring's alignment.)
-    static constexpr uint32_t TAB_MAX = 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1);
+    static constexpr uint32_t OWN = gathers(N) ? 8 * kOwnPairs : 0;  // int[2][kOwnPairs]
+    static constexpr uint32_t TAB_MAX = 8 * (DSA_MAX_EXPERTS + DSA_MAX_TOPK + 1) + OWN;
     static constexpr uint32_t OTHER = STG_GROUPS * STG_BUFS * kStgBytes + 2 * SFBUF + TAB_MAX + 512 + 1024;
     static constexpr int S = (int)((227 * 1024 - OTHER) / STAGE);  // ring stages
     static constexpr uint32_t STG = S * STAGE;
@@ -80,16 +90,13 @@ struct EL {  // shared and tensor memory of one block
     static constexpr uint32_t BARS = SF + 2 * SFBUF;
     static constexpr int NBARS = 2 * S + 9;  // full, empty; 2 + 2 scales, accumulators; drain
     static constexpr uint32_t MISC = BARS + 8 * NBARS;
-    static constexpr uint32_t TAB = MISC + 16;  // int[2][n_experts + 1]
+    static constexpr uint32_t TAB = MISC + 16 + OWN;  // int[2][n_experts + 1]
     static_assert(8 * NBARS + 16 <= 512 && SF % 128 == 0 && BARS % 8 == 0 && STAGE % 1024 == 0, "layout");
 };
 
-// The first product gathers rows of x itself for small tiles. A gathering copy takes about 60
-// cycles for its four rows: 16 of them (64 pairs) would take longer than the weights of their
-// stage do to arrive, so larger tiles read a copy of x in the pairs' order.
-constexpr bool gathers(int n) { return n < 64; }
-
 struct GemmArgs {
+    const int32_t* ids;      // [pairs], where the blocks order the pairs; else NULL
+    int32_t* place_of;       // [pairs] ... and the first product's first block says in which order
     const int32_t* counts;   // [E] pairs of each expert
     const int32_t* starts;   // [E] pairs before them
     const int32_t* pair_of;  // [pairs] pair (row * topk + j) at a place of the order
@@ -280,37 +287,67 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         else
             tc_alloc(tmem_slot, L::TMEM);
     }
-    // The tables of the dispatch. The first product waits for it; the second starts early
-    // (its predecessor lets it once it has itself seen the dispatch finished) and waits
+    // The tables of the dispatch. The first product waits for it (or for the ids); the second
+    // starts early (its predecessor lets it once it has itself seen them finished) and waits
     // below, before it touches h.
     if constexpr (UP) {
         pdl_wait();
         pdl_trigger();
     }
-    for (int i = threadIdx.x; i < a.n_experts; i += blockDim.x) {
-        tab[i] = (a.counts[i] + N - 1) / N;
-        start[i] = a.starts[i];
+    const int32_t* pair_of = a.pair_of;
+    const bool own = gathers(N) && a.ids;
+    int* const own_ids = reinterpret_cast<int*>(smem + L::MISC + 16);
+    int* const own_pairs = own_ids + kOwnPairs;
+    if (own) {
+        for (int i = threadIdx.x; i < a.n_experts; i += blockDim.x) start[i] = 0;
+        __syncthreads();
+        const int q = threadIdx.x;  // (there are more threads than pairs)
+        if (q < a.pairs) {
+            int id = __ldg(a.ids + q);
+            if (id < 0 || id >= a.n_experts) {
+                if (UP && blockIdx.x == 0 && id != -1) flag_status(a.status, DSA_STATUS_BAD_EXPERT);
+                id = -1;
+            }
+            own_ids[q] = id;
+            if (id >= 0) atomicAdd(start + id, 1);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.n_experts; i += blockDim.x) tab[i] = (start[i] + N - 1) / N;
+    } else {
+        for (int i = threadIdx.x; i < a.n_experts; i += blockDim.x) {
+            const int n = a.counts[i];
+            tab[i] = (n + N - 1) / N;
+            start[i] = n;
+        }
     }
     __syncthreads();
-    if (warp == 0) {  // exclusive scan of the tile counts
+    if (warp < 2) {  // exclusive scans of the tile counts and the pair counts
+        int* const list = warp == 0 ? tab : start;
         int run = 0;
         for (int i0 = 0; i0 < a.n_experts; i0 += 32) {
             const int i = i0 + lane;
-            const int v = i < a.n_experts ? tab[i] : 0;
+            const int v = i < a.n_experts ? list[i] : 0;
             int x = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, x, o);
                 if (lane >= o) x += y;
             }
-            if (i < a.n_experts) tab[i] = run + x - v;
+            if (i < a.n_experts) list[i] = run + x - v;
             run += __shfl_sync(0xffffffffu, x, 31);
         }
-        if (lane == 0) {
-            tab[a.n_experts] = run;
-            const int last = a.n_experts - 1;
-            start[a.n_experts] = start[last] + a.counts[last];
+        if (lane == 0) list[a.n_experts] = run;
+    }
+    if (UP && own) {
+        __syncthreads();
+        const int q = threadIdx.x;
+        if (q < a.pairs && own_ids[q] >= 0) {
+            int place = start[own_ids[q]];
+            for (int j = 0; j < q; ++j) place += own_ids[j] == own_ids[q];
+            own_pairs[place] = q;
+            if (blockIdx.x == 0) a.place_of[q] = place;
         }
+        pair_of = own_pairs;
     }
     tc_fence_before();
     __syncthreads();
@@ -352,7 +389,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int p = lane * 4 + j;
-                    row[j] = a.pair_of[it.pos + (p < it.n ? p : 0)] / a.topk;
+                    row[j] = pair_of[it.pos + (p < it.n ? p : 0)] / a.topk;
                 }
             }
             const int half = (it.n + 31) / 32 * 16;  // of a pair of blocks: columns from each
@@ -601,7 +638,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const int p = it.pos + (sub + 16 * k < it.n ? sub + 16 * k : 0);
-                pb[k] = (uint32_t)(UP ? a.pair_of[p] / a.topk : p);
+                pb[k] = (uint32_t)(UP ? pair_of[p] / a.topk : p);
             }
         };
         uint32_t va[8], vb[NB];
@@ -972,11 +1009,17 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     int32_t* pair_of = reinterpret_cast<int32_t*>(ws + p.pair_of);
     int32_t* place_of = reinterpret_cast<int32_t*>(ws + p.place_of);
     const int threads = pairs >= 1024 ? 1024 : (pairs + 31) / 32 * 32;
-    cudaError_t e = launch_pdl(dispatch_kernel, dim3((unsigned)n_experts), dim3((unsigned)threads), 0, st, ids, pairs,
-                               n_experts, counts, starts, pair_of, place_of, status);
-    if (e == cudaSuccess) e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "dsa_experts dispatch launch");
+    const bool own = pairs <= kOwnPairs && gathers(tile_of(pairs, n_experts, f8));
+    cudaError_t e = cudaSuccess;
+    if (!own) {
+        e = launch_pdl(dispatch_kernel, dim3((unsigned)n_experts), dim3((unsigned)threads), 0, st, ids, pairs, n_experts,
+                       counts, starts, pair_of, place_of, status);
+        if (e == cudaSuccess) e = cudaGetLastError();
+        if (e != cudaSuccess) return cuda_fail(e, "dsa_experts dispatch launch");
+    }
     GemmArgs a = {};
+    a.ids = own ? ids : nullptr;
+    a.place_of = place_of;
     a.counts = counts;
     a.starts = starts;
     a.pair_of = pair_of;

@@ -700,14 +700,16 @@ class DsaDecodeLayer:
         with their reductions and the norm kernel, the append, the step, the experts' half."""
         n = 5 + self.launches_per_step()
         if self.ex is not None:
-            # two norms, the logits, the route; the experts' dispatch, products and sums, and
-            # for more than 14 pairs an expert the copy of x in their order
+            # two norms, the logits, the route; the experts' products and sums, for more than
+            # 256 pairs the dispatch, for more than 14 pairs an expert that and the copy of x
+            # in their order
             R, nr = self.wl.rows, int(self.w_router.shape[0])
             tc = (api.dsa_get_option(api._lib.DSA_OPT_PROJECT_KERNEL)
                   != api._lib.DSA_PROJECT_KERNEL_MMA and nr % 128 == 0
                   and self.geom.hidden % 512 == 0)
             pairs, experts = self.expert_ids.numel(), int(self.w2.shape[0])
-            n += 3 + (R + 63) // 64 + (0 if tc else 1) + 4 + (1 if pairs > 14 * experts else 0)
+            n += 3 + (R + 63) // 64 + (0 if tc else 1)
+            n += 5 if pairs > 14 * experts else 4 if pairs > 256 else 3
         return n + (0 if self.decode_from is None else self._append_launches())
 
     def launches_per_append_step(self) -> int:

@@ -113,7 +113,7 @@ def test_launches_of_the_experts_half():
     """What the experts add to launches_per_layer_step is what a profiler sees, on both sides of
     the copy of x."""
     from torch.profiler import ProfilerActivity, profile
-    for rows, n_experts in (((300, 517, 77), 12), ((40,) * 60, 4)):
+    for rows, n_experts in (((300, 517, 77), 12), ((40,) * 70, 30), ((40,) * 60, 4)):
         lay = _layer(75, rows=rows, n_experts=n_experts, n_group=1, topk_group=1)
         lay.layer_step()
         torch.cuda.synchronize()

@@ -124,6 +124,10 @@ CASES = [
     (257, 1, 1, 128, 256),
     (40, 100, 3, 1024, 128),
     (600, 40, 4, 256, 768),    # more items than SMs
+    (64, 40, 4, 128, 128),     # 256 pairs, ordered by each block
+    (257, 40, 1, 256, 128),    # 257, by the dispatch
+    (100, 64, 4, 256, 128),    # mean 7: 16 a tile behind the dispatch
+    (90, 32, 4, 128, 256),     # mean 12: 32 a tile behind the dispatch
 ]
 
 

@@ -9,6 +9,15 @@
 // output (rms_vec_kernel); rows whose width is no multiple of 8, or too wide for that, are
 // read twice (rms_any_kernel). The mean is of the unrounded sum v, so the residual's
 // rounding to bf16 does not enter the norm. An FP8 group is 16 lanes of one warp.
+//
+// The sum of squares, the root and the products carry their rounding errors along in a second
+// f32 (the standard error-free transformations by fused multiply-add), so that out is the
+// formula's value rounded to f32 and then to bf16: in plain f32 one value in some 50,000 came
+// out one bf16 step off, and its FP8 code with it one step of 2^-3. It costs 4,096 rows of 4,096
+// with residual and FP8 rows 31 us instead of 27 (their 151 MB: 23 us at the copy rate). Measured
+// there: 8 warps a row and two pieces a thread 31.8 us, 4 and four 33.0, 16 and one 35 (with the
+// plain sums); the weights requested with the row 33.5 (registers, so fewer blocks an SM), though
+// 8 rows take 3.2 us with that instead of 3.5.
 #include "fp8.cuh"
 
 namespace dsa {
@@ -24,13 +33,46 @@ struct RmsArgs {
     float* scales;
     long long rows;
     int width;
+    float inv_width;  // 1 / width
     float eps;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+// A sum of squares and its rounding errors.
+struct Squares {
+    float s, c;
+};
+__device__ __forceinline__ void add_square(Squares& a, float v) {
+    const float t = fmaf(v, v, a.s);
+    a.c += fmaf(v, v, a.s - t);
+    a.s = t;
+}
+__device__ __forceinline__ Squares add_squares(const Squares& a, const Squares& b) {
+    const float t = a.s + b.s, u = t - a.s;
+    return {t, a.c + b.c + ((a.s - (t - u)) + (b.s - u))};
+}
+__device__ __forceinline__ Squares warp_squares(Squares a) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int o = 16; o > 0; o >>= 1)
+        a = add_squares(a, {__shfl_xor_sync(0xffffffffu, a.s, o), __shfl_xor_sync(0xffffffffu, a.c, o)});
+    return a;
+}
+// 1 / sqrt(mean + eps) as hi + lo: one Newton step on the root of the leading part.
+struct Root {
+    float hi, lo;
+};
+__device__ __forceinline__ Root root_of(const Squares& a, float n, float inv_n, float eps) {
+    const float q = a.s * inv_n;  // near a.s / n; the rest of it is in `low`
+    const float m = q + eps, u = m - q;
+    const float low = fmaf(fmaf(-q, n, a.s) + a.c, inv_n, (q - (m - u)) + (eps - u));
+    const float r = rsqrtf(m), t = r * r;
+    const float e = fmaf(low, t, fmaf(m, fmaf(r, r, -t), fmaf(m, t, -1.f)));
+    return {r, m > 0.f && m < __uint_as_float(0x7f800000u) ? -0.5f * r * e : 0.f};
+}
+// v * root * w, rounded once.
+__device__ __forceinline__ float normed(float v, const Root& r, float w) {
+    const float h = v * r.hi, l = fmaf(v, r.lo, fmaf(v, r.hi, -h));
+    const float p = h * w;
+    return fabsf(p) < __uint_as_float(0x7f800000u) ? p + fmaf(l, w, fmaf(h, w, -p)) : p;
 }
 
 // WPR warps per row, 8 / WPR rows per 256-thread block (WPR <= 8), or one row per block of
@@ -38,7 +80,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 template <int WPR, int V>
 __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsArgs a) {
     constexpr int ROWS = WPR >= 8 ? 1 : 8 / WPR;
-    __shared__ float red[WPR * ROWS];
+    __shared__ Squares red[WPR * ROWS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / WPR;
     const long long r = (long long)blockIdx.x * ROWS + team;
@@ -48,7 +90,7 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
     const long long base = r * a.width;
     pdl_wait();
     float v[V][8];
-    float ss = 0.f;
+    Squares ss = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int p = t + k * WPR * 32;
@@ -82,17 +124,17 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
 #pragma unroll
     for (int k = 0; k < V; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[k][j], v[k][j], ss);
-    ss = warp_sum(ss);
+        for (int j = 0; j < 8; ++j) add_square(ss, v[k][j]);
+    ss = warp_squares(ss);
     if constexpr (WPR > 1) {
         if (lane == 0) red[warp] = ss;
         __syncthreads();
-        ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) ss += red[team * WPR + i];
+        ss = red[team * WPR];
+#pragma unroll 4
+        for (int i = 1; i < WPR; ++i) ss = add_squares(ss, red[team * WPR + i]);
     }
     if (!row_ok) return;
-    const float rs = __frsqrt_rn(ss / (float)a.width + a.eps);
+    const Root rs = root_of(ss, (float)a.width, a.inv_width, a.eps);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int p = t + k * WPR * 32;
@@ -112,7 +154,7 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
         uint32_t o[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            o[j] = pack_bf16x2(v[k][2 * j] * rs * bf16_lo(w[j]), v[k][2 * j + 1] * rs * bf16_hi(w[j]));
+            o[j] = pack_bf16x2(normed(v[k][2 * j], rs, bf16_lo(w[j])), normed(v[k][2 * j + 1], rs, bf16_hi(w[j])));
         if (a.out) *reinterpret_cast<uint4*>(a.out + base + p * 8) = make_uint4(o[0], o[1], o[2], o[3]);
         if (a.codes) {
             float f[8], m = 0.f;
@@ -141,22 +183,22 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
 // element a thread reads is the element it writes, so outputs may be the inputs.
 constexpr int kAnyThreads = 512;
 __global__ void __launch_bounds__(kAnyThreads) rms_any_kernel(RmsArgs a) {
-    __shared__ float red[kAnyThreads / 32];
+    __shared__ Squares red[kAnyThreads / 32];
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long r = blockIdx.x, base = r * a.width;
-    float ss = 0.f;
+    Squares ss = {0.f, 0.f};
     for (int c = threadIdx.x; c < a.width; c += kAnyThreads) {
         float v = bf16_lo(a.x[base + c]);
         if (a.residual) v += bf16_lo(a.residual[base + c]);
-        ss = fmaf(v, v, ss);
+        add_square(ss, v);
     }
-    ss = warp_sum(ss);
+    ss = warp_squares(ss);
     if (lane == 0) red[warp] = ss;
     __syncthreads();
-    ss = 0.f;
-    for (int i = 0; i < kAnyThreads / 32; ++i) ss += red[i];
-    const float rs = __frsqrt_rn(ss / (float)a.width + a.eps);
+    ss = red[0];
+    for (int i = 1; i < kAnyThreads / 32; ++i) ss = add_squares(ss, red[i]);
+    const Root rs = root_of(ss, (float)a.width, a.inv_width, a.eps);
     // a group of 128 channels is a warp's turn of four channels a lane
     for (int c0 = warp * 128; c0 < a.width; c0 += kAnyThreads * 4) {
         float f[4], m = 0.f;
@@ -167,7 +209,7 @@ __global__ void __launch_bounds__(kAnyThreads) rms_any_kernel(RmsArgs a) {
             if (c < a.width) {
                 float v = bf16_lo(a.x[base + c]);
                 if (a.residual) v += bf16_lo(a.residual[base + c]);
-                f[j] = round_bf16(v * rs * bf16_lo(a.weight[c]));
+                f[j] = round_bf16(normed(v, rs, bf16_lo(a.weight[c])));
                 if (a.residual_out)
                     a.residual_out[base + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
                 if (a.out) a.out[base + c] = __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));
@@ -251,6 +293,7 @@ extern "C" int dsa_rmsnorm(const dsa_bf16* x, const dsa_bf16* residual, const ds
     a.scales = scales;
     a.rows = rows;
     a.width = width;
+    a.inv_width = 1.f / (float)width;
     a.eps = eps;
     const bool aligned = ((((uintptr_t)x) | ((uintptr_t)residual) | ((uintptr_t)weight) |
                            ((uintptr_t)residual_out) | ((uintptr_t)out)) & 15) == 0 &&

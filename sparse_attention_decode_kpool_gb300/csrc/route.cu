@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
             z[i] = odd ? NI : z[i];
             if (SOFTMAX) top = fmaxf(top, z[i]);
         }
-        // Scores by the special-function unit, for the choice: within 2^-21 of the largest of them,
-        // the softmax's common factor within 2^-18 of itself.
+        // Scores by the special-function unit, for the choice: a softmax's within 2^-21 of the largest of
+        // them, its common factor within 2^-18 of itself; a sigmoid's see below.
         constexpr float kLog2e = 1.4426950408889634f;
         if (SOFTMAX) {
             top = warp_max_t(top);
@@ -467,8 +467,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32) route_kernel(RouteArgs a) {
         }
         const bool nan = __any_sync(kAll, bad);
         // |c as computed - c|: the score's error (but for the softmax's common factor, which moves
-        // no score past another) and the addition's
-        const float err = (SOFTMAX && a.bias ? 3.8146973e-6f : 4.7683716e-7f) * smax + 1.2e-7f * bmax + 1e-37f;
+        // no score past another), the addition's and half of a group sum's. A sigmoid's: 2^-22 by
+        // the power of two, 2^-23 by the reciprocal, 2^-24 by the sum under it, and |z| (2^-24 + 2^-26)
+        // by the rounding of z log2(e) and of that constant, less the more s exceeds 1/2. s |z| is
+        // largest at the largest logit, whose -z is at most -ln(smax), or near 1. (1e-37: what the
+        // unit takes for zero.)
+        const float far = SOFTMAX ? 1.f : fmaxf(1.f, fminf(-__logf(smax), 128.f));
+        const float err = (SOFTMAX ? (a.bias ? 3.8146973e-6f : 4.7683716e-7f) : 5.4e-7f + 7.6e-8f * far) * smax +
+                          1.2e-7f * bmax + 1e-37f;
         bool sure = true;
         if (a.groups > 1) {
             float* buf = reinterpret_cast<float*>(stage[warp]);

@@ -278,7 +278,8 @@ __device__ __noinline__ uint32_t choose_groups_f64(const RouteArgs& a, long long
 // The chosen experts (count >= 0 of them, by their keys; else by the bits of `taken`),
 // their scores and the row's outputs in ascending expert id; then padding and shared experts.
 // Lane k takes the k-th chosen one; T: what the scores are computed in. In f32
-// it gives up (false) where a ratio of scores needs digits that numbers near its smallest lack.
+// it gives up (false) where a ratio of scores, or a score to be scaled up, needs digits that numbers
+// near f32's smallest lack, and where the scale over the sum of the scores passes its largest.
 template <typename T, int NPL>
 __device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, uint32_t taken, int count,
                                      const uint32_t (&mine)[kSets], T top, T inv, bool nan, int* chosen) {
@@ -323,11 +324,12 @@ __device__ __forceinline__ bool emit(const RouteArgs& a, long long r, int lane, 
         }
         total += s[q];
     }
-    if (sizeof(T) == 4 && a.renorm && __any_sync(kAll, tiny)) return false;
+    if (sizeof(T) == 4 && (a.renorm || fabsf(a.scale) > 1.f) && __any_sync(kAll, tiny)) return false;
     T f = (T)a.scale;
     if (a.renorm) {
         total = warp_sum_t(total);
         f = total > 0 ? f / total : (T)0;
+        if (sizeof(T) == 4 && !(fabs(f) < (T)3.4e38)) return false;
     }
 #pragma unroll
     for (int q = 0; q < kSets; ++q) {

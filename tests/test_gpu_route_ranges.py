@@ -24,3 +24,21 @@ def test_groups_nearly_alike_far_below_zero(mean):
     _check_route(z[:500].cuda(), 3, None, "sigmoid", 4, 2, 1, True, 0)
     z = mean + 0.01 * torch.randn(500, 256, generator=g)
     _check_route(z.cuda(), 8, None, "sigmoid", 8, 4, 2, True, 0)
+
+
+@pytest.mark.parametrize("score,mean,scale,renorm", [
+    ("sigmoid", -65.0, 1e12, True),    # 1e12 over a sum of 1e-28 passes f32's largest, the weights do not
+    ("sigmoid", -65.0, -1e12, True),
+    ("sigmoid", -95.0, 1e30, False),   # scores below f32's smallest, scaled into its range
+    ("sigmoid", -89.0, 2.5, False),
+    ("softmax", -60.0, 1e30, False),
+    ("sigmoid", 0.0, 3e38, True),
+    ("sigmoid", -20.0, 1e-30, True),
+])
+def test_weights_under_large_scales(score, mean, scale, renorm):
+    g = torch.Generator().manual_seed(17)
+    z = mean + torch.randn(50, 64, generator=g)
+    if score == "softmax":
+        z[:, 9] = 40.0  # the others' shares are near 1e-44
+    _check_route(z.cuda(), 8, None, score, 1, 1, 1, renorm, 0, scale=scale)
+    _check_route(z.cuda(), 8, None, score, 4, 2, 2, renorm, 1, scale=scale)

@@ -75,6 +75,19 @@ __device__ __forceinline__ float normed(float v, const Root& r, float w) {
     return fabsf(p) < __uint_as_float(0x7f800000u) ? p + fmaf(l, w, fmaf(h, w, -p)) : p;
 }
 
+__device__ __forceinline__ void team_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Below this mean of squares (eps included) f32 runs out of digits and then of range for the squares
+// and the root: such a row, every value below 2^-36 (width <= 2^24), is multiplied by 2^96 and its eps by
+// 2^192, which leaves the result as it is. (The root of a mean above 2^-96 squared is below 2^96.)
+constexpr float kSmallMean = 1.262177448e-29f;  // 2^-96
+constexpr float kRaise = 7.922816251e28f;       // 2^96
+__device__ __forceinline__ bool small_row(const Squares& a, float inv_n, float eps) {
+    return fmaf(a.s, inv_n, eps) < kSmallMean;
+}
+
 // WPR warps per row, 8 / WPR rows per 256-thread block (WPR <= 8), or one row per block of
 // WPR warps; V pieces of eight channels per thread.
 template <int WPR, int V>
@@ -134,14 +147,11 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
         for (int i = 1; i < WPR; ++i) ss = add_squares(ss, red[team * WPR + i]);
     }
     if (!row_ok) return;
-    const Root rs = root_of(ss, (float)a.width, a.inv_width, a.eps);
+    if (a.residual_out) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const int p = t + k * WPR * 32;
-        // With codes the width is a multiple of 128, so the 16 lanes of a group are all
-        // inside the row or all outside.
-        if (p >= nvec) continue;
-        if (a.residual_out) {
+        for (int k = 0; k < V; ++k) {
+            const int p = t + k * WPR * 32;
+            if (p >= nvec) continue;
             uint4 q;
             q.x = pack_bf16x2(v[k][0], v[k][1]);
             q.y = pack_bf16x2(v[k][2], v[k][3]);
@@ -149,6 +159,35 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
             q.w = pack_bf16x2(v[k][6], v[k][7]);
             *reinterpret_cast<uint4*>(a.residual_out + base + p * 8) = q;
         }
+    }
+    float eps = a.eps;
+    if (small_row(ss, a.inv_width, eps)) {  // (the whole row's warps alike)
+        ss = {0.f, 0.f};
+        eps = eps * kRaise * kRaise;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[k][j] *= kRaise;
+                add_square(ss, v[k][j]);
+            }
+        }
+        ss = warp_squares(ss);
+        if constexpr (WPR > 1) {
+            team_sync(1 + team, WPR * 32);  // the first sums are read
+            if (lane == 0) red[warp] = ss;
+            team_sync(1 + team, WPR * 32);
+            ss = red[team * WPR];
+            for (int i = 1; i < WPR; ++i) ss = add_squares(ss, red[team * WPR + i]);
+        }
+    }
+    const Root rs = root_of(ss, (float)a.width, a.inv_width, eps);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        const int p = t + k * WPR * 32;
+        // With codes the width is a multiple of 128, so the 16 lanes of a group are all
+        // inside the row or all outside.
+        if (p >= nvec) continue;
         const uint4 wq = ldg16(a.weight + p * 8);
         const uint32_t w[4] = {wq.x, wq.y, wq.z, wq.w};
         uint32_t o[4];
@@ -179,7 +218,7 @@ __global__ void __launch_bounds__(WPR >= 8 ? WPR * 32 : 256) rms_vec_kernel(RmsA
     }
 }
 
-// Any width: one block per row, the row read twice (the second time from L1 or L2). The
+// Any width: one block per row, the row read twice (the second time from L1 or L2; a small row thrice). The
 // element a thread reads is the element it writes, so outputs may be the inputs.
 constexpr int kAnyThreads = 512;
 __global__ void __launch_bounds__(kAnyThreads) rms_any_kernel(RmsArgs a) {
@@ -187,18 +226,26 @@ __global__ void __launch_bounds__(kAnyThreads) rms_any_kernel(RmsArgs a) {
     pdl_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long r = blockIdx.x, base = r * a.width;
-    Squares ss = {0.f, 0.f};
-    for (int c = threadIdx.x; c < a.width; c += kAnyThreads) {
-        float v = bf16_lo(a.x[base + c]);
-        if (a.residual) v += bf16_lo(a.residual[base + c]);
-        add_square(ss, v);
+    float up = 1.f, eps = a.eps;
+    Squares ss;
+    for (int turn = 0; turn < 2; ++turn) {
+        ss = {0.f, 0.f};
+        for (int c = threadIdx.x; c < a.width; c += kAnyThreads) {
+            float v = bf16_lo(a.x[base + c]);
+            if (a.residual) v += bf16_lo(a.residual[base + c]);
+            add_square(ss, v * up);
+        }
+        ss = warp_squares(ss);
+        if (turn) __syncthreads();  // the first sums are read
+        if (lane == 0) red[warp] = ss;
+        __syncthreads();
+        ss = red[0];
+        for (int i = 1; i < kAnyThreads / 32; ++i) ss = add_squares(ss, red[i]);
+        if (turn || !small_row(ss, a.inv_width, eps)) break;
+        up = kRaise;
+        eps = eps * kRaise * kRaise;
     }
-    ss = warp_squares(ss);
-    if (lane == 0) red[warp] = ss;
-    __syncthreads();
-    ss = red[0];
-    for (int i = 1; i < kAnyThreads / 32; ++i) ss = add_squares(ss, red[i]);
-    const Root rs = root_of(ss, (float)a.width, a.inv_width, a.eps);
+    const Root rs = root_of(ss, (float)a.width, a.inv_width, eps);
     // a group of 128 channels is a warp's turn of four channels a lane
     for (int c0 = warp * 128; c0 < a.width; c0 += kAnyThreads * 4) {
         float f[4], m = 0.f;
@@ -209,7 +256,7 @@ __global__ void __launch_bounds__(kAnyThreads) rms_any_kernel(RmsArgs a) {
             if (c < a.width) {
                 float v = bf16_lo(a.x[base + c]);
                 if (a.residual) v += bf16_lo(a.residual[base + c]);
-                f[j] = round_bf16(normed(v, rs, bf16_lo(a.weight[c])));
+                f[j] = round_bf16(normed(v * up, rs, bf16_lo(a.weight[c])));
                 if (a.residual_out)
                     a.residual_out[base + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
                 if (a.out) a.out[base + c] = __bfloat16_as_ushort(__float2bfloat16_rn(f[j]));

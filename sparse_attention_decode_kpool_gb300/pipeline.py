@@ -323,6 +323,9 @@ class DsaDecodeLayer:
             raise ValueError("the experts take the projected output (with_o_absorb=True)")
         if tuple(ex.stream.shape) != (R, g.hidden):
             raise ValueError(f"the experts' stream must be [{R}, {g.hidden}]")
+        if int(ex.w2.shape[0]) < ex.n_experts + ex.shared:
+            raise ValueError(f"w13 and w2 must hold the router's {ex.n_experts} experts and "
+                             f"{ex.shared} shared ones (got {int(ex.w2.shape[0])})")
         up = lambda t: None if t is None else t.to(dev).contiguous()
         n, H, I = int(ex.w2.shape[0]), g.hidden, ex.inter
         self.ex, self.experts_fp8 = ex, fp8
@@ -353,6 +356,8 @@ class DsaDecodeLayer:
         ne = api.dsa_experts_workspace(R, k, n, H, I, fp8)
         self.logits_workspace = torch.zeros(max(nl, 1), dtype=torch.uint8, device=dev)
         self.experts_workspace = torch.zeros(max(ne, 1), dtype=torch.uint8, device=dev)
+        # a call without rows: the router's options are refused here, not at the first step
+        self._route(self.logits[:0], self.expert_ids[:0], self.expert_weights[:0])
 
     def attn_input(self, stream=None) -> None:
         """resid += mlp_out (what the layer before added); x = its norm, the front-end's input."""
@@ -367,6 +372,11 @@ class DsaDecodeLayer:
             raise ValueError("the layer was not built with experts")
         self._mlp_from(self.resid, stream)
 
+    def _route(self, logits, ids, weights, stream=None) -> None:
+        ex = self.ex
+        api.dsa_route(logits, ex.topk, ids, weights, ex.n_experts, ex.score, self.route_bias,
+                      ex.n_group, ex.topk_group, ex.group_top, ex.renorm, ex.scale, ex.shared, stream)
+
     def _mlp_from(self, residual_out, stream=None) -> None:
         ex = self.ex
         api.dsa_rmsnorm(self.y, self.mlp_norm, ex.eps, self.mlp_x, residual=self.resid,
@@ -374,9 +384,7 @@ class DsaDecodeLayer:
                         stream=stream)
         api.dsa_router_logits(self.mlp_x, self.w_router, self.logits, self.status,
                               self.logits_workspace, stream=stream)
-        api.dsa_route(self.logits, ex.topk, self.expert_ids, self.expert_weights, ex.n_experts,
-                      ex.score, self.route_bias, ex.n_group, ex.topk_group, scale=ex.scale,
-                      shared=ex.shared, stream=stream)
+        self._route(self.logits, self.expert_ids, self.expert_weights, stream)
         api.dsa_experts(self.mlp_codes if self.experts_fp8 else self.mlp_x, self.expert_ids,
                         self.expert_weights, self.w13, self.w2, self.mlp_out, self.mlp_scales,
                         self.w13_scales, self.w2_scales, self.status, self.experts_workspace,

@@ -444,6 +444,8 @@ class Experts:
     shared: int
     eps: float
     score: str = "sigmoid"
+    group_top: int = 2       # a group goes by the sum of its best two experts, or by its best one
+    renorm: bool = True      # weights over the sum of the chosen experts' scores
 
     @property
     def n_experts(self) -> int:
@@ -462,7 +464,8 @@ class Experts:
 
 def make_experts(g: "Geometry", rows: int, n_experts: int, topk: int, inter: int, seed: int = 0,
                  n_group: int = 1, topk_group: int = 1, shared: int = 1, scale: float = 2.5,
-                 eps: float = 1e-6) -> Experts:
+                 eps: float = 1e-6, score: str = "sigmoid", group_top: int = 2,
+                 renorm: bool = True) -> Experts:
     hidden, n = g.hidden, n_experts + shared
     mat = lambda t, *s, std: _normal_bf16(seed, t, 0, math.prod(s), 0.0, std).view(*s)
     return Experts(
@@ -473,7 +476,8 @@ def make_experts(g: "Geometry", rows: int, n_experts: int, topk: int, inter: int
         bias=torch.from_numpy(_normal_f32(_rng(seed, _T_EB), (n_experts,), 0.0, 0.05)),
         w13=mat(_T_EW13, n, 2 * inter, hidden, std=hidden ** -0.5),
         w2=mat(_T_EW2, n, hidden, inter, std=inter ** -0.5),
-        topk=topk, n_group=n_group, topk_group=topk_group, scale=scale, shared=shared, eps=eps)
+        topk=topk, n_group=n_group, topk_group=topk_group, scale=scale, shared=shared, eps=eps,
+        score=score, group_top=group_top, renorm=renorm)
 
 
 # ---------------------------------------------------------------------------

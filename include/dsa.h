@@ -59,6 +59,7 @@ extern "C" {
 #define DSA_STATUS_NO_PAGES 32  /* dsa_pages_reserve: too few free pages for a sequence;
                                    dsa_decode_append_guarded: its next page is still shared   */
 #define DSA_STATUS_BAD_EXPERT 64 /* dsa_experts: an expert id outside [-1, n_experts) (skipped) */
+#define DSA_STATUS_BAD_SCALE 128 /* dsa_experts: an FP8 scale that is no power of two (cut down) */
 
 #define DSA_KV_LORA_RANK 512 /* latent width the attention kernels are built for */
 #define DSA_MAX_KPOOL 16     /* most slots per pool dsa_compress handles         */
@@ -880,11 +881,12 @@ int dsa_route(const float* logits, int rows, int n_experts, long long ld, int sc
  * w2 [n_experts, hidden, inter]: all bf16 with the three scales NULL, or all FP8 codes (u8)
  * with x_scales [rows, hidden / 128], w13_scales [n_experts, 2 inter, hidden / 128],
  * w2_scales [n_experts, hidden, inter / 128] f32, as dsa_quantize_latent or dsa_rmsnorm make
- * them: the scales are powers of two, and only their exponents are read. ids, weights [rows,
- * topk]; y [rows, hidden] bf16 (may be x). Limits: hidden and inter multiples of 128, at most
- * 65536; n_experts <=
- * DSA_MAX_EXPERTS + DSA_MAX_TOPK; rows * topk <= 2^24; 16-byte aligned tensors (4 for scales, ids and
- * weights) and workspace. The workspace's contents need not be kept between calls; calls
+ * them: the scales are powers of two, and only their exponents are read (0 counts as 2^-127). A
+ * scale with other digits or a sign among those that the chosen experts read sets
+ * DSA_STATUS_BAD_SCALE; NaN and Inf are NaN. ids, weights [rows, topk]; y [rows, hidden] bf16
+ * (may be x). Limits: hidden and inter multiples of 128, at most 65536; n_experts <=
+ * DSA_MAX_EXPERTS + DSA_MAX_TOPK; rows * topk <= 2^24; 16-byte aligned tensors (4 for scales,
+ * ids and weights) and workspace. The workspace's contents need not be kept between calls; calls
  * that overlap in time need one each. `status` also gets DSA_STATUS_TIMEOUT if a wait inside
  * a kernel gives up (about 1 s); y is then incomplete.
  */

@@ -24,6 +24,7 @@ DSA_STATUS_CACHE_FULL = 8
 DSA_STATUS_BAD_SEQ = 16
 DSA_STATUS_NO_PAGES = 32
 DSA_STATUS_BAD_EXPERT = 64
+DSA_STATUS_BAD_SCALE = 128
 DSA_MAX_PAGE_ARRAYS = 128
 DSA_MAX_EXPERTS = 1024
 DSA_MAX_TOPK = 64

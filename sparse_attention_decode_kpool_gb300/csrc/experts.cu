@@ -623,6 +623,8 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             }
         };
         uint32_t va[8], vb[NB];
+        uint32_t odd = 0;  // what the scales seen have beyond an exponent
+        auto digits = [](uint32_t v) { return (v & 0x7fffffffu) > 0x7f800000u ? 0u : v & 0x807fffffu; };
         auto load = [&](int st0) {
             const bool in = st0 + sst < a.nst;
 #pragma unroll
@@ -660,6 +662,11 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             fence_async_smem();
             __syncwarp();
             if (lane == 0) arrive_leader(sf_full + (chunk & 1));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) odd |= digits(va[k]);
+            if constexpr (UP)
+#pragma unroll
+                for (int k = 0; k < NB; ++k) odd |= digits(vb[k]);
             st0 += kSfStages;
             if (st0 >= a.nst) {
                 st0 = 0;
@@ -668,6 +675,7 @@ __global__ void __launch_bounds__(F8 ? 512 : 384, 1)
             }
             if (w < items) load(st0);
         }
+        if (odd) flag_status(a.status, DSA_STATUS_BAD_SCALE);
     }
     __syncthreads();
     if constexpr (kPair) cluster_barrier();  // neither leaves while the other may reach it

@@ -32,7 +32,10 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quantize_latent_kernel(
 
 // 16 codes per piece (they lie in one group), PER pieces a thread, a block's pieces
 // consecutive so that loads and stores are whole lines. All loads are requested before the
-// first is used. Bound by memory: 4,096 rows of 4,096 channels (50 MB) in 10 us.
+// first is used. Bound by memory: 4,096 rows of 4,096 channels (50 MB) in 10 us. PER is 1, or 4 for
+// named rows from 16 x 2,048 pieces an SM on, where the lookups of several rows go at once. Measured
+// with a cold L2, rows of 4,096 channels, 1 | 4 a thread: in order 16,384 rows 37 | 41 us, 32,768
+// 70 | 72, 131,072 254 | 254; named 16,384 rows 41 | 41, 65,536 143 | 133, 131,072 279 | 258.
 constexpr int kDequantThreads = 256;
 template <int PER>
 __global__ void __launch_bounds__(kDequantThreads) dequantize_latent_kernel(
@@ -122,7 +125,7 @@ extern "C" int dsa_dequantize_latent(const uint8_t* codes, const float* scales,
         return fail(DSA_ERR_UNSUPPORTED, "dsa_dequantize_latent: too many rows");
     const long long pieces = rows * per_row;
     const int sms = sm_count();
-    const bool many = pieces >= 16LL * 2048 * (sms > 0 ? sms : 152);
+    const bool many = row_ids && pieces >= 16LL * 2048 * (sms > 0 ? sms : 152);
     const long long per = kDequantThreads * (many ? 4 : 1);
     cudaError_t e = launch_pdl(many ? dequantize_latent_kernel<4> : dequantize_latent_kernel<1>,
                                dim3((unsigned)((pieces + per - 1) / per)), dim3(kDequantThreads), 0,

@@ -561,7 +561,7 @@ def dsa_dequantize_latent_fp4(codes, scales, out, cache_exp: int = 0, rows=None,
 def _fp8_rows(codes, scales) -> int:
     """Width of FP8 rows: codes [.., w] with scales [.., w/128] over the same rows."""
     w = codes.size(-1)
-    if w % 128 or scales.size(-1) * 128 != w or scales.numel() * 128 != codes.numel():
+    if w < 1 or w % 128 or scales.size(-1) * 128 != w or scales.numel() * 128 != codes.numel():
         raise ValueError("codes must be [.., w] and scales [.., w/128] of the same rows, w a "
                          "multiple of 128")
     return w

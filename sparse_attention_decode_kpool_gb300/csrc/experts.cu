@@ -12,8 +12,8 @@
 // both by the same persistent tensor-core kernel, (5) the weighted sums.
 //
 // Experts of 4,096 x 1,024, eight a row: 8 rows of 128 experts, bf16, read 1.3 GB of weights in
-// 198 us (HBM bounds it); 4,096 rows of 64 take 667 us in bf16 (350 and 242 for the products: 0.83
-// and 0.60 of the measured bf16 rate, waiting for L2) and 511 us in FP8 (236 and 210: the scale
+// 200 us (HBM bounds it); 4,096 rows of 64 take 729 us in bf16 (353 and 256 for the products: 0.82
+// and 0.57 of the measured bf16 rate, waiting for L2) and 537 us in FP8 (243 and 195: the scale
 // copies between the MMAs).
 //
 // Each product has the weights as the MMA's M operand and the pairs as N: D^T [128 weight
@@ -147,8 +147,11 @@ __device__ __forceinline__ Item item_of(const GemmArgs& a, const int* tab, const
     return it;
 }
 
-// g / (1 + exp(-g)) with the division and the exponential of the special-function unit, off by a
-// few 2^-22 of the result: h is rounded to 2^-9 at best.
+// g / (1 + exp(-g)) with the division and the exponential of the special-function unit: off by about
+// 2 + |g| units of 2^-23 of the result (the exponential's argument is rounded), and 0 below g of -87,
+// where the formula gives less than 2^-118. Where |g| is large the result is g itself (the exponential
+// adds nothing to 1) or below |g| e^g, so 2^-17 of it at g = -50 is still far below what h is rounded to:
+// 2^-9 of itself, or 2^-4 with FP8.
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.f + __expf(-g)); }
 
 __device__ __forceinline__ void tc_ld16(uint32_t (&v)[16], uint32_t taddr) {
@@ -815,10 +818,10 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Pairs per tile, by what an expert gets on average (its tiles are cut to its own count, so a
 // larger one costs shared memory for weights in flight rather than work). Measured with 64
-// experts of 4,096 x 1,024, bf16, some more popular than others: 12 pairs each 271 us at 16 a
-// tile, 257 at 32, 253 at 64; 20: 287 at 32, 258 at 64; 40: 278 at 64, 276 at 128, 281 at 256;
-// 56: 293, 283, 287; 104: 326 at 128, 311 at 256. FP8: 56: 183 at 64, 169 at 128, 179 at 224;
-// 104: 202 and 203; 130: 229 and 221.
+// experts of 4,096 x 1,024, bf16, some more popular than others: 12 pairs each 272 us at 16 a
+// tile, 258 at 32, 254 at 64; 20: 291 at 32, 261 at 64; 40: 281 at 64, 279 at 128, 282 at 256;
+// 56: 298, 288, 292; 104: 334 at 128, 319 at 256. FP8: 12: 162 at 16, 149 at 32, 150 at 64; 56: 189
+// at 64, 176 at 128, 186 at 224; 104: 210 and 210; 130: 237 and 227.
 int tile_of(long long pairs, int n_experts, bool f8) {
     const long long mean = (pairs + n_experts - 1) / n_experts;
     return mean <= 8 ? 16 : mean <= 14 ? 32 : mean <= 48 ? 64 : mean <= 96 ? 128 : f8 ? 224 : 256;
